@@ -7,7 +7,9 @@ ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", "qrow.hip"),
            os.path.join(HERE, "csrc", "imatrix.hip"),
            os.path.join(HERE, "csrc", "matmul.hip"),
-           os.path.join(HERE, "csrc", "stats.hip")]
+           os.path.join(HERE, "csrc", "stats.hip"),
+           os.path.join(HERE, "csrc", "serve_i8.hip"),
+           os.path.join(HERE, "csrc", "serve_kv8.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libqrow.so")
 # measurement only: VALU issue rates of the instruction classes the kernels

@@ -1,0 +1,763 @@
+// serve_kv8.hip -- gfx950 kernels and C-ABI of the paged 8-bit key/value cache
+// and of attention over it (declared in serve/qrow_kv8.h).
+
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "qr_internal.h"
+#include "qrow.h"
+#include "serve/qrow_kv8.h"
+
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int WAVE = 64;
+constexpr int GROUP = 32;        // tokens of a V group: every block holds whole groups
+constexpr int MAX_HEADS = 1024;
+
+__device__ __forceinline__ float bf16_value(uint16_t h) { return __builtin_bit_cast(float, (uint32_t)h << 16); }
+
+// fp32 to bf16, round to nearest even (NaN stays NaN).
+__device__ __forceinline__ uint16_t bf16_bits(float f) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, f);
+  if ((u & 0x7fffffffu) > 0x7f800000u) return (uint16_t)((u >> 16) | 0x40u);
+  return (uint16_t)((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
+}
+
+template <int SRC>
+__device__ __forceinline__ float value_at(const void* x, int64_t i) {
+  return SRC == QR_BF16 ? bf16_value(reinterpret_cast<const uint16_t*>(x)[i]) : reinterpret_cast<const float*>(x)[i];
+}
+
+template <int DST>
+__device__ __forceinline__ void store_at(void* x, int64_t i, float v) {
+  if (DST == QR_BF16) reinterpret_cast<uint16_t*>(x)[i] = bf16_bits(v);
+  else reinterpret_cast<float*>(x)[i] = v;
+}
+
+// The sequences of a call and the cache they live in.
+struct Batch {
+  const int32_t* cu;
+  const int32_t* kv_len;
+  const int32_t* table;
+  int64_t table_width;
+  int n_seq, n_tok;
+};
+
+struct Cache {
+  int8_t* k;
+  int8_t* v;
+  float* kd;
+  float* vd;
+  int n_blocks, n_heads, block;   // block: tokens per block
+};
+
+// A sequence's rows and tokens. Rows [row0, row0 + n) of the call are the
+// positions len - n ...
+struct Span {
+  int seq, row0, n, len;
+};
+
+__device__ __forceinline__ int clamp_row(const Batch& b, int r) { return r < 0 ? 0 : r > b.n_tok ? b.n_tok : r; }
+
+// Which sequence a unit of work belongs to, without a table of units on the
+// host: sequence s gets the units from floor(cu[s] * mul / div) + s * pad on,
+// which leaves every sequence room for ceil(rows * mul / div) + pad - 1 units
+// or more. A whole wave asks together: its lanes look at 64 sequences at once.
+// Returns the unit's number within its sequence.
+__device__ __forceinline__ int find_unit(const Batch& b, int64_t unit, int64_t mul, int64_t div, int pad, Span& sp) {
+  const int lane = threadIdx.x & (WAVE - 1);
+  int seq = -1;
+  for (int base = 0; base < b.n_seq; base += WAVE) {
+    bool begun = false;
+    if (base + lane < b.n_seq)
+      begun = (int64_t)clamp_row(b, b.cu[base + lane]) * mul / div + (int64_t)(base + lane) * pad <= unit;
+    const uint64_t m = __ballot(begun);
+    if (m != 0) seq = base + 63 - __builtin_clzll(m);
+    if (m != ~0ull) break;
+  }
+  seq = __builtin_amdgcn_readfirstlane(seq);
+  sp.seq = seq < 0 ? 0 : seq;
+  sp.row0 = clamp_row(b, b.cu[sp.seq]);
+  sp.n = clamp_row(b, b.cu[sp.seq + 1]) - sp.row0;
+  sp.len = b.kv_len[sp.seq];
+  if (seq < 0 || sp.n < 0) sp.n = 0;
+  return (int)(unit - ((int64_t)sp.row0 * mul / div + (int64_t)sp.seq * pad));
+}
+
+// The block that holds a sequence's tokens slot * block .., or -1.
+__device__ __forceinline__ int block_of(const Batch& b, const Cache& c, int seq, int64_t slot) {
+  if (slot < 0 || slot >= b.table_width) return -1;
+  const int id = b.table[(int64_t)seq * b.table_width + slot];
+  return id >= 0 && id < c.n_blocks ? id : -1;
+}
+
+// Byte of channel d of token t in its V block.
+template <int D>
+__device__ __forceinline__ int v_byte(int t, int d) {
+  return (t / GROUP) * (GROUP * D) + (d >> 1) * 64 + ((t % GROUP) >> 3) * 16 + (d & 1) * 8 + (t & 7);
+}
+
+// ---------------------------------------------------------------------------
+// writing and reading
+
+constexpr int RW_THREADS = 256;
+
+// The part of a sequence's rows that lies in one block: tokens [t0, t1) of
+// the block are rows row .. row + (t1 - t0) - 1.
+struct Piece {
+  int id, t0, t1, row;
+};
+
+__device__ __forceinline__ Piece find_piece(const Batch& b, const Cache& c, int64_t unit) {
+  Span sp;
+  const int u = find_unit(b, unit, 1, c.block, 2, sp);
+  Piece p = {-1, 0, 0, 0};
+  const int64_t first = (int64_t)sp.len - sp.n;         // position of the first row, may be negative
+  const int64_t from = first < 0 ? 0 : first;
+  const int64_t slot = from / c.block + u;
+  const int64_t lo = slot * c.block;
+  if (u < 0 || sp.n == 0 || lo >= sp.len) return p;
+  p.id = block_of(b, c, sp.seq, slot);
+  p.t0 = (int)(from > lo ? from - lo : 0);
+  p.t1 = (int)(sp.len - lo < c.block ? sp.len - lo : c.block);
+  p.row = (int)(sp.row0 + (lo + p.t0 - first));
+  return p;
+}
+
+// One workgroup per (block, head, keys or values). The new values are read
+// twice, the second time from the cache of the CU or the XCD: bound by memory.
+template <int SRC, int D>
+__global__ __launch_bounds__(RW_THREADS) void k_kv8_append(Cache c, Batch b, const void* __restrict__ k,
+                                                           const void* __restrict__ v, int64_t k_stride,
+                                                           int64_t v_stride) {
+  __shared__ uint32_t wave_max[RW_THREADS / WAVE];
+  const Piece p = find_piece(b, c, blockIdx.x);
+  if (p.id < 0 || p.t1 <= p.t0) return;
+  const int tid = threadIdx.x, head = blockIdx.y;
+  const bool values = blockIdx.z != 0;
+  const void* x = values ? v : k;
+  const int64_t stride = values ? v_stride : k_stride;
+  const int64_t x0 = (int64_t)p.row * stride + (int64_t)head * D;
+  const int nt = p.t1 - p.t0;
+  uint32_t top = 0;
+  for (int e = tid; e < nt * D; e += RW_THREADS) {
+    const uint32_t m =
+        __builtin_bit_cast(uint32_t, value_at<SRC>(x, x0 + (int64_t)(e / D) * stride + e % D)) & 0x7fffffffu;
+    top = m > top ? m : top;
+  }
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) {
+    const uint32_t o = (uint32_t)__shfl_xor((int)top, s);
+    top = o > top ? o : top;
+  }
+  if ((tid & (WAVE - 1)) == 0) wave_max[tid / WAVE] = top;
+  const int64_t at = (int64_t)p.id * c.n_heads + head;
+  float* scale = (values ? c.vd : c.kd) + at;
+  const float old = p.t0 > 0 ? *scale : 0.0f;
+  __syncthreads();   // every thread has read the old scale
+#pragma unroll
+  for (int w = 0; w < RW_THREADS / WAVE; ++w) top = wave_max[w] > top ? wave_max[w] : top;
+  float cand = __builtin_bit_cast(float, top) / 127.0f;
+  if (!(1.0f / cand < __builtin_inff())) cand = 0.0f;
+  const bool bad = top >= 0x7f800000u || old != old;
+  const float d = bad ? __builtin_nanf("") : old > cand ? old : cand;
+  float inv = 1.0f / d;
+  if (bad || !(inv < __builtin_inff())) inv = 0.0f;
+  const bool grown = p.t0 > 0 && !bad && d > old;
+  const float ratio = grown ? old / d : 1.0f;
+  if (tid == 0) *scale = d;
+
+  int8_t* codes = (values ? c.v : c.k) + at * c.block * D;
+  // eight codes at a time: of one token for keys, of one channel for values
+  const int first8 = grown ? 0 : p.t0;
+  if (!values) {
+    for (int e = tid; e < (p.t1 - first8) * (D / 8); e += RW_THREADS) {
+      const int t = first8 + e / (D / 8), d0 = e % (D / 8) * 8;
+      u32x2* dst = reinterpret_cast<u32x2*>(codes + (int64_t)t * D + d0);
+      uint32_t u[2] = {0, 0};
+      const u32x2 prev = t < p.t0 ? *dst : u32x2{0, 0};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float q;
+        if (t < p.t0) q = (float)(int8_t)(prev[i >> 2] >> (8 * (i & 3))) * ratio;
+        else q = bad ? 0.0f : value_at<SRC>(x, x0 + (int64_t)(t - p.t0) * stride + d0 + i) * inv;
+        q = __builtin_rintf(q);
+        q = q > 127.0f ? 127.0f : q < -127.0f ? -127.0f : q;
+        u[i >> 2] |= ((uint32_t)(int)q & 0xffu) << (8 * (i & 3));
+      }
+      *dst = u32x2{u[0], u[1]};
+    }
+  } else {
+    const int c8 = first8 / 8, n8 = (p.t1 + 7) / 8 - c8;
+    for (int e = tid; e < n8 * D; e += RW_THREADS) {
+      const int t = (c8 + e / D) * 8, ch = e % D;
+      u32x2* dst = reinterpret_cast<u32x2*>(codes + v_byte<D>(t, ch));
+      const u32x2 prev = *dst;
+      uint32_t u[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t was = (prev[i >> 2] >> (8 * (i & 3))) & 0xffu;
+        uint32_t code = was;   // a token before an unchanged scale, or one behind the new ones
+        if (t + i < p.t1 && (t + i >= p.t0 || grown)) {
+          float q;
+          if (t + i < p.t0) q = (float)(int8_t)was * ratio;
+          else q = bad ? 0.0f : value_at<SRC>(x, x0 + (int64_t)(t + i - p.t0) * stride + ch) * inv;
+          q = __builtin_rintf(q);
+          q = q > 127.0f ? 127.0f : q < -127.0f ? -127.0f : q;
+          code = (uint32_t)(int)q & 0xffu;
+        }
+        u[i >> 2] |= code << (8 * (i & 3));
+      }
+      *dst = u32x2{u[0], u[1]};
+    }
+  }
+}
+
+// The decoder, over the same pieces.
+template <int DST, int D>
+__global__ __launch_bounds__(RW_THREADS) void k_kv8_read(Cache c, Batch b, void* __restrict__ k, void* __restrict__ v,
+                                                         int64_t k_stride, int64_t v_stride) {
+  const int tid = threadIdx.x, head = blockIdx.y;
+  const bool values = blockIdx.z != 0;
+  void* x = values ? v : k;
+  const int64_t stride = values ? v_stride : k_stride;
+  Piece p = find_piece(b, c, blockIdx.x);
+  if (p.t1 > p.t0) {
+    const int64_t at = (int64_t)p.id * c.n_heads + head;
+    const float d = p.id < 0 ? 0.0f : (values ? c.vd : c.kd)[at];
+    const int8_t* codes = (values ? c.v : c.k) + at * c.block * D;
+    for (int e = tid; e < (p.t1 - p.t0) * D; e += RW_THREADS) {
+      const int t = p.t0 + e / D, ch = e % D;
+      float f = 0.0f;
+      if (p.id >= 0) f = (float)codes[values ? v_byte<D>(t, ch) : t * D + ch] * d;
+      store_at<DST>(x, (int64_t)(p.row + t - p.t0) * stride + (int64_t)head * D + ch, f);
+    }
+  }
+  // rows before position 0: the sequence's first unit clears them
+  Span sp;
+  if (find_unit(b, blockIdx.x, 1, c.block, 2, sp) == 0 && sp.len < sp.n) {
+    const int64_t lost = sp.len < 0 ? sp.n : (int64_t)sp.n - sp.len;
+    for (int64_t e = tid; e < lost * D; e += RW_THREADS)
+      store_at<DST>(x, (sp.row0 + e / D) * stride + (int64_t)head * D + e % D, 0.0f);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// attention
+
+// Four codes to four fp16 values, exactly: the byte u = code + 128 in the low
+// bits of 1024 (0x6400), minus 1152.
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const h16x2 bias = {(_Float16)1152.0f, (_Float16)1152.0f};
+  const uint32_t a = __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u);
+  const uint32_t b = __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u);
+  lo = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h16x2, a) - bias);
+  hi = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h16x2, b) - bias);
+}
+
+__device__ __forceinline__ h16x8 codes8(uint32_t w0, uint32_t w1) {
+  u32x4 r;
+  uint32_t a, b;
+  codes_to_half(w0, a, b);
+  r[0] = a;
+  r[1] = b;
+  codes_to_half(w1, a, b);
+  r[2] = a;
+  r[3] = b;
+  return __builtin_bit_cast(h16x8, r);
+}
+
+struct Attention {
+  const void* q;
+  void* out;
+  float* part;       // [units][heads][splits][16] x (D values, maximum, sum)
+  int64_t q_stride, out_stride;
+  float scale;       // times log2(e)
+  int64_t window;
+  int group;         // query heads per key/value head
+  int n_splits;
+};
+
+constexpr int A_ROWS = 16;       // rows of a unit
+constexpr int A_WAVES = 4;
+constexpr int A_MIN_GROUPS = 8;  // token groups a split is worth
+constexpr float NEG_INF = -__builtin_inff();
+// Weights are exp2(s - max + 10): the largest is 2^10, so that small ones keep
+// more of their bits in fp16, whose normal range ends at 2^-14.
+constexpr float P_SHIFT = 10.0f;
+
+// The visible groups of 32 tokens of a unit and their share for one split.
+struct Range {
+  int g0, n, per, used;   // first group, groups, groups per split, splits that have any
+};
+
+__device__ __forceinline__ Range visible(const Span& sp, int first_row, int rows, const Attention& a, int64_t limit) {
+  Range r = {0, 0, 0, 0};
+  if (rows <= 0) return r;
+  int64_t last = (int64_t)sp.len - sp.n + (first_row + rows - 1) / a.group;
+  if (last >= limit) last = limit - 1;
+  int64_t from = 0;
+  if (a.window > 0) {
+    from = (int64_t)sp.len - sp.n + first_row / a.group - a.window + 1;
+    if (from < 0) from = 0;
+  }
+  if (last < from) return r;
+  r.g0 = (int)(from / GROUP);
+  r.n = (int)(last / GROUP) - r.g0 + 1;
+  r.per = (r.n + a.n_splits - 1) / a.n_splits;
+  if (r.per < A_MIN_GROUPS) r.per = A_MIN_GROUPS;
+  r.used = (r.n + r.per - 1) / r.per;
+  return r;
+}
+
+// Eight query values of one row as fp16 operands: the row is scaled by 2^-e
+// (its largest magnitude then lies in [2^13, 2^14)), and fp32 rows keep a
+// second part for the bits that the first one lost.
+template <int SRC>
+__device__ __forceinline__ void query_half(const float (&x)[8], int e, h16x8& hi, h16x8& lo) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float f = __builtin_ldexpf(x[i], 14 - e);
+    hi[i] = (_Float16)f;
+    if (SRC == QR_F32) lo[i] = (_Float16)(f - (float)hi[i]);
+  }
+}
+
+// Attention of 16 rows (a row is a token and one of the query heads of the
+// key/value head) over one split of their tokens. Four waves take the
+// 32-token groups in turn; everything a wave needs of a group goes from
+// memory straight into matrix operands, once. Transposed products: S' = K Q',
+// so that a lane holds eight neighbouring tokens of one row, which is what
+// the second product, O' = V' P', takes as its right operand.
+template <int SRC, int D>
+__global__ __launch_bounds__(A_WAVES * WAVE) void k_attention_kv8(Cache c, Batch b, Attention a) {
+  constexpr int KS = D / 64;   // 64-channel steps of the first product
+  constexpr int VS = D / 32;   // 32-channel steps of the second
+  constexpr bool F32 = SRC == QR_F32;
+  __shared__ float join_o[A_WAVES][A_ROWS][D + 4];
+  __shared__ float join_m[A_WAVES][A_ROWS], join_l[A_WAVES][A_ROWS];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int li = lane & 15, lg = lane >> 4;
+  const int head = blockIdx.y, split = blockIdx.z;
+
+  Span sp;
+  const int u = find_unit(b, blockIdx.x, a.group, A_ROWS, 1, sp);
+  const int64_t n_rows = (int64_t)sp.n * a.group;
+  const int64_t first_row = (int64_t)u * A_ROWS;
+  if (u < 0 || first_row >= n_rows) return;
+  const int rows = (int)(n_rows - first_row < A_ROWS ? n_rows - first_row : A_ROWS);
+  const int64_t limit = b.table_width * c.block;
+  const Range vis = visible(sp, (int)first_row, rows, a, limit);
+  if (split > 0 && split >= vis.used) return;
+
+  // this lane's row
+  const int r = (int)first_row + (li < rows ? li : rows - 1);
+  const int tok = sp.row0 + r / a.group;
+  const int qh = head * a.group + r % a.group;
+  const int64_t pos = (int64_t)sp.len - sp.n + r / a.group;
+  const int64_t low = a.window > 0 ? pos - a.window : -1;   // positions above low, up to pos
+
+  // queries
+  h16x8 qhi[2 * KS], qlo[2 * KS];
+  float row_scale;
+  {
+    float x[2 * KS][8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float f = value_at<SRC>(a.q, tok * a.q_stride + (int64_t)qh * D + 64 * s + 16 * lg + 8 * h + i);
+          x[2 * s + h][i] = f;
+          const uint32_t m = __builtin_bit_cast(uint32_t, f) & 0x7fffffffu;
+          top = m > top ? m : top;
+        }
+#pragma unroll
+    for (int s = 16; s < 64; s <<= 1) {
+      const uint32_t o = (uint32_t)__shfl_xor((int)top, s);
+      top = o > top ? o : top;
+    }
+    const bool bad = top >= 0x7f800000u;
+    const float amax = bad ? 0.0f : __builtin_bit_cast(float, top);
+    int e = 0;
+    if (amax > 0.0f) (void)__builtin_frexpf(amax, &e);
+#pragma unroll
+    for (int s = 0; s < 2 * KS; ++s) query_half<SRC>(x[s], e, qhi[s], qlo[s]);
+    row_scale = bad ? __builtin_nanf("") : __builtin_ldexpf(a.scale, e - 14);
+  }
+
+  f32x4 acc[2 * VS] = {};
+  float m_run = NEG_INF, l_run = 0.0f;
+  const int end = vis.g0 + (vis.n < (split + 1) * vis.per ? vis.n : (split + 1) * vis.per);
+  for (int g = vis.g0 + split * vis.per + wave; g < end; g += A_WAVES) {
+    const int64_t t0 = (int64_t)g * GROUP;
+    const int id = __builtin_amdgcn_readfirstlane(block_of(b, c, sp.seq, t0 / c.block));
+    if (id < 0) continue;
+    const int64_t at = (int64_t)id * c.n_heads + head;
+    const int in_block = (int)(t0 % c.block);
+    const int8_t* kp = c.k + (at * c.block + in_block) * D;
+    const int8_t* vp = c.v + (at * c.block + in_block) * D;
+    const float kd = c.kd[at], vd = c.vd[at];
+    f32x4 s[2] = {};
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int8_t* row = kp + (8 * (li >> 2) + 4 * t + (li & 3)) * D + 16 * lg;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(row + 64 * ks);
+        const h16x8 k0 = codes8(w[0], w[1]), k1 = codes8(w[2], w[3]);
+        s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qhi[2 * ks], s[t], 0, 0, 0);
+        s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qhi[2 * ks + 1], s[t], 0, 0, 0);
+        if (F32) {
+          s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qlo[2 * ks], s[t], 0, 0, 0);
+          s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qlo[2 * ks + 1], s[t], 0, 0, 0);
+        }
+      }
+    }
+    // scores of tokens t0 + 8 lg + i, in units of log 2
+    const float f = row_scale * kd;
+    float p[8];
+    float top = NEG_INF;
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t j = t0 + 8 * lg + i;
+      const bool seen = j <= pos && j > low;
+      p[i] = seen ? s[i >> 2][i & 3] * f : NEG_INF;
+      top = __builtin_fmaxf(top, p[i]);
+      any |= seen;
+    }
+    // a row that sees none of the group must not meet its value scale, which
+    // may be NaN
+    uint64_t sees = __ballot(any);
+    sees |= sees >> 32;
+    sees |= sees >> 16;
+    const float vs = (sees >> li) & 1 ? vd : 0.0f;
+    top = __builtin_fmaxf(top, __shfl_xor(top, 16));
+    top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+    const float m_new = __builtin_fmaxf(m_run, top);
+    const float ref = m_new == NEG_INF ? 0.0f : m_new - P_SHIFT;
+    const float alpha = __builtin_amdgcn_exp2f(m_run - (m_new == NEG_INF ? 0.0f : m_new));
+    m_run = m_new;
+    float sum = 0.0f;
+    h16x8 phi, plo;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      p[i] = __builtin_amdgcn_exp2f(p[i] - ref);
+      sum += p[i];
+      phi[i] = (_Float16)p[i];
+      if (F32) plo[i] = (_Float16)(p[i] - (float)phi[i]);
+    }
+    l_run = __builtin_fmaf(l_run, alpha, sum);
+#pragma unroll
+    for (int vsx = 0; vsx < VS; ++vsx) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(vp + (16 * vsx + li) * 64 + 16 * lg);
+      const h16x8 v0 = codes8(w[0], w[1]), v1 = codes8(w[2], w[3]);
+      f32x4 o0 = {}, o1 = {};
+      o0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, phi, o0, 0, 0, 0);
+      o1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, phi, o1, 0, 0, 0);
+      if (F32) {
+        o0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, plo, o0, 0, 0, 0);
+        o1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, plo, o1, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[2 * vsx][i] = __builtin_fmaf(o0[i], vs, acc[2 * vsx][i] * alpha);
+        acc[2 * vsx + 1][i] = __builtin_fmaf(o1[i], vs, acc[2 * vsx + 1][i] * alpha);
+      }
+    }
+  }
+  l_run += __shfl_xor(l_run, 16);
+  l_run += __shfl_xor(l_run, 32);
+
+  // the waves' parts joined: lane (li, lg) holds channels 32 vs + 8 lg + 2 i +
+  // (0, 1) of row li
+#pragma unroll
+  for (int vsx = 0; vsx < VS; ++vsx)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      join_o[wave][li][32 * vsx + 8 * lg + 2 * i] = acc[2 * vsx][i];
+      join_o[wave][li][32 * vsx + 8 * lg + 2 * i + 1] = acc[2 * vsx + 1][i];
+    }
+  if (lg == 0) {
+    join_m[wave][li] = m_run;
+    join_l[wave][li] = l_run;
+  }
+  __syncthreads();
+  for (int e = tid; e < rows * D; e += A_WAVES * WAVE) {
+    const int row = e / D, ch = e % D;
+    float m = NEG_INF;
+#pragma unroll
+    for (int w = 0; w < A_WAVES; ++w) m = __builtin_fmaxf(m, join_m[w][row]);
+    const float ref = m == NEG_INF ? 0.0f : m;
+    float o = 0.0f, l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < A_WAVES; ++w) {
+      const float f = __builtin_amdgcn_exp2f(join_m[w][row] - ref);
+      o = __builtin_fmaf(join_o[w][row][ch], f, o);
+      l = __builtin_fmaf(join_l[w][row], f, l);
+    }
+    if (vis.used <= 1) {
+      const int rr = (int)first_row + row;
+      const int64_t at = (int64_t)(sp.row0 + rr / a.group) * a.out_stride + (int64_t)(head * a.group + rr % a.group) * D + ch;
+      store_at<SRC>(a.out, at, l == 0.0f ? 0.0f : o / l);
+    } else {
+      float* part = a.part + (((int64_t)blockIdx.x * c.n_heads + head) * a.n_splits + split) * A_ROWS * (D + 2);
+      part[row * D + ch] = o;
+      if (ch == 0) {
+        part[A_ROWS * D + row] = m;
+        part[A_ROWS * D + A_ROWS + row] = l;
+      }
+    }
+  }
+}
+
+// Joins the splits of a unit.
+template <int SRC, int D>
+__global__ __launch_bounds__(256) void k_attention_join(Cache c, Batch b, Attention a) {
+  Span sp;
+  const int u = find_unit(b, blockIdx.x, a.group, A_ROWS, 1, sp);
+  const int64_t n_rows = (int64_t)sp.n * a.group;
+  const int64_t first_row = (int64_t)u * A_ROWS;
+  if (u < 0 || first_row >= n_rows) return;
+  const int rows = (int)(n_rows - first_row < A_ROWS ? n_rows - first_row : A_ROWS);
+  const Range vis = visible(sp, (int)first_row, rows, a, b.table_width * c.block);
+  if (vis.used <= 1) return;
+  const int head = blockIdx.y;
+  const float* part = a.part + ((int64_t)blockIdx.x * c.n_heads + head) * a.n_splits * A_ROWS * (D + 2);
+  for (int e = threadIdx.x; e < rows * D; e += 256) {
+    const int row = e / D, ch = e % D;
+    float m = NEG_INF;
+    for (int z = 0; z < vis.used; ++z) m = __builtin_fmaxf(m, part[z * A_ROWS * (D + 2) + A_ROWS * D + row]);
+    const float ref = m == NEG_INF ? 0.0f : m;
+    float o = 0.0f, l = 0.0f;
+    for (int z = 0; z < vis.used; ++z) {
+      const float* pz = part + z * A_ROWS * (D + 2);
+      const float f = __builtin_amdgcn_exp2f(pz[A_ROWS * D + row] - ref);
+      o = __builtin_fmaf(pz[row * D + ch], f, o);
+      l = __builtin_fmaf(pz[A_ROWS * D + A_ROWS + row], f, l);
+    }
+    const int rr = (int)first_row + row;
+    const int64_t at = (int64_t)(sp.row0 + rr / a.group) * a.out_stride + (int64_t)(head * a.group + rr % a.group) * D + ch;
+    store_at<SRC>(a.out, at, l == 0.0f ? 0.0f : o / l);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+
+bool valid_cache(const qr_kv8* c) {
+  return c && c->n_blocks >= 0 && c->n_blocks <= INT32_MAX && c->n_heads >= 1 && c->n_heads <= MAX_HEADS &&
+         (c->head_dim == 64 || c->head_dim == 128 || c->head_dim == 256) &&
+         (c->block_tokens == 32 || c->block_tokens == 64 || c->block_tokens == 128);
+}
+
+int check_batch(const qr_kv8* c, int dtype, int64_t n_tok, int64_t n_seq, int64_t table_width) {
+  if (dtype != QR_F32 && dtype != QR_BF16) return qr_fail(QR_EINVAL_TYPE, "element type %d is not QR_F32 or QR_BF16", dtype);
+  if (!valid_cache(c))
+    return qr_fail(QR_EINVAL_SHAPE, "the cache needs 0 <= n_blocks < 2^31, 1 <= n_heads <= %d, head_dim 64, 128 or 256 "
+                   "and block_tokens 32, 64 or 128", MAX_HEADS);
+  if (n_tok < 0 || n_seq < 0 || table_width < 0)
+    return qr_fail(QR_EINVAL_SHAPE, "negative n_tok, n_seq or table_width");
+  if (n_tok > INT32_MAX || n_seq > INT32_MAX - 1 || table_width > INT32_MAX)
+    return qr_fail(QR_EOVERFLOW, "n_tok, n_seq and table_width must be below 2^31");
+  return QR_OK;
+}
+
+int check_stride(const char* what, int64_t stride, int64_t least, int64_t n_tok) {
+  if (stride < least || stride % 8 != 0)
+    return qr_fail(QR_EINVAL_SHAPE, "%s=%lld must be a multiple of 8, at least %lld", what, (long long)stride,
+                   (long long)least);
+  if (n_tok > 0 && stride > INT64_MAX / 4 / n_tok) return qr_fail(QR_EOVERFLOW, "%s too large", what);
+  return QR_OK;
+}
+
+int check_pointers(const qr_kv8* c, const int32_t* cu, const int32_t* kv_len, const int32_t* table, int64_t table_width) {
+  if (!cu || !kv_len || (!table && table_width > 0)) return qr_fail(QR_EINVAL_PTR, "cu, kv_len and table must be non-NULL");
+  if (!qr_aligned(cu, 4) || !qr_aligned(kv_len, 4) || !qr_aligned(table, 4))
+    return qr_fail(QR_EINVAL_PTR, "cu, kv_len and table must be 4-byte aligned");
+  if (c->n_blocks > 0 && (!c->k || !c->v || !c->kd || !c->vd)) return qr_fail(QR_EINVAL_PTR, "the cache's arrays must be non-NULL");
+  if (!qr_aligned(c->k, 16) || !qr_aligned(c->v, 16) || !qr_aligned(c->kd, 4) || !qr_aligned(c->vd, 4))
+    return qr_fail(QR_EINVAL_PTR, "the cache's codes must be 16-byte aligned, its scales 4-byte aligned");
+  return QR_OK;
+}
+
+Cache device_cache(const qr_kv8* c) {
+  return {c->k, c->v, c->kd, c->vd, (int)c->n_blocks, (int)c->n_heads, (int)c->block_tokens};
+}
+
+// Units of a call that takes one piece of a block at a time.
+int64_t piece_units(const qr_kv8* c, int64_t n_tok, int64_t n_seq) { return n_tok / c->block_tokens + 2 * n_seq; }
+
+int64_t row_units(int64_t n_tok, int64_t n_seq, int64_t group) { return n_tok * group / A_ROWS + n_seq; }
+
+// Splits of the tokens, so that a few sequences still fill 256 CUs: about
+// four workgroups per CU, none for less than A_MIN_GROUPS groups.
+int64_t splits(const qr_kv8* c, int64_t n_tok, int64_t n_seq, int64_t group, int64_t table_width) {
+  const int64_t rows = (n_tok * group + n_seq - 1) / n_seq;
+  const int64_t busy = n_seq * ((rows + A_ROWS - 1) / A_ROWS) * c->n_heads;
+  const int64_t most = (table_width * (c->block_tokens / GROUP) + A_MIN_GROUPS - 1) / A_MIN_GROUPS;
+  int64_t z = (1024 + busy - 1) / busy;
+  if (z > most) z = most;
+  if (z > 128) z = 128;
+  return z < 1 ? 1 : z;
+}
+
+template <int SRC, int D>
+int launch_attention(const Cache& c, const Batch& b, const Attention& a, uint32_t units, hipStream_t s) {
+  const dim3 grid(units, (uint32_t)c.n_heads, (uint32_t)a.n_splits);
+  hipLaunchKernelGGL((k_attention_kv8<SRC, D>), grid, dim3(A_WAVES * WAVE), 0, s, c, b, a);
+  if (a.n_splits > 1) {
+    const int rc = qr_check_launch("k_attention_kv8");
+    if (rc != QR_OK) return rc;
+    hipLaunchKernelGGL((k_attention_join<SRC, D>), dim3(units, (uint32_t)c.n_heads), dim3(256), 0, s, c, b, a);
+  }
+  return qr_check_launch("k_attention_kv8");
+}
+
+template <int SRC, int D>
+int launch_append(const Cache& c, const Batch& b, const void* k, const void* v, int64_t ks, int64_t vs, uint32_t units,
+                  hipStream_t s) {
+  hipLaunchKernelGGL((k_kv8_append<SRC, D>), dim3(units, (uint32_t)c.n_heads, 2), dim3(RW_THREADS), 0, s, c, b, k, v, ks, vs);
+  return qr_check_launch("k_kv8_append");
+}
+
+template <int DST, int D>
+int launch_read(const Cache& c, const Batch& b, void* k, void* v, int64_t ks, int64_t vs, uint32_t units, hipStream_t s) {
+  hipLaunchKernelGGL((k_kv8_read<DST, D>), dim3(units, (uint32_t)c.n_heads, 2), dim3(RW_THREADS), 0, s, c, b, k, v, ks, vs);
+  return qr_check_launch("k_kv8_read");
+}
+
+// The checks that writing and reading share; QR_OK with *units == 0: nothing to do.
+int check_rows(const qr_kv8* c, int dtype, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+               int64_t n_tok, int64_t n_seq, const int32_t* cu, const int32_t* kv_len, const int32_t* table,
+               int64_t table_width, int64_t* units) {
+  *units = 0;
+  int rc = check_batch(c, dtype, n_tok, n_seq, table_width);
+  if (rc == QR_OK) rc = check_stride("k_stride", k_stride, c->n_heads * c->head_dim, n_tok);
+  if (rc == QR_OK) rc = check_stride("v_stride", v_stride, c->n_heads * c->head_dim, n_tok);
+  if (rc != QR_OK || n_tok == 0 || n_seq == 0) return rc;
+  rc = check_pointers(c, cu, kv_len, table, table_width);
+  if (rc != QR_OK) return rc;
+  if (!k || !v || !qr_aligned(k, 16) || !qr_aligned(v, 16))
+    return qr_fail(QR_EINVAL_PTR, "k and v must be non-NULL and 16-byte aligned");
+  *units = piece_units(c, n_tok, n_seq);
+  if (*units > UINT32_MAX / RW_THREADS) return qr_fail(QR_EOVERFLOW, "n_tok and n_seq need too many workgroups for one launch");
+  return QR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qr_kv8_code_bytes(const qr_kv8* c) {
+  if (!valid_cache(c)) return 0;
+  return (size_t)(c->n_blocks * c->n_heads * c->block_tokens * c->head_dim);
+}
+
+int qr_kv8_append(const qr_kv8* c, int src, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                  int64_t n_tok, int64_t n_seq, const int32_t* cu, const int32_t* kv_len, const int32_t* table,
+                  int64_t table_width, void* stream) {
+  qr_clear_error();
+  int64_t units;
+  const int rc = check_rows(c, src, k, v, k_stride, v_stride, n_tok, n_seq, cu, kv_len, table, table_width, &units);
+  if (rc != QR_OK || units == 0) return rc;
+  const Cache cc = device_cache(c);
+  const Batch b = {cu, kv_len, table, table_width, (int)n_seq, (int)n_tok};
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const uint32_t n = (uint32_t)units;
+  switch (c->head_dim) {
+    case 64: return src == QR_BF16 ? launch_append<QR_BF16, 64>(cc, b, k, v, k_stride, v_stride, n, s)
+                                   : launch_append<QR_F32, 64>(cc, b, k, v, k_stride, v_stride, n, s);
+    case 128: return src == QR_BF16 ? launch_append<QR_BF16, 128>(cc, b, k, v, k_stride, v_stride, n, s)
+                                    : launch_append<QR_F32, 128>(cc, b, k, v, k_stride, v_stride, n, s);
+    default: return src == QR_BF16 ? launch_append<QR_BF16, 256>(cc, b, k, v, k_stride, v_stride, n, s)
+                                   : launch_append<QR_F32, 256>(cc, b, k, v, k_stride, v_stride, n, s);
+  }
+}
+
+int qr_kv8_read(const qr_kv8* c, int dst, void* k, void* v, int64_t k_stride, int64_t v_stride, int64_t n_tok,
+                int64_t n_seq, const int32_t* cu, const int32_t* kv_len, const int32_t* table, int64_t table_width,
+                void* stream) {
+  qr_clear_error();
+  int64_t units;
+  const int rc = check_rows(c, dst, k, v, k_stride, v_stride, n_tok, n_seq, cu, kv_len, table, table_width, &units);
+  if (rc != QR_OK || units == 0) return rc;
+  const Cache cc = device_cache(c);
+  const Batch b = {cu, kv_len, table, table_width, (int)n_seq, (int)n_tok};
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const uint32_t n = (uint32_t)units;
+  switch (c->head_dim) {
+    case 64: return dst == QR_BF16 ? launch_read<QR_BF16, 64>(cc, b, k, v, k_stride, v_stride, n, s)
+                                   : launch_read<QR_F32, 64>(cc, b, k, v, k_stride, v_stride, n, s);
+    case 128: return dst == QR_BF16 ? launch_read<QR_BF16, 128>(cc, b, k, v, k_stride, v_stride, n, s)
+                                    : launch_read<QR_F32, 128>(cc, b, k, v, k_stride, v_stride, n, s);
+    default: return dst == QR_BF16 ? launch_read<QR_BF16, 256>(cc, b, k, v, k_stride, v_stride, n, s)
+                                   : launch_read<QR_F32, 256>(cc, b, k, v, k_stride, v_stride, n, s);
+  }
+}
+
+size_t qr_attention_kv8_workspace_bytes(const qr_kv8* c, int64_t n_q_heads, int64_t n_tok, int64_t n_seq,
+                                        int64_t table_width) {
+  if (!valid_cache(c) || n_q_heads <= 0 || n_q_heads % c->n_heads != 0 || n_tok <= 0 || n_seq <= 0 || table_width < 0 ||
+      n_tok > INT32_MAX || n_seq > INT32_MAX - 1 || table_width > INT32_MAX || n_q_heads / c->n_heads > 1024 ||
+      n_tok * n_q_heads > INT32_MAX)
+    return 0;
+  const int64_t group = n_q_heads / c->n_heads;
+  const int64_t z = splits(c, n_tok, n_seq, group, table_width);
+  if (z == 1) return 0;
+  return (size_t)(row_units(n_tok, n_seq, group) * c->n_heads * z * A_ROWS * (c->head_dim + 2)) * sizeof(float);
+}
+
+int qr_attention_kv8(const qr_kv8* c, int src, const void* q, int64_t q_stride, int64_t n_q_heads, int64_t n_tok,
+                     int64_t n_seq, const int32_t* cu, const int32_t* kv_len, const int32_t* table, int64_t table_width,
+                     float scale, int64_t window, void* out, int64_t out_stride, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  qr_clear_error();
+  int rc = check_batch(c, src, n_tok, n_seq, table_width);
+  if (rc != QR_OK) return rc;
+  if (n_q_heads <= 0 || n_q_heads % c->n_heads != 0 || n_q_heads / c->n_heads > 1024)
+    return qr_fail(QR_EINVAL_SHAPE, "n_q_heads=%lld must be a multiple of n_heads=%lld, at most 1024 times it",
+                   (long long)n_q_heads, (long long)c->n_heads);
+  if (window < 0 || !(scale - scale == 0.0f)) return qr_fail(QR_EINVAL_SHAPE, "window must not be negative, scale must be finite");
+  rc = check_stride("q_stride", q_stride, n_q_heads * c->head_dim, n_tok);
+  if (rc == QR_OK) rc = check_stride("out_stride", out_stride, n_q_heads * c->head_dim, n_tok);
+  if (rc != QR_OK || n_tok == 0 || n_seq == 0) return rc;
+  if (n_tok * n_q_heads > INT32_MAX) return qr_fail(QR_EOVERFLOW, "n_tok * n_q_heads must be below 2^31");
+  rc = check_pointers(c, cu, kv_len, table, table_width);
+  if (rc != QR_OK) return rc;
+  if (!q || !out || !qr_aligned(q, 16) || !qr_aligned(out, 16))
+    return qr_fail(QR_EINVAL_PTR, "q and out must be non-NULL and 16-byte aligned");
+  const int64_t group = n_q_heads / c->n_heads;
+  const int64_t units = row_units(n_tok, n_seq, group);
+  if (units > UINT32_MAX / 256) return qr_fail(QR_EOVERFLOW, "n_tok and n_seq need too many workgroups for one launch");
+  const size_t need = qr_attention_kv8_workspace_bytes(c, n_q_heads, n_tok, n_seq, table_width);
+  if (need > 0 && (!workspace || !qr_aligned(workspace, 256)))
+    return qr_fail(QR_EINVAL_PTR, "workspace must be non-NULL and 256-byte aligned");
+  if (workspace_bytes < need)
+    return qr_fail(QR_EINVAL_SHAPE, "workspace has %zu bytes, %zu are needed", workspace_bytes, need);
+  const Cache cc = device_cache(c);
+  const Batch b = {cu, kv_len, table, table_width, (int)n_seq, (int)n_tok};
+  const Attention a = {q, out, reinterpret_cast<float*>(workspace), q_stride, out_stride, scale * 1.44269504088896340736f,
+                       window < (int64_t)1 << 32 ? window : (int64_t)1 << 32, (int)group, (int)splits(c, n_tok, n_seq, group, table_width)};
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const uint32_t n = (uint32_t)units;
+  switch (c->head_dim) {
+    case 64: return src == QR_BF16 ? launch_attention<QR_BF16, 64>(cc, b, a, n, s) : launch_attention<QR_F32, 64>(cc, b, a, n, s);
+    case 128: return src == QR_BF16 ? launch_attention<QR_BF16, 128>(cc, b, a, n, s) : launch_attention<QR_F32, 128>(cc, b, a, n, s);
+    default: return src == QR_BF16 ? launch_attention<QR_BF16, 256>(cc, b, a, n, s) : launch_attention<QR_F32, 256>(cc, b, a, n, s);
+  }
+}
+
+}  // extern "C"

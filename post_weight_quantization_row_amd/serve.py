@@ -1,0 +1,293 @@
+"""Python binding of libqrow.so's serving operators (argument marshalling
+only): 8-bit rows with one scale each and their product
+(include/serve/qrow_i8.h), a paged 8-bit key/value cache and attention over
+it (include/serve/qrow_kv8.h).
+
+Every function has the name of the C entry point it calls and takes torch
+tensors that live on the GPU; all arithmetic runs in the library's HIP
+kernels, on the device of the tensors and the stream given (torch's current
+one by default). There is no CPU fallback: without the built library or a GPU
+the calls raise.
+"""
+from __future__ import annotations
+
+import ctypes as C
+from typing import NamedTuple
+
+import torch
+
+from . import qrow
+from .qrow import QR_BF16, QR_F32, _check, _cuda_device, _on, _out, _stream
+
+# Every symbol the headers under include/serve/ declare.
+EXPORTS = ("qr_i8_row_bytes", "qr_quantize_rows_i8", "qr_matmul_i8", "qr_kv8_code_bytes", "qr_kv8_append",
+           "qr_kv8_read", "qr_attention_kv8_workspace_bytes", "qr_attention_kv8")
+HEAD_DIMS = (64, 128, 256)
+BLOCK_TOKENS = (32, 64, 128)
+
+_DTYPES = {torch.float32: QR_F32, torch.bfloat16: QR_BF16}
+_lib = None
+
+
+class _Kv8(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("kd", C.c_void_p), ("vd", C.c_void_p),
+                ("n_blocks", C.c_int64), ("n_heads", C.c_int64), ("head_dim", C.c_int64),
+                ("block_tokens", C.c_int64)]
+
+
+def load_library():
+    """libqrow.so with the serving entry points declared."""
+    global _lib
+    if _lib is None:
+        L = qrow.load_library()
+        vp, i64, i32, cache = C.c_void_p, C.c_int64, C.c_int, C.POINTER(_Kv8)
+        L.qr_i8_row_bytes.argtypes = [i64]
+        L.qr_quantize_rows_i8.argtypes = [i32, vp, i64, i64, i64, vp, vp, vp]
+        L.qr_matmul_i8.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i32, vp, i64, vp]
+        L.qr_kv8_code_bytes.argtypes = [cache]
+        rows = [cache, i32, vp, vp, i64, i64, i64, i64, vp, vp, vp, i64, vp]
+        L.qr_kv8_append.argtypes = rows
+        L.qr_kv8_read.argtypes = rows
+        L.qr_attention_kv8_workspace_bytes.argtypes = [cache, i64, i64, i64, i64]
+        L.qr_attention_kv8.argtypes = [cache, i32, vp, i64, i64, i64, i64, vp, vp, vp, i64, C.c_float, i64, vp, i64,
+                                       vp, C.c_size_t, vp]
+        for name in ("qr_i8_row_bytes", "qr_kv8_code_bytes", "qr_attention_kv8_workspace_bytes"):
+            getattr(L, name).restype = C.c_size_t
+        for name in ("qr_quantize_rows_i8", "qr_matmul_i8", "qr_kv8_append", "qr_kv8_read", "qr_attention_kv8"):
+            getattr(L, name).restype = C.c_int
+        _lib = L
+    return _lib
+
+
+def _dtype_id(t: torch.Tensor, name: str) -> int:
+    try:
+        return _DTYPES[t.dtype]
+    except KeyError:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}") from None
+
+
+def _call(device, fn, *args):
+    """fn(*args) with `device` current, as a launch on its stream needs."""
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args))
+
+
+# --------------------------------------------------------------------------
+# 8-bit rows and their product (include/serve/qrow_i8.h)
+
+def qr_i8_row_bytes(n_per_row: int) -> int:
+    return int(load_library().qr_i8_row_bytes(n_per_row))
+
+
+def qr_quantize_rows_i8(x: torch.Tensor, codes=None, scales=None, stream=None):
+    """Quantizes the rows of x ([n_rows, n_per_row] fp32/bf16, elements of a
+    row adjacent, rows any stride apart) to 8 bits with one scale per row:
+    tokens and weight channels alike. Returns (codes int8 [n_rows,
+    qr_i8_row_bytes(n_per_row)], scales fp32 [n_rows])."""
+    device = _cuda_device(x, "x")
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be 2-D with adjacent elements in a row")
+    src = _dtype_id(x, "x")
+    n_rows, n = x.shape
+    stride = x.stride(0) if n_rows > 1 else n
+    if stride < n:
+        raise ValueError("the rows of x must not overlap")
+    codes = _out(codes, (n_rows, qr_i8_row_bytes(n)), torch.int8, device)
+    scales = _out(scales, (n_rows,), torch.float32, device)
+    _call(device, load_library().qr_quantize_rows_i8, src, x.data_ptr(), n_rows, n, stride, codes.data_ptr(),
+          scales.data_ptr(), _stream(x, stream))
+    return codes, scales
+
+
+def _i8_rows(codes, scales, name, row_bytes, device):
+    _on(codes, name, device)
+    if codes.dtype != torch.int8 or codes.dim() != 2 or not codes.is_contiguous() or codes.shape[1] != row_bytes:
+        raise ValueError(f"{name} must be a contiguous int8 [n, {row_bytes}] tensor (qr_i8_row_bytes of n_in)")
+    _on(scales, name + "d", device)
+    if scales.dtype != torch.float32 or tuple(scales.shape) != (codes.shape[0],) or not scales.is_contiguous():
+        raise ValueError(f"{name}d must be a contiguous float32 tensor with one scale per row of {name}")
+
+
+def qr_matmul_i8(w: torch.Tensor, wd: torch.Tensor, x: torch.Tensor, xd: torch.Tensor, n_in: int, bias=None,
+                 dtype=torch.bfloat16, out=None, stream=None):
+    """y [n_tok, n_out] = (x * xd) @ (w * wd).T + bias for rows of 8-bit codes
+    w [n_out, qr_i8_row_bytes(n_in)] and x [n_tok, ...] with their scales wd
+    and xd (qr_quantize_rows_i8); bias fp32 [n_out] or None. y has `dtype`
+    (float32 or bfloat16), or is `out`, whose rows may be strided."""
+    device = _cuda_device(w, "w")
+    row_bytes = qr_i8_row_bytes(n_in)
+    _i8_rows(w, wd, "w", row_bytes, device)
+    _i8_rows(x, xd, "x", row_bytes, device)
+    n_out, n_tok = w.shape[0], x.shape[0]
+    if bias is not None:
+        _on(bias, "bias", device)
+        if bias.dtype != torch.float32 or tuple(bias.shape) != (n_out,) or not bias.is_contiguous():
+            raise ValueError("bias must be a contiguous float32 [n_out] tensor")
+    if out is None:
+        out = torch.empty((n_tok, n_out), dtype=dtype, device=device)
+    _on(out, "out", device)
+    dst = _dtype_id(out, "out")
+    if tuple(out.shape) != (n_tok, n_out) or (n_out > 1 and out.stride(1) != 1):
+        raise ValueError("out must be [n_tok, n_out] with adjacent elements in a row")
+    stride = out.stride(0) if n_tok > 1 else n_out
+    if stride < n_out:
+        raise ValueError("the rows of out must not overlap")
+    _call(device, load_library().qr_matmul_i8, w.data_ptr(), wd.data_ptr(), x.data_ptr(), xd.data_ptr(),
+          None if bias is None else bias.data_ptr(), n_out, n_tok, n_in, dst, out.data_ptr(), stride,
+          _stream(w, stream))
+    return out
+
+
+# --------------------------------------------------------------------------
+# the paged 8-bit cache and attention over it (include/serve/qrow_kv8.h)
+
+class Kv8Cache(NamedTuple):
+    """The arrays of a paged 8-bit cache (layouts in qrow_kv8.h)."""
+    k: torch.Tensor        # int8 [n_blocks, n_heads, block_tokens, head_dim]
+    v: torch.Tensor        # int8 [n_blocks, n_heads, block_tokens/32, head_dim/2, 4, 2, 8]
+    kd: torch.Tensor       # fp32 [n_blocks, n_heads]
+    vd: torch.Tensor       # fp32 [n_blocks, n_heads]
+
+
+def kv8_cache(n_blocks: int, n_heads: int, head_dim: int, block_tokens: int, device) -> Kv8Cache:
+    """A cache of n_blocks blocks (its contents need no clearing: what a
+    sequence's blocks hold is set when their tokens are appended)."""
+    if head_dim not in HEAD_DIMS or block_tokens not in BLOCK_TOKENS:
+        raise ValueError(f"head_dim must be one of {HEAD_DIMS}, block_tokens one of {BLOCK_TOKENS}")
+    empty = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=device)
+    return Kv8Cache(empty((n_blocks, n_heads, block_tokens, head_dim), torch.int8),
+                    empty((n_blocks, n_heads, block_tokens // 32, head_dim // 2, 4, 2, 8), torch.int8),
+                    empty((n_blocks, n_heads), torch.float32), empty((n_blocks, n_heads), torch.float32))
+
+
+def _cache(cache, device):
+    k, v, kd, vd = cache
+    _on(k, "cache.k", device)
+    _on(v, "cache.v", device)
+    _on(kd, "cache.kd", device)
+    _on(vd, "cache.vd", device)
+    if k.dim() != 4:
+        raise ValueError("cache.k must be [n_blocks, n_heads, block_tokens, head_dim]")
+    nb, h, bt, d = k.shape
+    if (k.dtype != torch.int8 or v.dtype != torch.int8 or kd.dtype != torch.float32 or vd.dtype != torch.float32
+            or tuple(v.shape) != (nb, h, bt // 32, d // 2, 4, 2, 8) or tuple(kd.shape) != (nb, h)
+            or tuple(vd.shape) != (nb, h) or not (k.is_contiguous() and v.is_contiguous() and kd.is_contiguous()
+                                                  and vd.is_contiguous())):
+        raise ValueError("the cache's tensors must have the types and shapes that kv8_cache gives them")
+    return _Kv8(k.data_ptr(), v.data_ptr(), kd.data_ptr(), vd.data_ptr(), nb, h, d, bt)
+
+
+def _batch(cu, kv_len, table, device):
+    _on(cu, "cu", device)
+    _on(kv_len, "kv_len", device)
+    _on(table, "table", device)
+    n_seq = kv_len.shape[0] if kv_len.dim() == 1 else -1
+    if (n_seq < 0 or tuple(cu.shape) != (n_seq + 1,) or table.dim() != 2 or table.shape[0] != n_seq
+            or not (cu.dtype == kv_len.dtype == table.dtype == torch.int32)
+            or not (cu.is_contiguous() and kv_len.is_contiguous() and table.is_contiguous())):
+        raise ValueError("cu, kv_len and table must be contiguous int32 tensors [n_seq + 1], [n_seq] and "
+                         "[n_seq, table_width]")
+    return n_seq, table.shape[1]
+
+
+def _heads(x, name, n_heads, head_dim, device):
+    """Stride of the tokens of x [n_tok, n_heads, head_dim], the heads of a
+    token adjacent."""
+    _on(x, name, device)
+    if x.dim() != 3 or x.shape[2] != head_dim or (n_heads is not None and x.shape[1] != n_heads):
+        raise ValueError(f"{name} must be [n_tok, {'n_heads' if n_heads is None else n_heads}, {head_dim}]")
+    if x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != head_dim):
+        raise ValueError(f"the heads of a token of {name} must be adjacent")
+    stride = x.stride(0) if x.shape[0] > 1 else x.shape[1] * head_dim
+    if stride % 8 or stride < x.shape[1] * head_dim:
+        raise ValueError(f"the tokens of {name} must be a multiple of 8 elements apart and not overlap")
+    return stride
+
+
+def qr_kv8_append(cache: Kv8Cache, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, kv_len: torch.Tensor,
+                  table: torch.Tensor, stream=None) -> Kv8Cache:
+    """Writes the keys and values k and v ([n_tok, n_heads, head_dim]
+    fp32/bf16, tokens any multiple of 8 elements apart) into the cache, in
+    place: rows cu[s] .. cu[s+1]-1 are the last tokens of sequence s, which
+    holds kv_len[s] tokens with them, in the blocks table[s]."""
+    device = _cuda_device(k, "k")
+    c = _cache(cache, device)
+    n_seq, width = _batch(cu, kv_len, table, device)
+    src = _dtype_id(k, "k")
+    ks = _heads(k, "k", c.n_heads, c.head_dim, device)
+    vs = _heads(v, "v", c.n_heads, c.head_dim, device)
+    if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must have one type and one number of tokens")
+    _call(device, load_library().qr_kv8_append, C.byref(c), src, k.data_ptr(), v.data_ptr(), ks, vs, k.shape[0],
+          n_seq, cu.data_ptr(), kv_len.data_ptr(), table.data_ptr(), width, _stream(k, stream))
+    return cache
+
+
+def qr_kv8_read(cache: Kv8Cache, cu: torch.Tensor, kv_len: torch.Tensor, table: torch.Tensor, n_tok: int,
+                dtype=torch.float32, k=None, v=None, stream=None):
+    """The values that the cache holds for the rows that cu, kv_len and table
+    describe (as in qr_kv8_append): (k, v), each [n_tok, n_heads, head_dim] of
+    `dtype`, or written into the tensors given. n_tok is the number of rows
+    (at least cu[n_seq]; rows from there on are left as they were)."""
+    device = _cuda_device(cache.k, "cache.k")
+    c = _cache(cache, device)
+    n_seq, width = _batch(cu, kv_len, table, device)
+    shape = (n_tok, c.n_heads, c.head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=device)
+    if v is None:
+        v = torch.empty(shape, dtype=dtype, device=device)
+    ks = _heads(k, "k", c.n_heads, c.head_dim, device)
+    vs = _heads(v, "v", c.n_heads, c.head_dim, device)
+    dst = _dtype_id(k, "k")
+    if v.dtype != k.dtype or k.shape[0] != n_tok or v.shape[0] != n_tok:
+        raise ValueError("k and v must have one type and n_tok tokens")
+    _call(device, load_library().qr_kv8_read, C.byref(c), dst, k.data_ptr(), v.data_ptr(), ks, vs, n_tok, n_seq,
+          cu.data_ptr(), kv_len.data_ptr(), table.data_ptr(), width, _stream(k, stream))
+    return k, v
+
+
+def qr_attention_kv8_workspace_bytes(cache: Kv8Cache, n_q_heads: int, n_tok: int, n_seq: int,
+                                     table_width: int) -> int:
+    c = _cache(cache, _cuda_device(cache.k, "cache.k"))
+    return int(load_library().qr_attention_kv8_workspace_bytes(C.byref(c), n_q_heads, n_tok, n_seq, table_width))
+
+
+def qr_attention_kv8(q: torch.Tensor, cache: Kv8Cache, cu: torch.Tensor, kv_len: torch.Tensor, table: torch.Tensor,
+                     scale=None, window: int = 0, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Causal attention of the rows q ([n_tok, n_q_heads, head_dim] fp32/bf16)
+    over their sequences' cached tokens; cu, kv_len and table as in
+    qr_kv8_append, scale 1/sqrt(head_dim) by default, window 0 or the number
+    of last tokens that a row sees. workspace: a CUDA uint8 tensor of at least
+    qr_attention_kv8_workspace_bytes bytes, or None to have one allocated
+    here. Rows from cu[n_seq] on are left as they were in `out` (undefined in
+    a new one)."""
+    device = _cuda_device(q, "q")
+    c = _cache(cache, device)
+    n_seq, width = _batch(cu, kv_len, table, device)
+    src = _dtype_id(q, "q")
+    qs = _heads(q, "q", None, c.head_dim, device)
+    n_tok, n_q = q.shape[0], q.shape[1]
+    if out is None:
+        out = torch.empty((n_tok, n_q, c.head_dim), dtype=q.dtype, device=device)
+    os_ = _heads(out, "out", n_q, c.head_dim, device)
+    if out.dtype != q.dtype or out.shape[0] != n_tok:
+        raise ValueError("out must have the type and shape of q")
+    lib = load_library()
+    need = lib.qr_attention_kv8_workspace_bytes(C.byref(c), n_q, n_tok, n_seq, width)
+    if stream is not None and workspace is None and need:
+        raise ValueError("a call on a stream of its own needs a workspace of its own")
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace is not None:
+        _on(workspace, "workspace", device)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call(device, lib.qr_attention_kv8, C.byref(c), src, q.data_ptr(), qs, n_q, n_tok, n_seq, cu.data_ptr(),
+          kv_len.data_ptr(), table.data_ptr(), width, c.head_dim ** -0.5 if scale is None else scale, window,
+          out.data_ptr(), os_, None if workspace is None else workspace.data_ptr(), ws_bytes, _stream(q, stream))
+    return out
