@@ -22,11 +22,7 @@ constexpr int ROW_ALIGN = 128;   // bytes: qr_i8_row_bytes
 __device__ __forceinline__ float bf16_value(uint16_t h) { return __builtin_bit_cast(float, (uint32_t)h << 16); }
 
 // fp32 to bf16, round to nearest even (NaN stays NaN).
-__device__ __forceinline__ uint16_t bf16_bits(float f) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, f);
-  if ((u & 0x7fffffffu) > 0x7f800000u) return (uint16_t)((u >> 16) | 0x40u);
-  return (uint16_t)((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
-}
+__device__ __forceinline__ uint16_t bf16_bits(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
 
 // ---------------------------------------------------------------------------
 // the row quantizer
@@ -166,7 +162,25 @@ struct Product {
   void* y;
   int64_t y_stride;
   int n_out, n_tok, row_bytes;
+  bool vec;   // four neighbouring outputs store as one vector
 };
+
+// Which tile a workgroup takes. Workgroups are dealt to the 8 XCDs in turn;
+// each XCD gets a run of neighbouring tiles, so that its L2 holds what they
+// share, and walks it in bands of GROUP_T token tiles.
+constexpr int XCDS = 8;
+constexpr int GROUP_T = 4;
+
+__device__ __forceinline__ void tile_of(uint32_t block, int out_tiles, int tok_tiles, int& bo, int& bt) {
+  const int n = out_tiles * tok_tiles;
+  const int xcd = (int)(block % XCDS), at = (int)(block / XCDS);
+  const int each = n / XCDS, extra = n % XCDS;
+  const int id = xcd * each + (xcd < extra ? xcd : extra) + at;
+  const int band = id / (GROUP_T * out_tiles), in_band = id % (GROUP_T * out_tiles);
+  const int width = tok_tiles - band * GROUP_T < GROUP_T ? tok_tiles - band * GROUP_T : GROUP_T;
+  bt = band * GROUP_T + in_band % width;
+  bo = in_band / width;
+}
 
 template <int DST>
 __device__ __forceinline__ void store_one(void* y, int64_t at, float v) {
@@ -178,73 +192,217 @@ __device__ __forceinline__ float scaled(int sum, float xd, float wd, float bias)
   return ((float)sum * xd) * wd + bias;
 }
 
-// 64 output channels x 64 tokens per workgroup, a 32 x 32 quarter per wave,
-// 128 values of the sum per step through LDS. The weights are the matrix
-// instruction's left operand: a lane then ends with four neighbouring
-// channels of one token.
-constexpr int T_OUT = 64, T_TOK = 64, T_K = 128;
-constexpr int T_PITCH = T_K + 16;   // bytes of a staged row
-
+// Stores four neighbouring channels of one token.
 template <int DST>
-__global__ __launch_bounds__(256) void k_matmul_i8(Product p) {
-  __shared__ __attribute__((aligned(16))) int8_t sw[T_OUT * T_PITCH];
-  __shared__ __attribute__((aligned(16))) int8_t sx[T_TOK * T_PITCH];
+__device__ __forceinline__ void store_four(const Product& p, int tok, int o, const i32x4& sum, float xd) {
+  const int64_t at = (int64_t)tok * p.y_stride + o;
+  if (o + 4 <= p.n_out) {
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = scaled(sum[e], xd, p.wd[o + e], p.bias ? p.bias[o + e] : 0.0f);
+    if (p.vec && DST == QR_BF16) {
+      *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(p.y) + at) =
+          u32x2{(uint32_t)bf16_bits(v[0]) | (uint32_t)bf16_bits(v[1]) << 16,
+                (uint32_t)bf16_bits(v[2]) | (uint32_t)bf16_bits(v[3]) << 16};
+    } else if (p.vec) {
+      *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p.y) + at) = f32x4{v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) store_one<DST>(p.y, at + e, v[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (o + e < p.n_out) store_one<DST>(p.y, at + e, scaled(sum[e], xd, p.wd[o + e], p.bias ? p.bias[o + e] : 0.0f));
+  }
+}
+
+// Few tokens: 16 channels x 16 * TT tokens per workgroup, the sum split over
+// its waves in chunks of 128 values, every operand loaded straight into the
+// registers that the matrix instruction reads (row li, 16 bytes at 16 lk). The
+// weights pass the chip once: bound by their bytes.
+constexpr int F_WAVES = 8;
+constexpr int F_BATCH = 4;   // chunks of a wave whose loads are in flight together
+
+template <int DST, int TT>
+__global__ __launch_bounds__(F_WAVES* WAVE) void k_matmul_i8_few(Product p) {
+  __shared__ i32x4 part[F_WAVES][TT][WAVE];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int li = lane & 15, lk = lane >> 4;
-  const int out_tiles = (p.n_out + T_OUT - 1) / T_OUT;
-  const int o0 = (int)(blockIdx.x % out_tiles) * T_OUT, t0 = (int)(blockIdx.x / out_tiles) * T_TOK;
-  const int wo = (wave & 1) * 32, wt = (wave >> 1) * 32;
-  i32x4 acc[2][2] = {};
-  for (int k0 = 0; k0 < p.row_bytes; k0 += T_K) {
+  const int out_tiles = (p.n_out + 15) / 16;
+  const int o0 = (int)(blockIdx.x % out_tiles) * 16, t0 = (int)(blockIdx.x / out_tiles) * 16 * TT;
+  // rows behind the last repeat it: their results are not stored
+  const int wr = o0 + li < p.n_out ? o0 + li : p.n_out - 1;
+  const int8_t* w = p.w + (int64_t)wr * p.row_bytes + 16 * lk;
+  const int8_t* x[TT];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = (tid >> 3) + 32 * i, col = (tid & 7) * 16;
-      // rows behind the last repeat it: their results are not stored
-      const int wr = o0 + row < p.n_out ? o0 + row : p.n_out - 1;
-      const int xr = t0 + row < p.n_tok ? t0 + row : p.n_tok - 1;
-      const i32x4 a = *reinterpret_cast<const i32x4*>(p.w + (int64_t)wr * p.row_bytes + k0 + col);
-      const i32x4 b = *reinterpret_cast<const i32x4*>(p.x + (int64_t)xr * p.row_bytes + k0 + col);
-      *reinterpret_cast<i32x4*>(sw + row * T_PITCH + col) = a;
-      *reinterpret_cast<i32x4*>(sx + row * T_PITCH + col) = b;
-    }
-    __syncthreads();
+  for (int j = 0; j < TT; ++j) {
+    const int xr = t0 + 16 * j + li < p.n_tok ? t0 + 16 * j + li : p.n_tok - 1;
+    x[j] = p.x + (int64_t)xr * p.row_bytes + 16 * lk;
+  }
+  const int chunks = p.row_bytes / 128;
+  i32x4 acc[TT] = {};
+  for (int c0 = wave; c0 < chunks; c0 += F_WAVES * F_BATCH) {
+    i32x4 a[F_BATCH][2], b[F_BATCH][2][TT];
 #pragma unroll
-    for (int kk = 0; kk < T_K; kk += 64) {
-      i32x4 a[2], b[2];
+    for (int u = 0; u < F_BATCH; ++u) {
+      const int c = c0 + u * F_WAVES < chunks ? c0 + u * F_WAVES : c0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        a[i] = *reinterpret_cast<const i32x4*>(sw + (wo + 16 * i + li) * T_PITCH + kk + 16 * lk);
-        b[i] = *reinterpret_cast<const i32x4*>(sx + (wt + 16 * i + li) * T_PITCH + kk + 16 * lk);
+      for (int h = 0; h < 2; ++h) {
+        a[u][h] = *reinterpret_cast<const i32x4*>(w + c * 128 + 64 * h);
+#pragma unroll
+        for (int j = 0; j < TT; ++j) b[u][h][j] = *reinterpret_cast<const i32x4*>(x[j] + c * 128 + 64 * h);
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], b[j], acc[i][j], 0, 0, 0);
     }
-    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < F_BATCH; ++u) {
+      if (c0 + u * F_WAVES < chunks) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < TT; ++j)
+            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u][h], b[u][h][j], acc[j], 0, 0, 0);
+      }
+    }
   }
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < TT; ++j) part[wave][j][lane] = acc[j];
+  __syncthreads();
+  if (wave < TT) {
+    i32x4 sum = part[0][wave][lane];
+#pragma unroll
+    for (int v = 1; v < F_WAVES; ++v) sum += part[v][wave][lane];
+    const int tok = t0 + 16 * wave + li;
+    if (tok < p.n_tok) store_four<DST>(p, tok, o0 + 4 * lk, sum, p.xd[tok]);
+  }
+}
+
+// Many tokens: a tile of 32 NI channels x 32 NJ tokens per workgroup, a
+// quarter of it per wave, 128 values of the sum per step through LDS. The
+// weights are the matrix instruction's left operand: a lane then ends with
+// four neighbouring channels of one token.
+//
+// A step's two halves of 64 values are in turn multiplied from registers
+// while the other half's operands are read from LDS; the next step's tile is
+// written to the second LDS buffer and the one after that is in flight from
+// memory. One barrier a step: it follows the reads of this step's second
+// half and the writes of the next step's tile.
+//
+// In LDS the 16-byte piece c of row r lies at r * 128 + (c ^ (r % 8)) * 16:
+// eight lanes that take one piece of neighbouring rows meet all banks.
+template <int DST, int NI, int NJ>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(NI * NJ > 32 ? 1 : 2))) void k_matmul_i8_tile(
+    Product p, int out_tiles, int tok_tiles) {
+  constexpr int TO = 32 * NI, TT = 32 * NJ;
+  __shared__ __attribute__((aligned(16))) int8_t lds[2][(TO + TT) * 128];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int li = lane & 15, lk = lane >> 4;
+  int bo, bt;
+  tile_of(blockIdx.x, out_tiles, tok_tiles, bo, bt);
+  const int o0 = bo * TO, t0 = bt * TT;
+  const int wo = (wave & 1) * (16 * NI), wt = (wave >> 1) * (16 * NJ);
+  const int8_t* wbase = p.w + (int64_t)o0 * p.row_bytes;
+  const int8_t* xbase = p.x + (int64_t)t0 * p.row_bytes;
+  // rows behind the last repeat it: their results are not stored
+  const int lr = tid >> 3, lc = (tid & 7) * 16;
+  uint32_t woff[NI], xoff[NJ];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int r = o0 + lr + 32 * i < p.n_out ? lr + 32 * i : p.n_out - 1 - o0;
+    woff[i] = (uint32_t)r * (uint32_t)p.row_bytes + lc;
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int r = t0 + lr + 32 * j < p.n_tok ? lr + 32 * j : p.n_tok - 1 - t0;
+    xoff[j] = (uint32_t)r * (uint32_t)p.row_bytes + lc;
+  }
+  const int put = lr * 128 + ((lc >> 4) ^ (lr & 7)) * 16;
+  i32x4 rw[NI], rx[NJ];
+  auto load = [&](int s) {
+    const int8_t* wk = wbase + (int64_t)s * 128;
+    const int8_t* xk = xbase + (int64_t)s * 128;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) rw[i] = *reinterpret_cast<const i32x4*>(wk + woff[i]);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) rx[j] = *reinterpret_cast<const i32x4*>(xk + xoff[j]);
+  };
+  auto store = [&](int8_t* buf) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) *reinterpret_cast<i32x4*>(buf + put + i * 32 * 128) = rw[i];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) *reinterpret_cast<i32x4*>(buf + TO * 128 + put + j * 32 * 128) = rx[j];
+  };
+  i32x4 a0[NI], b0[NJ], a1[NI], b1[NJ];
+  const int get0 = li * 128 + ((lk) ^ (li & 7)) * 16, get1 = li * 128 + ((4 + lk) ^ (li & 7)) * 16;
+  auto read = [&](const int8_t* buf, int get, i32x4(&a)[NI], i32x4(&b)[NJ]) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) a[i] = *reinterpret_cast<const i32x4*>(buf + wo * 128 + get + i * 16 * 128);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) b[j] = *reinterpret_cast<const i32x4*>(buf + TO * 128 + wt * 128 + get + j * 16 * 128);
+  };
+  i32x4 acc[NI][NJ] = {};
+  auto multiply = [&](const i32x4(&a)[NI], const i32x4(&b)[NJ]) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], b[j], acc[i][j], 0, 0, 0);
+  };
+  const int steps = p.row_bytes / 128;
+  load(0);
+  store(lds[0]);
+  load(steps > 1 ? 1 : 0);
+  __syncthreads();
+  read(lds[0], get0, a0, b0);
+  for (int s = 0; s + 1 < steps; ++s) {
+    read(lds[s & 1], get1, a1, b1);
+    store(lds[(s + 1) & 1]);
+    load(s + 2 < steps ? s + 2 : steps - 1);   // the last one twice: not used
+    multiply(a0, b0);
+    __syncthreads();
+    read(lds[(s + 1) & 1], get0, a0, b0);
+    multiply(a1, b1);
+  }
+  read(lds[(steps - 1) & 1], get1, a1, b1);
+  multiply(a0, b0);
+  multiply(a1, b1);
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
     const int tok = t0 + wt + 16 * j + li;
     if (tok >= p.n_tok) continue;
     const float xd = p.xd[tok];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int o = o0 + wo + 16 * i + 4 * lk + e;
-        if (o < p.n_out)
-          store_one<DST>(p.y, (int64_t)tok * p.y_stride + o, scaled(acc[i][j][e], xd, p.wd[o], p.bias ? p.bias[o] : 0.0f));
-      }
+    for (int i = 0; i < NI; ++i) store_four<DST>(p, tok, o0 + wo + 16 * i + 4 * lk, acc[i][j], xd);
   }
+}
+
+template <int DST, int TT>
+int launch_few(const Product& p, hipStream_t s) {
+  const int64_t tiles = (int64_t)((p.n_out + 15) / 16) * ((p.n_tok + 16 * TT - 1) / (16 * TT));
+  if (tiles > UINT32_MAX / (F_WAVES * WAVE)) return qr_fail(QR_EOVERFLOW, "n_out and n_tok need too many tiles for one launch");
+  hipLaunchKernelGGL((k_matmul_i8_few<DST, TT>), dim3((uint32_t)tiles), dim3(F_WAVES * WAVE), 0, s, p);
+  return qr_check_launch("k_matmul_i8_few");
+}
+
+template <int DST, int NI, int NJ>
+int launch_tile(const Product& p, hipStream_t s) {
+  const int out_tiles = (p.n_out + 32 * NI - 1) / (32 * NI), tok_tiles = (p.n_tok + 32 * NJ - 1) / (32 * NJ);
+  const int64_t tiles = (int64_t)out_tiles * tok_tiles;
+  if (tiles > UINT32_MAX / 256) return qr_fail(QR_EOVERFLOW, "n_out and n_tok need too many tiles for one launch");
+  hipLaunchKernelGGL((k_matmul_i8_tile<DST, NI, NJ>), dim3((uint32_t)tiles), dim3(256), 0, s, p, out_tiles, tok_tiles);
+  return qr_check_launch("k_matmul_i8_tile");
 }
 
 template <int DST>
 int launch_product(const Product& p, hipStream_t s) {
-  const int64_t tiles = (int64_t)((p.n_out + T_OUT - 1) / T_OUT) * ((p.n_tok + T_TOK - 1) / T_TOK);
-  if (tiles > UINT32_MAX / 256) return qr_fail(QR_EOVERFLOW, "n_out and n_tok need too many tiles for one launch");
-  hipLaunchKernelGGL((k_matmul_i8<DST>), dim3((uint32_t)tiles), dim3(256), 0, s, p);
-  return qr_check_launch("k_matmul_i8");
+  if (p.n_tok <= 16) return launch_few<DST, 1>(p, s);
+  if (p.n_tok <= 32) return launch_few<DST, 2>(p, s);
+  if (p.n_tok <= 64) return launch_few<DST, 4>(p, s);
+  // the largest tile that still gives most CUs (256) one
+  const int64_t big = (int64_t)((p.n_out + 255) / 256) * ((p.n_tok + 255) / 256);
+  if (big >= 200) return launch_tile<DST, 8, 8>(p, s);
+  const int64_t mid = (int64_t)((p.n_out + 127) / 128) * ((p.n_tok + 127) / 128);
+  if (mid >= 200) return launch_tile<DST, 4, 4>(p, s);
+  return launch_tile<DST, 2, 4>(p, s);
 }
 
 }  // namespace
@@ -290,7 +448,8 @@ int qr_matmul_i8(const int8_t* w, const float* wd, const int8_t* x, const float*
   if (!qr_aligned(w, 16) || !qr_aligned(x, 16) || !qr_aligned(wd, 4) || !qr_aligned(xd, 4) || !qr_aligned(bias, 4) ||
       !qr_aligned(y, dst == QR_BF16 ? 2 : 4))
     return qr_fail(QR_EINVAL_PTR, "codes must be 16-byte aligned, wd, xd, bias and y to their elements");
-  const Product p = {w, x, wd, xd, bias, y, y_stride, (int)n_out, (int)n_tok, (int)rb};
+  const uintptr_t four = dst == QR_BF16 ? 8 : 16;
+  const Product p = {w, x, wd, xd, bias, y, y_stride, (int)n_out, (int)n_tok, (int)rb, qr_aligned(y, four) && y_stride % 4 == 0};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   return dst == QR_BF16 ? launch_product<QR_BF16>(p, s) : launch_product<QR_F32>(p, s);
 }

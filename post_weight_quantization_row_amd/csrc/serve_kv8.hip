@@ -25,11 +25,7 @@ constexpr int MAX_HEADS = 1024;
 __device__ __forceinline__ float bf16_value(uint16_t h) { return __builtin_bit_cast(float, (uint32_t)h << 16); }
 
 // fp32 to bf16, round to nearest even (NaN stays NaN).
-__device__ __forceinline__ uint16_t bf16_bits(float f) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, f);
-  if ((u & 0x7fffffffu) > 0x7f800000u) return (uint16_t)((u >> 16) | 0x40u);
-  return (uint16_t)((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
-}
+__device__ __forceinline__ uint16_t bf16_bits(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
 
 template <int SRC>
 __device__ __forceinline__ float value_at(const void* x, int64_t i) {

@@ -108,7 +108,7 @@ def check_product(sv, n_out, n_tok, n_in, dtype, bias, seed, out=None, extreme=F
 
 SHAPES = [(1, 1, 1), (5, 1, 64), (17, 3, 129), (64, 64, 128), (65, 63, 256), (200, 1, 4096), (333, 16, 1000),
           (129, 17, 640), (256, 31, 2048), (100, 32, 2500), (40, 33, 384), (130, 100, 1024), (500, 64, 4096), (257, 129, 512),
-          (300, 333, 1100), (512, 512, 256), (1000, 700, 640), (77, 2000, 192), (2304, 520, 384)]
+          (300, 333, 1100), (512, 512, 256), (1000, 700, 640), (77, 2000, 192), (2304, 520, 384), (1900, 1801, 520), (3700, 3901, 200)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
