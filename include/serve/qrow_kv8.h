@@ -16,7 +16,8 @@
  *       a group of 32 tokens, byte (d/2)*64 + (t/8)*16 + (d%2)*8 + t%8 holds
  *       channel d of token t (eight tokens of one channel side by side, as the
  *       matrix instructions take them)
- *   kd, vd  [n_blocks][n_heads] scales; a code stands for scale * code.
+ *   kd, vd  [n_blocks][n_heads] scales, never negative; a code stands for
+ *       scale * code.
  * Sequence s: its token p lies in block table[s * table_width + p /
  * block_tokens], at p % block_tokens.
  *

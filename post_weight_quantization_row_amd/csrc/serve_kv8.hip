@@ -12,6 +12,7 @@
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
@@ -275,7 +276,7 @@ __device__ __forceinline__ h16x8 codes8(uint32_t w0, uint32_t w1) {
 struct Attention {
   const void* q;
   void* out;
-  float* part;       // [units][heads][splits][16] x (D values, maximum, sum)
+  float* part;       // [units][heads][splits] x (rows of D values, their maxima, their sums)
   int64_t q_stride, out_stride;
   float scale;       // times log2(e)
   int64_t window;
@@ -285,18 +286,19 @@ struct Attention {
 
 constexpr int A_ROWS = 16;       // rows of a unit
 constexpr int A_WAVES = 4;
-constexpr int A_MIN_GROUPS = 8;  // token groups a split is worth
+constexpr int A_MIN_GROUPS = 8;  // token groups a split is worth (both kernels)
 constexpr float NEG_INF = -__builtin_inff();
 // Weights are exp2(s - max + 10): the largest is 2^10, so that small ones keep
 // more of their bits in fp16, whose normal range ends at 2^-14.
 constexpr float P_SHIFT = 10.0f;
 
-// The visible groups of 32 tokens of a unit and their share for one split.
+// The visible tiles (of 32 `ng` tokens) of a unit and their share for one split.
 struct Range {
-  int g0, n, per, used;   // first group, groups, groups per split, splits that have any
+  int g0, n, per, used;   // first group of the first tile, tiles, tiles per split, splits that have any
 };
 
-__device__ __forceinline__ Range visible(const Span& sp, int first_row, int rows, const Attention& a, int64_t limit) {
+__device__ __forceinline__ Range visible(const Span& sp, int first_row, int rows, const Attention& a, int64_t limit,
+                                         int ng) {
   Range r = {0, 0, 0, 0};
   if (rows <= 0) return r;
   int64_t last = (int64_t)sp.len - sp.n + (first_row + rows - 1) / a.group;
@@ -307,10 +309,11 @@ __device__ __forceinline__ Range visible(const Span& sp, int first_row, int rows
     if (from < 0) from = 0;
   }
   if (last < from) return r;
-  r.g0 = (int)(from / GROUP);
-  r.n = (int)(last / GROUP) - r.g0 + 1;
+  const int tile = (int)(from / (GROUP * ng));
+  r.g0 = tile * ng;
+  r.n = (int)(last / (GROUP * ng)) - tile + 1;
   r.per = (r.n + a.n_splits - 1) / a.n_splits;
-  if (r.per < A_MIN_GROUPS) r.per = A_MIN_GROUPS;
+  if (r.per < A_MIN_GROUPS / ng) r.per = A_MIN_GROUPS / ng;
   r.used = (r.n + r.per - 1) / r.per;
   return r;
 }
@@ -352,7 +355,7 @@ __global__ __launch_bounds__(A_WAVES * WAVE) void k_attention_kv8(Cache c, Batch
   if (u < 0 || first_row >= n_rows) return;
   const int rows = (int)(n_rows - first_row < A_ROWS ? n_rows - first_row : A_ROWS);
   const int64_t limit = b.table_width * c.block;
-  const Range vis = visible(sp, (int)first_row, rows, a, limit);
+  const Range vis = visible(sp, (int)first_row, rows, a, limit, 1);
   if (split > 0 && split >= vis.used) return;
 
   // this lane's row
@@ -396,23 +399,72 @@ __global__ __launch_bounds__(A_WAVES * WAVE) void k_attention_kv8(Cache c, Batch
   f32x4 acc[2 * VS] = {};
   float m_run = NEG_INF, l_run = 0.0f;
   const int end = vis.g0 + (vis.n < (split + 1) * vis.per ? vis.n : (split + 1) * vis.per);
-  for (int g = vis.g0 + split * vis.per + wave; g < end; g += A_WAVES) {
-    const int64_t t0 = (int64_t)g * GROUP;
-    const int id = __builtin_amdgcn_readfirstlane(block_of(b, c, sp.seq, t0 / c.block));
-    if (id < 0) continue;
-    const int64_t at = (int64_t)id * c.n_heads + head;
-    const int in_block = (int)(t0 % c.block);
-    const int8_t* kp = c.k + (at * c.block + in_block) * D;
-    const int8_t* vp = c.v + (at * c.block + in_block) * D;
-    const float kd = c.kd[at], vd = c.vd[at];
+  const int begin = vis.g0 + split * vis.per + wave;
+  // every row sees all tokens from clear_from up to clear_to
+  const int64_t clear_to = (int64_t)sp.len - sp.n + first_row / a.group;
+  const int64_t clear_from = a.window > 0 ? (int64_t)sp.len - sp.n + (first_row + rows - 1) / a.group - a.window + 1 : 0;
+
+  // Blocks and scales of the wave's next 64 groups, one per lane; the codes of
+  // the next group are loaded while this one's are multiplied.
+  int ids = -1;
+  float kds = 0.0f, vds = 0.0f;
+  auto look_ahead = [&](int g) {
+    const int mine = g + lane * A_WAVES;
+    ids = mine < end ? block_of(b, c, sp.seq, (int64_t)mine * GROUP / c.block) : -1;
+    if (ids >= 0) {
+      kds = c.kd[(int64_t)ids * c.n_heads + head];
+      vds = c.vd[(int64_t)ids * c.n_heads + head];
+    }
+  };
+  u32x4 kw[2][KS], vw[VS];
+  int id = -1;
+  float kd = 0.0f, vd = 0.0f;
+  auto fetch = [&](int it) {
+    id = __builtin_amdgcn_readlane(ids, it);
+    kd = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, kds), it));
+    vd = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, vds), it));
+  };
+  auto load = [&](int g) {
+    if (id < 0) return;
+    const int64_t at = ((int64_t)id * c.n_heads + head) * c.block + ((int64_t)g * GROUP) % c.block;
+    const int8_t* kp = c.k + at * D;
+    const int8_t* vp = c.v + at * D;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+        kw[t][ks] =
+            *reinterpret_cast<const u32x4*>(kp + (8 * (li >> 2) + 4 * t + (li & 3)) * D + 16 * lg + 64 * ks);
+#pragma unroll
+    for (int vsx = 0; vsx < VS; ++vsx) vw[vsx] = *reinterpret_cast<const u32x4*>(vp + (16 * vsx + li) * 64 + 16 * lg);
+  };
+  look_ahead(begin);
+  fetch(0);
+  load(begin);
+  for (int g = begin, it = 0; g < end; g += A_WAVES) {
+    u32x4 kc[2][KS], vc[VS];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) kc[t][ks] = kw[t][ks];
+#pragma unroll
+    for (int vsx = 0; vsx < VS; ++vsx) vc[vsx] = vw[vsx];
+    const bool have = id >= 0;
+    const float kd_now = kd, vd_now = vd;
+    if (++it == WAVE) {
+      it = 0;
+      look_ahead(g + A_WAVES);
+    }
+    fetch(it);
+    load(g + A_WAVES);
+    if (!have) continue;
+
     f32x4 s[2] = {};
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int8_t* row = kp + (8 * (li >> 2) + 4 * t + (li & 3)) * D + 16 * lg;
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(row + 64 * ks);
-        const h16x8 k0 = codes8(w[0], w[1]), k1 = codes8(w[2], w[3]);
+        const h16x8 k0 = codes8(kc[t][ks][0], kc[t][ks][1]), k1 = codes8(kc[t][ks][2], kc[t][ks][3]);
         s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qhi[2 * ks], s[t], 0, 0, 0);
         s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qhi[2 * ks + 1], s[t], 0, 0, 0);
         if (F32) {
@@ -420,26 +472,35 @@ __global__ __launch_bounds__(A_WAVES * WAVE) void k_attention_kv8(Cache c, Batch
           s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qlo[2 * ks + 1], s[t], 0, 0, 0);
         }
       }
-    }
     // scores of tokens t0 + 8 lg + i, in units of log 2
-    const float f = row_scale * kd;
+    const int64_t t0 = (int64_t)g * GROUP;
+    const float f = row_scale * kd_now;
     float p[8];
     float top = NEG_INF;
-    bool any = false;
+    float vs = vd_now;
+    if (t0 >= clear_from && t0 + GROUP - 1 <= clear_to) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t j = t0 + 8 * lg + i;
-      const bool seen = j <= pos && j > low;
-      p[i] = seen ? s[i >> 2][i & 3] * f : NEG_INF;
-      top = __builtin_fmaxf(top, p[i]);
-      any |= seen;
+      for (int i = 0; i < 8; ++i) {
+        p[i] = s[i >> 2][i & 3] * f;
+        top = __builtin_fmaxf(top, p[i]);
+      }
+    } else {
+      bool any = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t j = t0 + 8 * lg + i;
+        const bool seen = j <= pos && j > low;
+        p[i] = seen ? s[i >> 2][i & 3] * f : NEG_INF;
+        top = __builtin_fmaxf(top, p[i]);
+        any |= seen;
+      }
+      // a row that sees none of the group must not meet its value scale,
+      // which may be NaN
+      uint64_t sees = __ballot(any);
+      sees |= sees >> 32;
+      sees |= sees >> 16;
+      if (!((sees >> li) & 1)) vs = 0.0f;
     }
-    // a row that sees none of the group must not meet its value scale, which
-    // may be NaN
-    uint64_t sees = __ballot(any);
-    sees |= sees >> 32;
-    sees |= sees >> 16;
-    const float vs = (sees >> li) & 1 ? vd : 0.0f;
     top = __builtin_fmaxf(top, __shfl_xor(top, 16));
     top = __builtin_fmaxf(top, __shfl_xor(top, 32));
     const float m_new = __builtin_fmaxf(m_run, top);
@@ -458,8 +519,7 @@ __global__ __launch_bounds__(A_WAVES * WAVE) void k_attention_kv8(Cache c, Batch
     l_run = __builtin_fmaf(l_run, alpha, sum);
 #pragma unroll
     for (int vsx = 0; vsx < VS; ++vsx) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(vp + (16 * vsx + li) * 64 + 16 * lg);
-      const h16x8 v0 = codes8(w[0], w[1]), v1 = codes8(w[2], w[3]);
+      const h16x8 v0 = codes8(vc[vsx][0], vc[vsx][1]), v1 = codes8(vc[vsx][2], vc[vsx][3]);
       f32x4 o0 = {}, o1 = {};
       o0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, phi, o0, 0, 0, 0);
       o1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, phi, o1, 0, 0, 0);
@@ -519,34 +579,400 @@ __global__ __launch_bounds__(A_WAVES * WAVE) void k_attention_kv8(Cache c, Batch
   }
 }
 
-// Joins the splits of a unit.
-template <int SRC, int D>
-__global__ __launch_bounds__(256) void k_attention_join(Cache c, Batch b, Attention a) {
+// ---------------------------------------------------------------------------
+// attention of many rows
+
+constexpr int P_ROWS = 128;      // rows of a unit: 32 per wave
+constexpr int P_WAVES = 4;
+constexpr float P_LAZY = 5.0f;   // how far scores may pass the reference maximum
+
+// The value scale of a group as (mantissa, exponent) for weights that carry
+// it: 2^e * 2^lm = scale, inv = 2^-lm. A scale of zero gets an exponent far
+// below all others, one that is not finite a NaN.
+struct ValueScale {
+  int e;
+  float lm, inv;
+};
+
+constexpr int E_NONE = -100000;
+
+__device__ __forceinline__ ValueScale value_scale(float vd) {
+  ValueScale v;
+  const float m = __builtin_amdgcn_frexp_mantf(vd);   // [0.5, 1)
+  v.e = vd > 0.0f ? __builtin_amdgcn_frexp_expf(vd) : E_NONE;
+  v.lm = vd > 0.0f ? __builtin_amdgcn_logf(m) : 0.0f;
+  v.inv = vd > 0.0f ? __builtin_amdgcn_rcpf(m) : 1.0f;
+  if (!(vd < __builtin_inff())) {
+    v.e = E_NONE;
+    v.lm = __builtin_nanf("");
+  }
+  return v;
+}
+
+// Attention of 128 rows (32 per wave) over one split of their tokens, in
+// tiles of 32 NG tokens. A tile's codes are turned into fp16 once, on their
+// way into LDS, and every wave multiplies from there: S' = K Q', O' = V' P'.
+// The rows of the K tile are placed so that the tokens which a lane gets from
+// the first product are the ones that it brings to the second.
+//
+// The value scale of a group of 32 tokens goes into the exponent of its
+// weights, relative to a power of two per row (e_ref) that follows the largest scale
+// met: no second pass over the outputs. Their sum takes the factor out again.
+// The outputs are rescaled only when a score passes the reference maximum by
+// 2^5 (the weights, at most 2^15, still fit fp16).
+template <int SRC, int D, int NG>
+__global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 128) ? 1 : 2) void k_attention_kv8_rows(Cache c, Batch b, Attention a) {
+  constexpr int THREADS = P_WAVES * WAVE;
+  constexpr int KS = D / 16;                     // steps of the first product
+  constexpr int DT = D / 32;                     // 32-channel tiles of the output
+  constexpr int TOK = GROUP * NG;
+  constexpr int CH = TOK * D / 16 / THREADS;     // 16-byte pieces per thread
+  constexpr bool F32 = SRC == QR_F32;
+  static_assert(CH >= 1 && TOK * D / 16 % THREADS == 0, "whole pieces");
+  __shared__ __attribute__((aligned(16))) uint8_t lds_k[2][TOK * D * 2];
+  __shared__ __attribute__((aligned(16))) uint8_t lds_v[2][TOK * D * 2];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int li = lane & 31, lh = lane >> 5;
+  const int head = blockIdx.y, split = blockIdx.z;
+
   Span sp;
-  const int u = find_unit(b, blockIdx.x, a.group, A_ROWS, 1, sp);
+  const int u = find_unit(b, blockIdx.x, a.group, P_ROWS, 1, sp);
   const int64_t n_rows = (int64_t)sp.n * a.group;
-  const int64_t first_row = (int64_t)u * A_ROWS;
+  const int64_t first_row = (int64_t)u * P_ROWS;
   if (u < 0 || first_row >= n_rows) return;
-  const int rows = (int)(n_rows - first_row < A_ROWS ? n_rows - first_row : A_ROWS);
-  const Range vis = visible(sp, (int)first_row, rows, a, b.table_width * c.block);
+  const int rows = (int)(n_rows - first_row < P_ROWS ? n_rows - first_row : P_ROWS);
+  const Range vis = visible(sp, (int)first_row, rows, a, b.table_width * c.block, NG);
+  if (split > 0 && split >= vis.used) return;
+
+  // this lane's row; a wave behind the last row repeats it
+  const int wrow = 32 * wave < rows ? 32 * wave : rows - 1;            // first row of the wave
+  const int wlast = 32 * wave + 31 < rows ? 32 * wave + 31 : rows - 1;
+  const int row = 32 * wave + li < rows ? 32 * wave + li : rows - 1;
+  const int r = (int)first_row + row;
+  const int tok = sp.row0 + r / a.group;
+  const int qh = head * a.group + r % a.group;
+  const int64_t base = (int64_t)sp.len - sp.n;
+  const int64_t pos = base + r / a.group;
+  const int64_t low = a.window > 0 ? pos - a.window : -1;
+  // all rows of the wave see the tokens clear_from .. clear_to, none sees any
+  // outside any_from .. any_to
+  const int64_t clear_to = base + (first_row + wrow) / a.group, any_to = base + (first_row + wlast) / a.group;
+  const int64_t clear_from = a.window > 0 ? any_to - a.window + 1 : 0;
+  const int64_t any_from = a.window > 0 ? clear_to - a.window + 1 : 0;
+
+  h16x8 qhi[KS], qlo[F32 ? KS : 1];
+  float row_scale;
+  {
+    uint32_t top = 0;
+    float x[KS][8];
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float f = value_at<SRC>(a.q, tok * a.q_stride + (int64_t)qh * D + 16 * s + 8 * lh + i);
+        x[s][i] = f;
+        const uint32_t m = __builtin_bit_cast(uint32_t, f) & 0x7fffffffu;
+        top = m > top ? m : top;
+      }
+    const uint32_t o = (uint32_t)__shfl_xor((int)top, 32);
+    top = o > top ? o : top;
+    const bool bad = top >= 0x7f800000u;
+    const float amax = bad ? 0.0f : __builtin_bit_cast(float, top);
+    int e = 0;
+    if (amax > 0.0f) (void)__builtin_frexpf(amax, &e);
+    // the factor's sign goes to the queries: a maximum of scores is then the
+    // maximum of products
+    const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[s][i] *= sign;
+      h16x8 lo;
+      query_half<SRC>(x[s], e, qhi[s], lo);
+      if (F32) qlo[s] = lo;
+    }
+    row_scale = bad ? __builtin_nanf("") : __builtin_ldexpf(a.scale * sign, e - 14);
+  }
+
+  f32x16 acc[DT] = {};
+  float m_run = NEG_INF, l_run = 0.0f;
+  int e_ref = E_NONE;
+
+  const int tile0 = vis.g0 / NG + split * vis.per;
+  const int tile_end = vis.g0 / NG + (vis.n < (split + 1) * vis.per ? vis.n : (split + 1) * vis.per);
+
+  // what is on its way: blocks of the tile after the staged one, codes and
+  // scales of the staged one
+  int ids[NG];
+  u32x4 rawk[CH] = {}, rawv[CH] = {};
+  float kd_in[NG], vd_in[NG];
+  bool have_in[NG];
+  auto look_up = [&](int tile) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+      ids[g] = tile < tile_end ? __builtin_amdgcn_readfirstlane(block_of(b, c, sp.seq, (int64_t)(tile * NG + g) * GROUP / c.block)) : -1;
+  };
+  auto fetch = [&](int tile) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int64_t at = (int64_t)(ids[g] < 0 ? 0 : ids[g]) * c.n_heads + head;
+      have_in[g] = ids[g] >= 0;
+      kd_in[g] = have_in[g] ? c.kd[at] : 0.0f;
+      vd_in[g] = have_in[g] ? c.vd[at] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int at = tid + i * THREADS;
+      const int g = __builtin_amdgcn_readfirstlane(at / (2 * D));   // group: 2 D pieces each
+      int id = ids[0];
+#pragma unroll
+      for (int k = 1; k < NG; ++k) id = g == k ? ids[k] : id;
+      if (id >= 0) {
+        const int64_t from =
+            (((int64_t)id * c.n_heads + head) * c.block + ((int64_t)(tile * NG + g) * GROUP) % c.block) * D + (at % (2 * D)) * 16;
+        rawk[i] = *reinterpret_cast<const u32x4*>(c.k + from);
+        rawv[i] = *reinterpret_cast<const u32x4*>(c.v + from);
+      }
+    }
+  };
+  auto stage = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int at = tid + i * THREADS;
+      // keys: token t of the tile goes to row t with bits 2 and 3 exchanged
+      const int t = at / (D / 16), piece = at % (D / 16) * 2;
+      const int to = (t & ~12) | ((t & 4) << 1) | ((t & 8) >> 1);
+      uint8_t* kr = lds_k[buf] + to * (2 * D);
+      *reinterpret_cast<h16x8*>(kr + (piece ^ (to & 7)) * 16) = codes8(rawk[i][0], rawk[i][1]);
+      *reinterpret_cast<h16x8*>(kr + ((piece + 1) ^ (to & 7)) * 16) = codes8(rawk[i][2], rawk[i][3]);
+      // values: eight tokens of a channel, by group, eight, channel
+      const int g = at / (2 * D), pair = at % (2 * D) / 4, eight = at % 4;
+      uint8_t* vr = lds_v[buf] + (g * 4 + eight) * (D * 16);
+      *reinterpret_cast<h16x8*>(vr + ((2 * pair) ^ (2 * eight)) * 16) = codes8(rawv[i][0], rawv[i][1]);
+      *reinterpret_cast<h16x8*>(vr + ((2 * pair + 1) ^ (2 * eight)) * 16) = codes8(rawv[i][2], rawv[i][3]);
+    }
+  };
+
+  float kd[NG], vd[NG];
+  bool have[NG];
+  auto take = [&]() {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      kd[g] = kd_in[g];
+      vd[g] = vd_in[g];
+      have[g] = have_in[g];
+    }
+  };
+
+  look_up(tile0);
+  fetch(tile0);
+  look_up(tile0 + 1);
+  stage(0);
+  take();
+  fetch(tile0 + 1);
+  look_up(tile0 + 2);
+  __syncthreads();
+  for (int tile = tile0; tile < tile_end; ++tile) {
+    const int buf = (tile - tile0) & 1;
+    float kd_now[NG], vd_now[NG];
+    bool have_now[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      kd_now[g] = kd[g];
+      vd_now[g] = vd[g];
+      have_now[g] = have[g];
+    }
+    if (tile + 1 < tile_end) {
+      stage(buf ^ 1);
+      take();
+      fetch(tile + 2);
+      look_up(tile + 3);
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int64_t t0 = (int64_t)(tile * NG + g) * GROUP;
+      if (!have_now[g] || t0 > any_to || t0 + GROUP - 1 < any_from) continue;
+      f32x16 s = {};
+      const int krow = g * GROUP + li;
+      const uint8_t* kr = lds_k[buf] + krow * (2 * D);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const h16x8 ka = *reinterpret_cast<const h16x8*>(kr + ((2 * k + lh) ^ (krow & 7)) * 16);
+        s = __builtin_amdgcn_mfma_f32_32x32x16_f16(ka, qhi[k], s, 0, 0, 0);
+        if (F32) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(ka, qlo[k], s, 0, 0, 0);
+      }
+      // s[i]: token t0 + 16 (i / 8) + 8 lh + i % 8 of this lane's row
+      const bool clear = t0 >= clear_from && t0 + GROUP - 1 <= clear_to;
+      bool seen_any = true;
+      uint32_t seen = 0xffffu;
+      float top = NEG_INF;
+      if (clear) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[i]);
+      } else {
+        seen = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int64_t j = t0 + 16 * (i >> 3) + 8 * lh + (i & 7);
+          if (j <= pos && j > low) {
+            seen |= 1u << i;
+            top = __builtin_fmaxf(top, s[i]);
+          }
+        }
+        const uint32_t other = (uint32_t)__shfl_xor((int)seen, 32);
+        seen_any = (seen | other) != 0;
+      }
+      top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+      const float f = row_scale * kd_now[g];
+      top = seen_any ? top * f : NEG_INF;
+      if (__any(top > m_run + P_LAZY)) {
+        const float m_new = __builtin_fmaxf(m_run, top);
+        const float alpha = __builtin_amdgcn_exp2f(m_run - (m_new == NEG_INF ? 0.0f : m_new));
+        m_run = m_new;
+        l_run *= alpha;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) acc[d] *= alpha;
+      }
+      const ValueScale vs = value_scale(vd_now[g]);
+      if (__any(seen_any && vs.e > e_ref)) {
+        const int e_new = seen_any && vs.e > e_ref ? vs.e : e_ref;
+        const float down = __builtin_ldexpf(1.0f, e_ref - e_new);
+        e_ref = e_new;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) acc[d] *= down;
+      }
+      int de = vs.e - e_ref;
+      de = de < -100 ? -100 : de > 0 ? 0 : de;
+      const float ref = (m_run == NEG_INF ? 0.0f : m_run) - P_SHIFT;
+      const float off = ((float)de + vs.lm) - ref;
+      float sum = 0.0f;
+      h16x8 phi[2], plo[2];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], f, off));
+        if (!clear && !((seen >> i) & 1)) p = 0.0f;
+        sum += p;
+        phi[i >> 3][i & 7] = (_Float16)p;
+        if (F32) plo[i >> 3][i & 7] = (_Float16)(p - (float)phi[i >> 3][i & 7]);
+      }
+      l_run = __builtin_fmaf(sum, __builtin_ldexpf(vs.inv, -de), l_run);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int eight = 2 * j + lh;
+        const uint8_t* vr = lds_v[buf] + (g * 4 + eight) * (D * 16);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const h16x8 va = *reinterpret_cast<const h16x8*>(vr + ((32 * d + li) ^ (2 * eight)) * 16);
+          acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(va, phi[j], acc[d], 0, 0, 0);
+          if (F32) acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(va, plo[j], acc[d], 0, 0, 0);
+        }
+      }
+    }
+    __syncthreads();
+  }
+  l_run += __shfl_xor(l_run, 32);
+  if (32 * wave + li >= rows) return;
+  // lane (li, lh) holds channels 32 d + 8 (i / 4) + 4 lh + i % 4 of its row. A
+  // row that met no scale above zero keeps e_ref == E_NONE: zeros
+  if (vis.used <= 1) {
+    const float norm = l_run == 0.0f ? 0.0f : 1.0f / l_run;
+    const int64_t at = (int64_t)tok * a.out_stride + (int64_t)qh * D + 4 * lh;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const int64_t to = at + 32 * d + 2 * i;
+        float o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = __builtin_ldexpf(acc[d][i + k] * norm, e_ref);
+        if (SRC == QR_BF16)
+          *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + to) =
+              u32x2{(uint32_t)bf16_bits(o[0]) | (uint32_t)bf16_bits(o[1]) << 16,
+                    (uint32_t)bf16_bits(o[2]) | (uint32_t)bf16_bits(o[3]) << 16};
+        else
+          *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.out) + to) = f32x4{o[0], o[1], o[2], o[3]};
+      }
+  } else {
+    float* part = a.part + (((int64_t)blockIdx.x * c.n_heads + head) * a.n_splits + split) * P_ROWS * (D + 2);
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<f32x4*>(part + row * D + 32 * d + 2 * i + 4 * lh) =
+            f32x4{__builtin_ldexpf(acc[d][i], e_ref), __builtin_ldexpf(acc[d][i + 1], e_ref),
+                  __builtin_ldexpf(acc[d][i + 2], e_ref), __builtin_ldexpf(acc[d][i + 3], e_ref)};
+    if (lh == 0) {
+      part[P_ROWS * D + row] = m_run;
+      part[P_ROWS * D + P_ROWS + row] = l_run;
+    }
+  }
+}
+
+// Joins the splits of a unit of UNIT rows; a wave takes a row at a time. Lane
+// z works out the factor of split z (and z + 64); then every lane adds its
+// channels over the splits, whose loads do not wait for each other.
+constexpr int J_WAVES = 4;
+constexpr int J_BATCH = 32;
+constexpr int MAX_SPLITS = 128;
+
+template <int SRC, int D, int UNIT, int NG>
+__global__ __launch_bounds__(J_WAVES * WAVE) void k_attention_join(Cache c, Batch b, Attention a) {
+  constexpr int PER = D / WAVE;   // channels of a lane
+  typedef float f32xp __attribute__((ext_vector_type(PER == 1 ? 2 : PER)));
+  Span sp;
+  const int u = find_unit(b, blockIdx.x, a.group, UNIT, 1, sp);
+  const int64_t n_rows = (int64_t)sp.n * a.group;
+  const int64_t first_row = (int64_t)u * UNIT;
+  if (u < 0 || first_row >= n_rows) return;
+  const int rows = (int)(n_rows - first_row < UNIT ? n_rows - first_row : UNIT);
+  const Range vis = visible(sp, (int)first_row, rows, a, b.table_width * c.block, NG);
   if (vis.used <= 1) return;
-  const int head = blockIdx.y;
-  const float* part = a.part + ((int64_t)blockIdx.x * c.n_heads + head) * a.n_splits * A_ROWS * (D + 2);
-  for (int e = threadIdx.x; e < rows * D; e += 256) {
-    const int row = e / D, ch = e % D;
-    float m = NEG_INF;
-    for (int z = 0; z < vis.used; ++z) m = __builtin_fmaxf(m, part[z * A_ROWS * (D + 2) + A_ROWS * D + row]);
+  const int head = blockIdx.y, lane = threadIdx.x & 63;
+  constexpr int64_t STEP = (int64_t)UNIT * (D + 2);
+  const float* part = a.part + ((int64_t)blockIdx.x * c.n_heads + head) * a.n_splits * STEP;
+  for (int row = threadIdx.x / WAVE + J_WAVES * (int)blockIdx.z; row < rows; row += J_WAVES * (int)gridDim.z) {
+    float f[2], l = 0.0f, m = NEG_INF;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int z = lane + i * WAVE;
+      f[i] = z < vis.used ? part[z * STEP + UNIT * D + row] : NEG_INF;
+      m = __builtin_fmaxf(m, f[i]);
+    }
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, s));
     const float ref = m == NEG_INF ? 0.0f : m;
-    float o = 0.0f, l = 0.0f;
-    for (int z = 0; z < vis.used; ++z) {
-      const float* pz = part + z * A_ROWS * (D + 2);
-      const float f = __builtin_amdgcn_exp2f(pz[A_ROWS * D + row] - ref);
-      o = __builtin_fmaf(pz[row * D + ch], f, o);
-      l = __builtin_fmaf(pz[A_ROWS * D + A_ROWS + row], f, l);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int z = lane + i * WAVE;
+      f[i] = __builtin_amdgcn_exp2f(f[i] - ref);
+      if (z < vis.used) l = __builtin_fmaf(part[z * STEP + UNIT * D + UNIT + row], f[i], l);
+    }
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) l += __shfl_xor(l, s);
+    float o[PER] = {};
+    for (int z0 = 0; z0 < vis.used; z0 += J_BATCH) {
+      f32xp v[J_BATCH];
+#pragma unroll
+      for (int k = 0; k < J_BATCH; ++k) {
+        const int z = z0 + k < vis.used ? z0 + k : vis.used - 1;
+        const float* pz = part + z * STEP + row * D + lane * PER;
+        if (PER == 1) v[k][0] = pz[0];
+        else v[k] = *reinterpret_cast<const f32xp*>(pz);
+      }
+#pragma unroll
+      for (int k = 0; k < J_BATCH; ++k) {
+        const int z = z0 + k;
+        const float fz = __builtin_bit_cast(
+            float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, z < WAVE ? f[0] : f[1]), z & (WAVE - 1)));
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (z < vis.used) o[i] = __builtin_fmaf(v[k][i], fz, o[i]);
+      }
     }
     const int rr = (int)first_row + row;
-    const int64_t at = (int64_t)(sp.row0 + rr / a.group) * a.out_stride + (int64_t)(head * a.group + rr % a.group) * D + ch;
-    store_at<SRC>(a.out, at, l == 0.0f ? 0.0f : o / l);
+    const int64_t at = (int64_t)(sp.row0 + rr / a.group) * a.out_stride + (int64_t)(head * a.group + rr % a.group) * D + lane * PER;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) store_at<SRC>(a.out, at + k, l == 0.0f ? 0.0f : o[k] / l);
   }
 }
 
@@ -596,28 +1022,43 @@ Cache device_cache(const qr_kv8* c) {
 // Units of a call that takes one piece of a block at a time.
 int64_t piece_units(const qr_kv8* c, int64_t n_tok, int64_t n_seq) { return n_tok / c->block_tokens + 2 * n_seq; }
 
-int64_t row_units(int64_t n_tok, int64_t n_seq, int64_t group) { return n_tok * group / A_ROWS + n_seq; }
+// How a call of attention is cut: units of 16 or 128 rows, and splits of the
+// tokens where that leaves CUs without work.
+struct Cut {
+  bool many;        // the kernel for many rows
+  int64_t units, splits;
+};
 
-// Splits of the tokens, so that a few sequences still fill 256 CUs: about
-// four workgroups per CU, none for less than A_MIN_GROUPS groups.
-int64_t splits(const qr_kv8* c, int64_t n_tok, int64_t n_seq, int64_t group, int64_t table_width) {
-  const int64_t rows = (n_tok * group + n_seq - 1) / n_seq;
-  const int64_t busy = n_seq * ((rows + A_ROWS - 1) / A_ROWS) * c->n_heads;
+Cut cut_for(const qr_kv8* c, int64_t n_tok, int64_t n_seq, int64_t group, int64_t table_width) {
+  Cut k;
+  const int64_t rows = (n_tok * group + n_seq - 1) / n_seq;   // of a sequence, on average
+  k.many = rows > 48;
+  const int64_t unit = k.many ? P_ROWS : A_ROWS;
+  k.units = n_tok * group / unit + n_seq;
+  const int64_t busy = n_seq * ((rows + unit - 1) / unit) * c->n_heads;
   const int64_t most = (table_width * (c->block_tokens / GROUP) + A_MIN_GROUPS - 1) / A_MIN_GROUPS;
-  int64_t z = (1024 + busy - 1) / busy;
-  if (z > most) z = most;
-  if (z > 128) z = 128;
-  return z < 1 ? 1 : z;
+  const int64_t want = k.many ? 512 : 1024;   // workgroups: two, four per CU
+  k.splits = (want + busy - 1) / busy;
+  if (k.splits > most) k.splits = most;
+  if (k.splits > MAX_SPLITS) k.splits = MAX_SPLITS;
+  if (k.splits < 1) k.splits = 1;
+  return k;
 }
 
 template <int SRC, int D>
-int launch_attention(const Cache& c, const Batch& b, const Attention& a, uint32_t units, hipStream_t s) {
+int launch_attention(const Cache& c, const Batch& b, const Attention& a, const Cut& k, hipStream_t s) {
+  constexpr int NG = D == 256 ? 1 : 2;   // what two LDS buffers hold in 64 KB
+  const uint32_t units = (uint32_t)k.units;
   const dim3 grid(units, (uint32_t)c.n_heads, (uint32_t)a.n_splits);
-  hipLaunchKernelGGL((k_attention_kv8<SRC, D>), grid, dim3(A_WAVES * WAVE), 0, s, c, b, a);
+  if (k.many) hipLaunchKernelGGL((k_attention_kv8_rows<SRC, D, NG>), grid, dim3(P_WAVES * WAVE), 0, s, c, b, a);
+  else hipLaunchKernelGGL((k_attention_kv8<SRC, D>), grid, dim3(A_WAVES * WAVE), 0, s, c, b, a);
   if (a.n_splits > 1) {
     const int rc = qr_check_launch("k_attention_kv8");
     if (rc != QR_OK) return rc;
-    hipLaunchKernelGGL((k_attention_join<SRC, D>), dim3(units, (uint32_t)c.n_heads), dim3(256), 0, s, c, b, a);
+    if (k.many)
+      hipLaunchKernelGGL((k_attention_join<SRC, D, P_ROWS, NG>), dim3(units, (uint32_t)c.n_heads, 8), dim3(J_WAVES * WAVE), 0, s, c, b, a);
+    else
+      hipLaunchKernelGGL((k_attention_join<SRC, D, A_ROWS, 1>), dim3(units, (uint32_t)c.n_heads), dim3(J_WAVES * WAVE), 0, s, c, b, a);
   }
   return qr_check_launch("k_attention_kv8");
 }
@@ -711,9 +1152,9 @@ size_t qr_attention_kv8_workspace_bytes(const qr_kv8* c, int64_t n_q_heads, int6
       n_tok * n_q_heads > INT32_MAX)
     return 0;
   const int64_t group = n_q_heads / c->n_heads;
-  const int64_t z = splits(c, n_tok, n_seq, group, table_width);
-  if (z == 1) return 0;
-  return (size_t)(row_units(n_tok, n_seq, group) * c->n_heads * z * A_ROWS * (c->head_dim + 2)) * sizeof(float);
+  const Cut k = cut_for(c, n_tok, n_seq, group, table_width);
+  if (k.splits == 1) return 0;
+  return (size_t)(k.units * c->n_heads * k.splits * (k.many ? P_ROWS : A_ROWS) * (c->head_dim + 2)) * sizeof(float);
 }
 
 int qr_attention_kv8(const qr_kv8* c, int src, const void* q, int64_t q_stride, int64_t n_q_heads, int64_t n_tok,
@@ -736,8 +1177,8 @@ int qr_attention_kv8(const qr_kv8* c, int src, const void* q, int64_t q_stride, 
   if (!q || !out || !qr_aligned(q, 16) || !qr_aligned(out, 16))
     return qr_fail(QR_EINVAL_PTR, "q and out must be non-NULL and 16-byte aligned");
   const int64_t group = n_q_heads / c->n_heads;
-  const int64_t units = row_units(n_tok, n_seq, group);
-  if (units > UINT32_MAX / 256) return qr_fail(QR_EOVERFLOW, "n_tok and n_seq need too many workgroups for one launch");
+  const Cut cut = cut_for(c, n_tok, n_seq, group, table_width);
+  if (cut.units > UINT32_MAX / 256) return qr_fail(QR_EOVERFLOW, "n_tok and n_seq need too many workgroups for one launch");
   const size_t need = qr_attention_kv8_workspace_bytes(c, n_q_heads, n_tok, n_seq, table_width);
   if (need > 0 && (!workspace || !qr_aligned(workspace, 256)))
     return qr_fail(QR_EINVAL_PTR, "workspace must be non-NULL and 256-byte aligned");
@@ -746,13 +1187,12 @@ int qr_attention_kv8(const qr_kv8* c, int src, const void* q, int64_t q_stride, 
   const Cache cc = device_cache(c);
   const Batch b = {cu, kv_len, table, table_width, (int)n_seq, (int)n_tok};
   const Attention a = {q, out, reinterpret_cast<float*>(workspace), q_stride, out_stride, scale * 1.44269504088896340736f,
-                       window < (int64_t)1 << 32 ? window : (int64_t)1 << 32, (int)group, (int)splits(c, n_tok, n_seq, group, table_width)};
+                       window < (int64_t)1 << 32 ? window : (int64_t)1 << 32, (int)group, (int)cut.splits};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const uint32_t n = (uint32_t)units;
   switch (c->head_dim) {
-    case 64: return src == QR_BF16 ? launch_attention<QR_BF16, 64>(cc, b, a, n, s) : launch_attention<QR_F32, 64>(cc, b, a, n, s);
-    case 128: return src == QR_BF16 ? launch_attention<QR_BF16, 128>(cc, b, a, n, s) : launch_attention<QR_F32, 128>(cc, b, a, n, s);
-    default: return src == QR_BF16 ? launch_attention<QR_BF16, 256>(cc, b, a, n, s) : launch_attention<QR_F32, 256>(cc, b, a, n, s);
+    case 64: return src == QR_BF16 ? launch_attention<QR_BF16, 64>(cc, b, a, cut, s) : launch_attention<QR_F32, 64>(cc, b, a, cut, s);
+    case 128: return src == QR_BF16 ? launch_attention<QR_BF16, 128>(cc, b, a, cut, s) : launch_attention<QR_F32, 128>(cc, b, a, cut, s);
+    default: return src == QR_BF16 ? launch_attention<QR_BF16, 256>(cc, b, a, cut, s) : launch_attention<QR_F32, 256>(cc, b, a, cut, s);
   }
 }
 
