@@ -44,8 +44,7 @@ struct Batch {
   const int32_t* cu;
   const int32_t* kv_len;
   const int32_t* table;
-  int64_t table_width;
-  int n_seq, n_tok;
+  int table_width, n_seq, n_tok;
 };
 
 struct Cache {
@@ -53,7 +52,7 @@ struct Cache {
   int8_t* v;
   float* kd;
   float* vd;
-  int n_blocks, n_heads, block;   // block: tokens per block
+  int n_blocks, n_heads, shift;   // 2^shift tokens per block
 };
 
 // A sequence's rows and tokens. Rows [row0, row0 + n) of the call are the
@@ -65,17 +64,17 @@ struct Span {
 __device__ __forceinline__ int clamp_row(const Batch& b, int r) { return r < 0 ? 0 : r > b.n_tok ? b.n_tok : r; }
 
 // Which sequence a unit of work belongs to, without a table of units on the
-// host: sequence s gets the units from floor(cu[s] * mul / div) + s * pad on,
-// which leaves every sequence room for ceil(rows * mul / div) + pad - 1 units
+// host: sequence s gets the units from floor(cu[s] * mul / 2^shift) + s * pad on,
+// which leaves every sequence room for ceil(rows * mul / 2^shift) + pad - 1 units
 // or more. A whole wave asks together: its lanes look at 64 sequences at once.
 // Returns the unit's number within its sequence.
-__device__ __forceinline__ int find_unit(const Batch& b, int64_t unit, int64_t mul, int64_t div, int pad, Span& sp) {
+__device__ __forceinline__ int find_unit(const Batch& b, int64_t unit, int64_t mul, int shift, int pad, Span& sp) {
   const int lane = threadIdx.x & (WAVE - 1);
   int seq = -1;
   for (int base = 0; base < b.n_seq; base += WAVE) {
     bool begun = false;
     if (base + lane < b.n_seq)
-      begun = (int64_t)clamp_row(b, b.cu[base + lane]) * mul / div + (int64_t)(base + lane) * pad <= unit;
+      begun = ((int64_t)clamp_row(b, b.cu[base + lane]) * mul >> shift) + (int64_t)(base + lane) * pad <= unit;
     const uint64_t m = __ballot(begun);
     if (m != 0) seq = base + 63 - __builtin_clzll(m);
     if (m != ~0ull) break;
@@ -86,14 +85,14 @@ __device__ __forceinline__ int find_unit(const Batch& b, int64_t unit, int64_t m
   sp.n = clamp_row(b, b.cu[sp.seq + 1]) - sp.row0;
   sp.len = b.kv_len[sp.seq];
   if (seq < 0 || sp.n < 0) sp.n = 0;
-  return (int)(unit - ((int64_t)sp.row0 * mul / div + (int64_t)sp.seq * pad));
+  return (int)(unit - (((int64_t)sp.row0 * mul >> shift) + (int64_t)sp.seq * pad));
 }
 
-// The block that holds a sequence's tokens slot * block .., or -1.
-__device__ __forceinline__ int block_of(const Batch& b, const Cache& c, int seq, int64_t slot) {
-  if (slot < 0 || slot >= b.table_width) return -1;
-  const int id = b.table[(int64_t)seq * b.table_width + slot];
-  return id >= 0 && id < c.n_blocks ? id : -1;
+// The block in slot `slot` of a sequence's row of the table, or -1.
+__device__ __forceinline__ int block_of(const int32_t* row, int width, int n_blocks, int slot) {
+  if (slot < 0 || slot >= width) return -1;
+  const int id = row[slot];
+  return id >= 0 && id < n_blocks ? id : -1;
 }
 
 // Byte of channel d of token t in its V block.
@@ -115,16 +114,17 @@ struct Piece {
 
 __device__ __forceinline__ Piece find_piece(const Batch& b, const Cache& c, int64_t unit) {
   Span sp;
-  const int u = find_unit(b, unit, 1, c.block, 2, sp);
+  const int u = find_unit(b, unit, 1, c.shift, 2, sp);
   Piece p = {-1, 0, 0, 0};
   const int64_t first = (int64_t)sp.len - sp.n;         // position of the first row, may be negative
   const int64_t from = first < 0 ? 0 : first;
-  const int64_t slot = from / c.block + u;
-  const int64_t lo = slot * c.block;
+  const int64_t slot = (from >> c.shift) + u;
+  const int64_t lo = slot << c.shift;
   if (u < 0 || sp.n == 0 || lo >= sp.len) return p;
-  p.id = block_of(b, c, sp.seq, slot);
+  p.id = slot < b.table_width ? block_of(b.table + (int64_t)sp.seq * b.table_width, b.table_width, c.n_blocks, (int)slot) : -1;
   p.t0 = (int)(from > lo ? from - lo : 0);
-  p.t1 = (int)(sp.len - lo < c.block ? sp.len - lo : c.block);
+  const int block = 1 << c.shift;
+  p.t1 = (int)(sp.len - lo < block ? sp.len - lo : block);
   p.row = (int)(sp.row0 + (lo + p.t0 - first));
   return p;
 }
@@ -172,7 +172,7 @@ __global__ __launch_bounds__(RW_THREADS) void k_kv8_append(Cache c, Batch b, con
   const float ratio = grown ? old / d : 1.0f;
   if (tid == 0) *scale = d;
 
-  int8_t* codes = (values ? c.v : c.k) + at * c.block * D;
+  int8_t* codes = (values ? c.v : c.k) + (at << c.shift) * D;
   // eight codes at a time: of one token for keys, of one channel for values
   const int first8 = grown ? 0 : p.t0;
   if (!values) {
@@ -230,7 +230,7 @@ __global__ __launch_bounds__(RW_THREADS) void k_kv8_read(Cache c, Batch b, void*
   if (p.t1 > p.t0) {
     const int64_t at = (int64_t)p.id * c.n_heads + head;
     const float d = p.id < 0 ? 0.0f : (values ? c.vd : c.kd)[at];
-    const int8_t* codes = (values ? c.v : c.k) + at * c.block * D;
+    const int8_t* codes = (values ? c.v : c.k) + (at << c.shift) * D;
     for (int e = tid; e < (p.t1 - p.t0) * D; e += RW_THREADS) {
       const int t = p.t0 + e / D, ch = e % D;
       float f = 0.0f;
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(RW_THREADS) void k_kv8_read(Cache c, Batch b, void*
   }
   // rows before position 0: the sequence's first unit clears them
   Span sp;
-  if (find_unit(b, blockIdx.x, 1, c.block, 2, sp) == 0 && sp.len < sp.n) {
+  if (find_unit(b, blockIdx.x, 1, c.shift, 2, sp) == 0 && sp.len < sp.n) {
     const int64_t lost = sp.len < 0 ? sp.n : (int64_t)sp.n - sp.len;
     for (int64_t e = tid; e < lost * D; e += RW_THREADS)
       store_at<DST>(x, (sp.row0 + e / D) * stride + (int64_t)head * D + e % D, 0.0f);
@@ -284,7 +284,7 @@ struct Attention {
   int n_splits;
 };
 
-constexpr int A_ROWS = 16;       // rows of a unit
+constexpr int A_SHIFT = 4, A_ROWS = 1 << A_SHIFT;   // rows of a unit
 constexpr int A_WAVES = 4;
 constexpr int A_MIN_GROUPS = 8;  // token groups a split is worth (both kernels)
 constexpr float NEG_INF = -__builtin_inff();
@@ -349,12 +349,12 @@ __global__ __launch_bounds__(A_WAVES * WAVE) void k_attention_kv8(Cache c, Batch
   const int head = blockIdx.y, split = blockIdx.z;
 
   Span sp;
-  const int u = find_unit(b, blockIdx.x, a.group, A_ROWS, 1, sp);
+  const int u = find_unit(b, blockIdx.x, a.group, A_SHIFT, 1, sp);
   const int64_t n_rows = (int64_t)sp.n * a.group;
   const int64_t first_row = (int64_t)u * A_ROWS;
   if (u < 0 || first_row >= n_rows) return;
   const int rows = (int)(n_rows - first_row < A_ROWS ? n_rows - first_row : A_ROWS);
-  const int64_t limit = b.table_width * c.block;
+  const int64_t limit = (int64_t)b.table_width << c.shift;
   const Range vis = visible(sp, (int)first_row, rows, a, limit, 1);
   if (split > 0 && split >= vis.used) return;
 
@@ -406,11 +406,12 @@ __global__ __launch_bounds__(A_WAVES * WAVE) void k_attention_kv8(Cache c, Batch
 
   // Blocks and scales of the wave's next 64 groups, one per lane; the codes of
   // the next group are loaded while this one's are multiplied.
+  const int32_t* table_row = b.table + (int64_t)sp.seq * b.table_width;
   int ids = -1;
   float kds = 0.0f, vds = 0.0f;
   auto look_ahead = [&](int g) {
     const int mine = g + lane * A_WAVES;
-    ids = mine < end ? block_of(b, c, sp.seq, (int64_t)mine * GROUP / c.block) : -1;
+    ids = mine < end ? block_of(table_row, b.table_width, c.n_blocks, mine >> (c.shift - 5)) : -1;
     if (ids >= 0) {
       kds = c.kd[(int64_t)ids * c.n_heads + head];
       vds = c.vd[(int64_t)ids * c.n_heads + head];
@@ -426,7 +427,7 @@ __global__ __launch_bounds__(A_WAVES * WAVE) void k_attention_kv8(Cache c, Batch
   };
   auto load = [&](int g) {
     if (id < 0) return;
-    const int64_t at = ((int64_t)id * c.n_heads + head) * c.block + ((int64_t)g * GROUP) % c.block;
+    const int64_t at = (((int64_t)id * c.n_heads + head) << c.shift) + (g * GROUP & ((1 << c.shift) - 1));
     const int8_t* kp = c.k + at * D;
     const int8_t* vp = c.v + at * D;
 #pragma unroll
@@ -582,7 +583,7 @@ __global__ __launch_bounds__(A_WAVES * WAVE) void k_attention_kv8(Cache c, Batch
 // ---------------------------------------------------------------------------
 // attention of many rows
 
-constexpr int P_ROWS = 128;      // rows of a unit: 32 per wave
+constexpr int P_SHIFT_ROWS = 7, P_ROWS = 1 << P_SHIFT_ROWS;   // rows of a unit: 32 per wave
 constexpr int P_WAVES = 4;
 constexpr float P_LAZY = 5.0f;   // how far scores may pass the reference maximum
 
@@ -595,6 +596,30 @@ struct ValueScale {
 };
 
 constexpr int E_NONE = -100000;
+
+template <int V>
+struct Index {
+  static constexpr int value = V;
+};
+
+// Where a 16-byte piece lies in LDS: piece p of K row r at p ^ k_swizzle(r),
+// channel d of the V tokens 8 e .. at d ^ v_swizzle(e). Sixteen lanes that read
+// or write side by side then meet sixteen different pieces of 256 bytes.
+template <int D>
+__device__ __forceinline__ int k_swizzle(int r) { return D == 64 ? (r >> 1) & 7 : r & 15; }
+__device__ __forceinline__ int v_swizzle(int e) { return (e & 1) << 3 | e >> 1; }
+
+// A float of one lane, for all.
+__device__ __forceinline__ float lane_value(float x, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
+
+// The value that the lane 32 further (or nearer) holds.
+__device__ __forceinline__ float other_half(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_bit_cast(float, (threadIdx.x & 32) ? r[0] : r[1]);
+}
 
 __device__ __forceinline__ ValueScale value_scale(float vd) {
   ValueScale v;
@@ -631,17 +656,17 @@ __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 
   static_assert(CH >= 1 && TOK * D / 16 % THREADS == 0, "whole pieces");
   __shared__ __attribute__((aligned(16))) uint8_t lds_k[2][TOK * D * 2];
   __shared__ __attribute__((aligned(16))) uint8_t lds_v[2][TOK * D * 2];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 31, lh = lane >> 5;
   const int head = blockIdx.y, split = blockIdx.z;
 
   Span sp;
-  const int u = find_unit(b, blockIdx.x, a.group, P_ROWS, 1, sp);
+  const int u = find_unit(b, gridDim.x - 1 - blockIdx.x, a.group, P_SHIFT_ROWS, 1, sp);
   const int64_t n_rows = (int64_t)sp.n * a.group;
   const int64_t first_row = (int64_t)u * P_ROWS;
   if (u < 0 || first_row >= n_rows) return;
   const int rows = (int)(n_rows - first_row < P_ROWS ? n_rows - first_row : P_ROWS);
-  const Range vis = visible(sp, (int)first_row, rows, a, b.table_width * c.block, NG);
+  const Range vis = visible(sp, (int)first_row, rows, a, (int64_t)b.table_width << c.shift, NG);
   if (split > 0 && split >= vis.used) return;
 
   // this lane's row; a wave behind the last row repeats it
@@ -651,14 +676,15 @@ __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 
   const int r = (int)first_row + row;
   const int tok = sp.row0 + r / a.group;
   const int qh = head * a.group + r % a.group;
-  const int64_t base = (int64_t)sp.len - sp.n;
-  const int64_t pos = base + r / a.group;
-  const int64_t low = a.window > 0 ? pos - a.window : -1;
+  // positions fit 32 bits: they are below kv_len
+  const int base = (int)((int64_t)sp.len - sp.n < INT32_MIN ? INT32_MIN : (int64_t)sp.len - sp.n);
+  const int pos = base + r / a.group;
+  auto window_of = [&](int p) { return a.window > 0 && (int64_t)p - a.window >= 0 ? (int)(p - a.window) : -1; };
+  const int low = window_of(pos);   // the row sees low + 1 .. pos
   // all rows of the wave see the tokens clear_from .. clear_to, none sees any
   // outside any_from .. any_to
-  const int64_t clear_to = base + (first_row + wrow) / a.group, any_to = base + (first_row + wlast) / a.group;
-  const int64_t clear_from = a.window > 0 ? any_to - a.window + 1 : 0;
-  const int64_t any_from = a.window > 0 ? clear_to - a.window + 1 : 0;
+  const int clear_to = base + ((int)first_row + wrow) / a.group, any_to = base + ((int)first_row + wlast) / a.group;
+  const int clear_from = window_of(any_to) + 1, any_from = window_of(clear_to) + 1;
 
   h16x8 qhi[KS], qlo[F32 ? KS : 1];
   float row_scale;
@@ -701,37 +727,36 @@ __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 
   const int tile0 = vis.g0 / NG + split * vis.per;
   const int tile_end = vis.g0 / NG + (vis.n < (split + 1) * vis.per ? vis.n : (split + 1) * vis.per);
 
-  // what is on its way: blocks of the tile after the staged one, codes and
-  // scales of the staged one
-  int ids[NG];
-  u32x4 rawk[CH] = {}, rawv[CH] = {};
-  float kd_in[NG], vd_in[NG];
-  bool have_in[NG];
+  // Blocks and scales of 64 groups from first_known on, one group per lane:
+  // looked up once for many tiles, and read from the lane that holds them.
+  const int32_t* table_row = b.table + (int64_t)sp.seq * b.table_width;
+  int first_known, ids;
+  float kds;
+  ValueScale vds;
   auto look_up = [&](int tile) {
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-      ids[g] = tile < tile_end ? __builtin_amdgcn_readfirstlane(block_of(b, c, sp.seq, (int64_t)(tile * NG + g) * GROUP / c.block)) : -1;
-  };
-  auto fetch = [&](int tile) {
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const int64_t at = (int64_t)(ids[g] < 0 ? 0 : ids[g]) * c.n_heads + head;
-      have_in[g] = ids[g] >= 0;
-      kd_in[g] = have_in[g] ? c.kd[at] : 0.0f;
-      vd_in[g] = have_in[g] ? c.vd[at] : 0.0f;
+    first_known = tile * NG;
+    const int g = first_known + lane;
+    ids = g < tile_end * NG ? block_of(table_row, b.table_width, c.n_blocks, g >> (c.shift - 5)) : -1;
+    float vd = 0.0f;
+    kds = 0.0f;
+    if (ids >= 0) {
+      const int64_t at = (int64_t)ids * c.n_heads + head;
+      kds = c.kd[at];
+      vd = c.vd[at];
     }
+    vds = value_scale(vd);
+  };
+  u32x4 rawk[CH] = {}, rawv[CH] = {};
+  auto fetch = [&](int tile) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int at = tid + i * THREADS;
-      const int g = __builtin_amdgcn_readfirstlane(at / (2 * D));   // group: 2 D pieces each
-      int id = ids[0];
-#pragma unroll
-      for (int k = 1; k < NG; ++k) id = g == k ? ids[k] : id;
+      const int g = tile * NG + __builtin_amdgcn_readfirstlane(at / (2 * D));   // group: 2 D pieces each
+      const int id = __builtin_amdgcn_readlane(ids, g - first_known);
       if (id >= 0) {
-        const int64_t from =
-            (((int64_t)id * c.n_heads + head) * c.block + ((int64_t)(tile * NG + g) * GROUP) % c.block) * D + (at % (2 * D)) * 16;
-        rawk[i] = *reinterpret_cast<const u32x4*>(c.k + from);
-        rawv[i] = *reinterpret_cast<const u32x4*>(c.v + from);
+        const int64_t from = ((((int64_t)id * c.n_heads + head) << c.shift) + (g * GROUP & ((1 << c.shift) - 1))) * D;
+        rawk[i] = *reinterpret_cast<const u32x4*>(c.k + from + (at % (2 * D)) * 16);
+        rawv[i] = *reinterpret_cast<const u32x4*>(c.v + from + (at % (2 * D)) * 16);
       }
     }
   };
@@ -743,132 +768,133 @@ __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 
       const int t = at / (D / 16), piece = at % (D / 16) * 2;
       const int to = (t & ~12) | ((t & 4) << 1) | ((t & 8) >> 1);
       uint8_t* kr = lds_k[buf] + to * (2 * D);
-      *reinterpret_cast<h16x8*>(kr + (piece ^ (to & 7)) * 16) = codes8(rawk[i][0], rawk[i][1]);
-      *reinterpret_cast<h16x8*>(kr + ((piece + 1) ^ (to & 7)) * 16) = codes8(rawk[i][2], rawk[i][3]);
+      *reinterpret_cast<h16x8*>(kr + (piece ^ k_swizzle<D>(to)) * 16) = codes8(rawk[i][0], rawk[i][1]);
+      *reinterpret_cast<h16x8*>(kr + ((piece + 1) ^ k_swizzle<D>(to)) * 16) = codes8(rawk[i][2], rawk[i][3]);
       // values: eight tokens of a channel, by group, eight, channel
       const int g = at / (2 * D), pair = at % (2 * D) / 4, eight = at % 4;
       uint8_t* vr = lds_v[buf] + (g * 4 + eight) * (D * 16);
-      *reinterpret_cast<h16x8*>(vr + ((2 * pair) ^ (2 * eight)) * 16) = codes8(rawv[i][0], rawv[i][1]);
-      *reinterpret_cast<h16x8*>(vr + ((2 * pair + 1) ^ (2 * eight)) * 16) = codes8(rawv[i][2], rawv[i][3]);
-    }
-  };
-
-  float kd[NG], vd[NG];
-  bool have[NG];
-  auto take = [&]() {
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      kd[g] = kd_in[g];
-      vd[g] = vd_in[g];
-      have[g] = have_in[g];
+      *reinterpret_cast<h16x8*>(vr + ((2 * pair) ^ v_swizzle(eight)) * 16) = codes8(rawv[i][0], rawv[i][1]);
+      *reinterpret_cast<h16x8*>(vr + ((2 * pair + 1) ^ v_swizzle(eight)) * 16) = codes8(rawv[i][2], rawv[i][3]);
     }
   };
 
   look_up(tile0);
   fetch(tile0);
-  look_up(tile0 + 1);
   stage(0);
-  take();
   fetch(tile0 + 1);
-  look_up(tile0 + 2);
   __syncthreads();
-  for (int tile = tile0; tile < tile_end; ++tile) {
-    const int buf = (tile - tile0) & 1;
-    float kd_now[NG], vd_now[NG];
-    bool have_now[NG];
+  // One tile: the next one is staged into the other buffer, the one after
+  // that is asked for, and this one multiplied.
+  auto step = [&](int tile, auto buf_tag) {
+    constexpr int BUF = decltype(buf_tag)::value;
+    if ((tile + 3) * NG > first_known + WAVE) look_up(tile);
+    const int tile_t0 = tile * TOK;
+    const bool idle = tile_t0 > any_to || tile_t0 + TOK - 1 < any_from;
+    f32x16 s[NG];
+    if (!idle) {
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      kd_now[g] = kd[g];
-      vd_now[g] = vd[g];
-      have_now[g] = have[g];
-    }
-    if (tile + 1 < tile_end) {
-      stage(buf ^ 1);
-      take();
-      fetch(tile + 2);
-      look_up(tile + 3);
-    }
+      for (int g = 0; g < NG; ++g) {
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const int64_t t0 = (int64_t)(tile * NG + g) * GROUP;
-      if (!have_now[g] || t0 > any_to || t0 + GROUP - 1 < any_from) continue;
-      f32x16 s = {};
-      const int krow = g * GROUP + li;
-      const uint8_t* kr = lds_k[buf] + krow * (2 * D);
+        for (int i = 0; i < 16; ++i) s[g][i] = 0.0f;
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const h16x8 ka = *reinterpret_cast<const h16x8*>(kr + ((2 * k + lh) ^ (krow & 7)) * 16);
-        s = __builtin_amdgcn_mfma_f32_32x32x16_f16(ka, qhi[k], s, 0, 0, 0);
-        if (F32) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(ka, qlo[k], s, 0, 0, 0);
+        for (int k = 0; k < KS; ++k) {
+          const h16x8 ka = *reinterpret_cast<const h16x8*>(lds_k[BUF] + (g * GROUP + li) * (2 * D) +
+                                                           ((2 * k + lh) ^ k_swizzle<D>(li)) * 16);
+          s[g] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ka, qhi[k], s[g], 0, 0, 0);
+          if (F32) s[g] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ka, qlo[k], s[g], 0, 0, 0);
+        }
       }
-      // s[i]: token t0 + 16 (i / 8) + 8 lh + i % 8 of this lane's row
-      const bool clear = t0 >= clear_from && t0 + GROUP - 1 <= clear_to;
-      bool seen_any = true;
-      uint32_t seen = 0xffffu;
-      float top = NEG_INF;
-      if (clear) {
+    }
+    // converting the next tile keeps the vector unit busy meanwhile
+    if (tile + 1 < tile_end) {
+      stage(BUF ^ 1);
+      fetch(tile + 2);
+    }
+    if (idle) return;
+    // s[g][i]: token t0 + 16 (i / 8) + 8 lh + i % 8 of this lane's row
+    float f[NG], top = NEG_INF;
+    ValueScale vs[NG];
+    int e_top = e_ref;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[i]);
-      } else {
-        seen = 0;
+    for (int g = 0; g < NG; ++g) {
+      const int t0 = tile_t0 + g * GROUP;
+      // (a factor of zero becomes one that moves no score: -inf times it
+      // stays -inf)
+      const int from = tile * NG + g - first_known;
+      const bool have = __builtin_amdgcn_readlane(ids, from) >= 0;
+      f[g] = row_scale * lane_value(kds, from);
+      f[g] = f[g] < 1e-30f ? 1e-30f : f[g];
+      vs[g] = {__builtin_amdgcn_readlane(vds.e, from), lane_value(vds.lm, from), lane_value(vds.inv, from)};
+      bool seen_any = true;
+      if (!have || t0 < clear_from || t0 + GROUP - 1 > clear_to) {
+        // the row sees the group's tokens lo + 1 .. hi
+        const int hi = have && pos >= t0 ? pos - t0 : -1, lo = low >= t0 ? low - t0 : -1;
+        const int first = lo + 1 - 8 * lh;
+        const uint32_t count = hi > lo ? hi - lo : 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int64_t j = t0 + 16 * (i >> 3) + 8 * lh + (i & 7);
-          if (j <= pos && j > low) {
-            seen |= 1u << i;
-            top = __builtin_fmaxf(top, s[i]);
-          }
+          const int j = 16 * (i >> 3) + (i & 7);
+          s[g][i] = (uint32_t)(j - first) < count ? s[g][i] : NEG_INF;
         }
-        const uint32_t other = (uint32_t)__shfl_xor((int)seen, 32);
-        seen_any = (seen | other) != 0;
+        seen_any = hi >= 0 && lo < GROUP - 1;
+        if (!seen_any) {   // the group's scales, which may be NaN, stay out
+          f[g] = 1.0f;
+          vs[g].lm = 0.0f;
+        }
       }
-      top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-      const float f = row_scale * kd_now[g];
-      top = seen_any ? top * f : NEG_INF;
-      if (__any(top > m_run + P_LAZY)) {
-        const float m_new = __builtin_fmaxf(m_run, top);
-        const float alpha = __builtin_amdgcn_exp2f(m_run - (m_new == NEG_INF ? 0.0f : m_new));
-        m_run = m_new;
-        l_run *= alpha;
+      float t = s[g][0];
 #pragma unroll
-        for (int d = 0; d < DT; ++d) acc[d] *= alpha;
-      }
-      const ValueScale vs = value_scale(vd_now[g]);
-      if (__any(seen_any && vs.e > e_ref)) {
-        const int e_new = seen_any && vs.e > e_ref ? vs.e : e_ref;
-        const float down = __builtin_ldexpf(1.0f, e_ref - e_new);
-        e_ref = e_new;
+      for (int i = 1; i < 16; ++i) t = __builtin_elementwise_maximum(t, s[g][i]);
+      t *= f[g];
+      top = t > top ? t : top;
+      e_top = seen_any && vs[g].e > e_top ? vs[g].e : e_top;
+    }
+    const float across = other_half(top);
+    top = across > top ? across : top;
+    if (__any(top > m_run + P_LAZY || e_top > e_ref)) {
+      const float m_new = top > m_run ? top : m_run;
+      const float alpha = __builtin_amdgcn_exp2f(m_run - (m_new == NEG_INF ? 0.0f : m_new));
+      const float down = __builtin_ldexpf(alpha, e_ref - e_top);
+      m_run = m_new;
+      e_ref = e_top;
+      l_run *= alpha;
 #pragma unroll
-        for (int d = 0; d < DT; ++d) acc[d] *= down;
-      }
-      int de = vs.e - e_ref;
+      for (int d = 0; d < DT; ++d) acc[d] *= down;
+    }
+    const float ref = (m_run == NEG_INF ? 0.0f : m_run) - P_SHIFT;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      int de = vs[g].e - e_ref;
       de = de < -100 ? -100 : de > 0 ? 0 : de;
-      const float ref = (m_run == NEG_INF ? 0.0f : m_run) - P_SHIFT;
-      const float off = ((float)de + vs.lm) - ref;
-      float sum = 0.0f;
+      const float off = ((float)de + vs[g].lm) - ref;
+      float sum[2] = {0.0f, 0.0f};
       h16x8 phi[2], plo[2];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], f, off));
-        if (!clear && !((seen >> i) & 1)) p = 0.0f;
-        sum += p;
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g][i], f[g], off));
+        sum[i & 1] += p;
         phi[i >> 3][i & 7] = (_Float16)p;
         if (F32) plo[i >> 3][i & 7] = (_Float16)(p - (float)phi[i >> 3][i & 7]);
       }
-      l_run = __builtin_fmaf(sum, __builtin_ldexpf(vs.inv, -de), l_run);
+      l_run = __builtin_fmaf(sum[0] + sum[1], __builtin_ldexpf(vs[g].inv, -de), l_run);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int eight = 2 * j + lh;
-        const uint8_t* vr = lds_v[buf] + (g * 4 + eight) * (D * 16);
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          const h16x8 va = *reinterpret_cast<const h16x8*>(vr + ((32 * d + li) ^ (2 * eight)) * 16);
+          const h16x8 va = *reinterpret_cast<const h16x8*>(lds_v[BUF] + (g * 4 + 2 * j + lh) * (D * 16) +
+                                                           ((32 * d + li) ^ v_swizzle(2 * j + lh)) * 16);
           acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(va, phi[j], acc[d], 0, 0, 0);
           if (F32) acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(va, plo[j], acc[d], 0, 0, 0);
         }
-      }
     }
+  };
+  for (int tile = tile0; tile < tile_end; tile += 2) {
+    step(tile, Index<0>());
     __syncthreads();
+    if (tile + 1 < tile_end) {
+      step(tile + 1, Index<1>());
+      __syncthreads();
+    }
   }
   l_run += __shfl_xor(l_run, 32);
   if (32 * wave + li >= rows) return;
@@ -893,7 +919,7 @@ __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 
           *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.out) + to) = f32x4{o[0], o[1], o[2], o[3]};
       }
   } else {
-    float* part = a.part + (((int64_t)blockIdx.x * c.n_heads + head) * a.n_splits + split) * P_ROWS * (D + 2);
+    float* part = a.part + (((int64_t)(gridDim.x - 1 - blockIdx.x) * c.n_heads + head) * a.n_splits + split) * P_ROWS * (D + 2);
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -920,12 +946,12 @@ __global__ __launch_bounds__(J_WAVES * WAVE) void k_attention_join(Cache c, Batc
   constexpr int PER = D / WAVE;   // channels of a lane
   typedef float f32xp __attribute__((ext_vector_type(PER == 1 ? 2 : PER)));
   Span sp;
-  const int u = find_unit(b, blockIdx.x, a.group, UNIT, 1, sp);
+  const int u = find_unit(b, blockIdx.x, a.group, UNIT == A_ROWS ? A_SHIFT : P_SHIFT_ROWS, 1, sp);
   const int64_t n_rows = (int64_t)sp.n * a.group;
   const int64_t first_row = (int64_t)u * UNIT;
   if (u < 0 || first_row >= n_rows) return;
   const int rows = (int)(n_rows - first_row < UNIT ? n_rows - first_row : UNIT);
-  const Range vis = visible(sp, (int)first_row, rows, a, b.table_width * c.block, NG);
+  const Range vis = visible(sp, (int)first_row, rows, a, (int64_t)b.table_width << c.shift, NG);
   if (vis.used <= 1) return;
   const int head = blockIdx.y, lane = threadIdx.x & 63;
   constexpr int64_t STEP = (int64_t)UNIT * (D + 2);
@@ -1016,7 +1042,7 @@ int check_pointers(const qr_kv8* c, const int32_t* cu, const int32_t* kv_len, co
 }
 
 Cache device_cache(const qr_kv8* c) {
-  return {c->k, c->v, c->kd, c->vd, (int)c->n_blocks, (int)c->n_heads, (int)c->block_tokens};
+  return {c->k, c->v, c->kd, c->vd, (int)c->n_blocks, (int)c->n_heads, c->block_tokens == 32 ? 5 : c->block_tokens == 64 ? 6 : 7};
 }
 
 // Units of a call that takes one piece of a block at a time.
@@ -1111,7 +1137,7 @@ int qr_kv8_append(const qr_kv8* c, int src, const void* k, const void* v, int64_
   const int rc = check_rows(c, src, k, v, k_stride, v_stride, n_tok, n_seq, cu, kv_len, table, table_width, &units);
   if (rc != QR_OK || units == 0) return rc;
   const Cache cc = device_cache(c);
-  const Batch b = {cu, kv_len, table, table_width, (int)n_seq, (int)n_tok};
+  const Batch b = {cu, kv_len, table, (int)table_width, (int)n_seq, (int)n_tok};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const uint32_t n = (uint32_t)units;
   switch (c->head_dim) {
@@ -1132,7 +1158,7 @@ int qr_kv8_read(const qr_kv8* c, int dst, void* k, void* v, int64_t k_stride, in
   const int rc = check_rows(c, dst, k, v, k_stride, v_stride, n_tok, n_seq, cu, kv_len, table, table_width, &units);
   if (rc != QR_OK || units == 0) return rc;
   const Cache cc = device_cache(c);
-  const Batch b = {cu, kv_len, table, table_width, (int)n_seq, (int)n_tok};
+  const Batch b = {cu, kv_len, table, (int)table_width, (int)n_seq, (int)n_tok};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const uint32_t n = (uint32_t)units;
   switch (c->head_dim) {
@@ -1185,7 +1211,7 @@ int qr_attention_kv8(const qr_kv8* c, int src, const void* q, int64_t q_stride, 
   if (workspace_bytes < need)
     return qr_fail(QR_EINVAL_SHAPE, "workspace has %zu bytes, %zu are needed", workspace_bytes, need);
   const Cache cc = device_cache(c);
-  const Batch b = {cu, kv_len, table, table_width, (int)n_seq, (int)n_tok};
+  const Batch b = {cu, kv_len, table, (int)table_width, (int)n_seq, (int)n_tok};
   const Attention a = {q, out, reinterpret_cast<float*>(workspace), q_stride, out_stride, scale * 1.44269504088896340736f,
                        window < (int64_t)1 << 32 ? window : (int64_t)1 << 32, (int)group, (int)cut.splits};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
