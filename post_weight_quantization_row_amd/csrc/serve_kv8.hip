@@ -281,7 +281,7 @@ struct Attention {
   float scale;       // times log2(e)
   int64_t window;
   int group;         // query heads per key/value head
-  int n_splits;
+  int n_splits, n_units;
 };
 
 constexpr int A_SHIFT = 4, A_ROWS = 1 << A_SHIFT;   // rows of a unit
@@ -346,10 +346,10 @@ __global__ __launch_bounds__(A_WAVES * WAVE) void k_attention_kv8(Cache c, Batch
   __shared__ float join_m[A_WAVES][A_ROWS], join_l[A_WAVES][A_ROWS];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int li = lane & 15, lg = lane >> 4;
-  const int head = blockIdx.y, split = blockIdx.z;
+  const int unit = blockIdx.x / c.n_heads, head = blockIdx.x % c.n_heads, split = blockIdx.y;
 
   Span sp;
-  const int u = find_unit(b, blockIdx.x, a.group, A_SHIFT, 1, sp);
+  const int u = find_unit(b, unit, a.group, A_SHIFT, 1, sp);
   const int64_t n_rows = (int64_t)sp.n * a.group;
   const int64_t first_row = (int64_t)u * A_ROWS;
   if (u < 0 || first_row >= n_rows) return;
@@ -570,7 +570,7 @@ __global__ __launch_bounds__(A_WAVES * WAVE) void k_attention_kv8(Cache c, Batch
       const int64_t at = (int64_t)(sp.row0 + rr / a.group) * a.out_stride + (int64_t)(head * a.group + rr % a.group) * D + ch;
       store_at<SRC>(a.out, at, l == 0.0f ? 0.0f : o / l);
     } else {
-      float* part = a.part + (((int64_t)blockIdx.x * c.n_heads + head) * a.n_splits + split) * A_ROWS * (D + 2);
+      float* part = a.part + (((int64_t)unit * c.n_heads + head) * a.n_splits + split) * A_ROWS * (D + 2);
       part[row * D + ch] = o;
       if (ch == 0) {
         part[A_ROWS * D + row] = m;
@@ -658,10 +658,12 @@ __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 
   __shared__ __attribute__((aligned(16))) uint8_t lds_v[2][TOK * D * 2];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 31, lh = lane >> 5;
-  const int head = blockIdx.y, split = blockIdx.z;
+  // the longest prefixes first, the heads of a unit side by side: with 8 heads
+  // each XCD reads the keys and values of one
+  const int unit = a.n_units - 1 - blockIdx.x / c.n_heads, head = blockIdx.x % c.n_heads, split = blockIdx.y;
 
   Span sp;
-  const int u = find_unit(b, gridDim.x - 1 - blockIdx.x, a.group, P_SHIFT_ROWS, 1, sp);
+  const int u = find_unit(b, unit, a.group, P_SHIFT_ROWS, 1, sp);
   const int64_t n_rows = (int64_t)sp.n * a.group;
   const int64_t first_row = (int64_t)u * P_ROWS;
   if (u < 0 || first_row >= n_rows) return;
@@ -919,7 +921,7 @@ __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 
           *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.out) + to) = f32x4{o[0], o[1], o[2], o[3]};
       }
   } else {
-    float* part = a.part + (((int64_t)(gridDim.x - 1 - blockIdx.x) * c.n_heads + head) * a.n_splits + split) * P_ROWS * (D + 2);
+    float* part = a.part + (((int64_t)unit * c.n_heads + head) * a.n_splits + split) * P_ROWS * (D + 2);
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -945,18 +947,19 @@ template <int SRC, int D, int UNIT, int NG>
 __global__ __launch_bounds__(J_WAVES * WAVE) void k_attention_join(Cache c, Batch b, Attention a) {
   constexpr int PER = D / WAVE;   // channels of a lane
   typedef float f32xp __attribute__((ext_vector_type(PER == 1 ? 2 : PER)));
+  const int unit = blockIdx.x / c.n_heads, head = blockIdx.x % c.n_heads;
   Span sp;
-  const int u = find_unit(b, blockIdx.x, a.group, UNIT == A_ROWS ? A_SHIFT : P_SHIFT_ROWS, 1, sp);
+  const int u = find_unit(b, unit, a.group, UNIT == A_ROWS ? A_SHIFT : P_SHIFT_ROWS, 1, sp);
   const int64_t n_rows = (int64_t)sp.n * a.group;
   const int64_t first_row = (int64_t)u * UNIT;
   if (u < 0 || first_row >= n_rows) return;
   const int rows = (int)(n_rows - first_row < UNIT ? n_rows - first_row : UNIT);
   const Range vis = visible(sp, (int)first_row, rows, a, (int64_t)b.table_width << c.shift, NG);
   if (vis.used <= 1) return;
-  const int head = blockIdx.y, lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63;
   constexpr int64_t STEP = (int64_t)UNIT * (D + 2);
-  const float* part = a.part + ((int64_t)blockIdx.x * c.n_heads + head) * a.n_splits * STEP;
-  for (int row = threadIdx.x / WAVE + J_WAVES * (int)blockIdx.z; row < rows; row += J_WAVES * (int)gridDim.z) {
+  const float* part = a.part + ((int64_t)unit * c.n_heads + head) * a.n_splits * STEP;
+  for (int row = threadIdx.x / WAVE + J_WAVES * (int)blockIdx.y; row < rows; row += J_WAVES * (int)gridDim.y) {
     float f[2], l = 0.0f, m = NEG_INF;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -1074,17 +1077,17 @@ Cut cut_for(const qr_kv8* c, int64_t n_tok, int64_t n_seq, int64_t group, int64_
 template <int SRC, int D>
 int launch_attention(const Cache& c, const Batch& b, const Attention& a, const Cut& k, hipStream_t s) {
   constexpr int NG = D == 256 ? 1 : 2;   // what two LDS buffers hold in 64 KB
-  const uint32_t units = (uint32_t)k.units;
-  const dim3 grid(units, (uint32_t)c.n_heads, (uint32_t)a.n_splits);
+  const uint32_t blocks = (uint32_t)(k.units * c.n_heads);
+  const dim3 grid(blocks, (uint32_t)a.n_splits);
   if (k.many) hipLaunchKernelGGL((k_attention_kv8_rows<SRC, D, NG>), grid, dim3(P_WAVES * WAVE), 0, s, c, b, a);
   else hipLaunchKernelGGL((k_attention_kv8<SRC, D>), grid, dim3(A_WAVES * WAVE), 0, s, c, b, a);
   if (a.n_splits > 1) {
     const int rc = qr_check_launch("k_attention_kv8");
     if (rc != QR_OK) return rc;
     if (k.many)
-      hipLaunchKernelGGL((k_attention_join<SRC, D, P_ROWS, NG>), dim3(units, (uint32_t)c.n_heads, 8), dim3(J_WAVES * WAVE), 0, s, c, b, a);
+      hipLaunchKernelGGL((k_attention_join<SRC, D, P_ROWS, NG>), dim3(blocks, 8), dim3(J_WAVES * WAVE), 0, s, c, b, a);
     else
-      hipLaunchKernelGGL((k_attention_join<SRC, D, A_ROWS, 1>), dim3(units, (uint32_t)c.n_heads), dim3(J_WAVES * WAVE), 0, s, c, b, a);
+      hipLaunchKernelGGL((k_attention_join<SRC, D, A_ROWS, 1>), dim3(blocks), dim3(J_WAVES * WAVE), 0, s, c, b, a);
   }
   return qr_check_launch("k_attention_kv8");
 }
@@ -1204,7 +1207,7 @@ int qr_attention_kv8(const qr_kv8* c, int src, const void* q, int64_t q_stride, 
     return qr_fail(QR_EINVAL_PTR, "q and out must be non-NULL and 16-byte aligned");
   const int64_t group = n_q_heads / c->n_heads;
   const Cut cut = cut_for(c, n_tok, n_seq, group, table_width);
-  if (cut.units > UINT32_MAX / 256) return qr_fail(QR_EOVERFLOW, "n_tok and n_seq need too many workgroups for one launch");
+  if (cut.units * c->n_heads > UINT32_MAX / 256) return qr_fail(QR_EOVERFLOW, "n_tok and n_seq need too many workgroups for one launch");
   const size_t need = qr_attention_kv8_workspace_bytes(c, n_q_heads, n_tok, n_seq, table_width);
   if (need > 0 && (!workspace || !qr_aligned(workspace, 256)))
     return qr_fail(QR_EINVAL_PTR, "workspace must be non-NULL and 256-byte aligned");
@@ -1213,7 +1216,7 @@ int qr_attention_kv8(const qr_kv8* c, int src, const void* q, int64_t q_stride, 
   const Cache cc = device_cache(c);
   const Batch b = {cu, kv_len, table, (int)table_width, (int)n_seq, (int)n_tok};
   const Attention a = {q, out, reinterpret_cast<float*>(workspace), q_stride, out_stride, scale * 1.44269504088896340736f,
-                       window < (int64_t)1 << 32 ? window : (int64_t)1 << 32, (int)group, (int)cut.splits};
+                       window < (int64_t)1 << 32 ? window : (int64_t)1 << 32, (int)group, (int)cut.splits, (int)cut.units};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   switch (c->head_dim) {
     case 64: return src == QR_BF16 ? launch_attention<QR_BF16, 64>(cc, b, a, cut, s) : launch_attention<QR_F32, 64>(cc, b, a, cut, s);
