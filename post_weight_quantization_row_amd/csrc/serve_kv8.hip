@@ -39,6 +39,17 @@ __device__ __forceinline__ void store_at(void* x, int64_t i, float v) {
   else reinterpret_cast<float*>(x)[i] = v;
 }
 
+// Four neighbouring outputs, at a multiple of four elements of an aligned array.
+template <int DST>
+__device__ __forceinline__ void store_heads(void* x, int64_t i, const f32x4& v) {
+  if (DST == QR_BF16)
+    *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(x) + i) =
+        u32x2{(uint32_t)bf16_bits(v[0]) | (uint32_t)bf16_bits(v[1]) << 16,
+              (uint32_t)bf16_bits(v[2]) | (uint32_t)bf16_bits(v[3]) << 16};
+  else
+    *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(x) + i) = v;
+}
+
 // The sequences of a call and the cache they live in.
 struct Batch {
   const int32_t* cu;
@@ -104,8 +115,6 @@ __device__ __forceinline__ int v_byte(int t, int d) {
 // ---------------------------------------------------------------------------
 // writing and reading
 
-constexpr int RW_THREADS = 256;
-
 // The part of a sequence's rows that lies in one block: tokens [t0, t1) of
 // the block are rows row .. row + (t1 - t0) - 1.
 struct Piece {
@@ -121,7 +130,9 @@ __device__ __forceinline__ Piece find_piece(const Batch& b, const Cache& c, int6
   const int64_t slot = (from >> c.shift) + u;
   const int64_t lo = slot << c.shift;
   if (u < 0 || sp.n == 0 || lo >= sp.len) return p;
-  p.id = slot < b.table_width ? block_of(b.table + (int64_t)sp.seq * b.table_width, b.table_width, c.n_blocks, (int)slot) : -1;
+  p.id = slot < b.table_width
+             ? block_of(b.table + (int64_t)sp.seq * b.table_width, b.table_width, c.n_blocks, (int)slot)
+             : -1;
   p.t0 = (int)(from > lo ? from - lo : 0);
   const int block = 1 << c.shift;
   p.t1 = (int)(sp.len - lo < block ? sp.len - lo : block);
@@ -129,120 +140,317 @@ __device__ __forceinline__ Piece find_piece(const Batch& b, const Cache& c, int6
   return p;
 }
 
-// One workgroup per (block, head, keys or values). The new values are read
-// twice, the second time from the cache of the CU or the XCD: bound by memory.
-template <int SRC, int D>
-__global__ __launch_bounds__(RW_THREADS) void k_kv8_append(Cache c, Batch b, const void* __restrict__ k,
-                                                           const void* __restrict__ v, int64_t k_stride,
-                                                           int64_t v_stride) {
-  __shared__ uint32_t wave_max[RW_THREADS / WAVE];
-  const Piece p = find_piece(b, c, blockIdx.x);
-  if (p.id < 0 || p.t1 <= p.t0) return;
-  const int tid = threadIdx.x, head = blockIdx.y;
-  const bool values = blockIdx.z != 0;
-  const void* x = values ? v : k;
-  const int64_t stride = values ? v_stride : k_stride;
-  const int64_t x0 = (int64_t)p.row * stride + (int64_t)head * D;
-  const int nt = p.t1 - p.t0;
-  uint32_t top = 0;
-  for (int e = tid; e < nt * D; e += RW_THREADS) {
-    const uint32_t m =
-        __builtin_bit_cast(uint32_t, value_at<SRC>(x, x0 + (int64_t)(e / D) * stride + e % D)) & 0x7fffffffu;
-    top = m > top ? m : top;
+// A workgroup takes the keys or the values of one head in one block. A thread
+// takes squares of 8 tokens x 8 channels: rows of 16 or 32 bytes on the side
+// of the caller's tensors, and on the side of the cache 8 codes of a token
+// (keys) or 8 tokens of a channel (values), turned in registers. Up to four
+// waves, and as many squares per thread as the block then needs; lanes are
+// dealt so that neighbours meet neighbouring bytes on both sides.
+constexpr int RW_THREADS = 256;
+
+template <int D>
+constexpr int squares_of(int block) { return block * D / 64; }
+
+template <int D>
+constexpr int rw_threads(int block) {
+  return squares_of<D>(block) < WAVE ? WAVE : squares_of<D>(block) > RW_THREADS ? RW_THREADS : squares_of<D>(block);
+}
+
+// Square number `at`: its first token and channel in the block.
+template <int D, bool VALUES>
+__device__ __forceinline__ void square(int at, int& t, int& ch) {
+  if (VALUES) {   // the four eights of a group first: 64 bytes of a pair of channels
+    t = (at / (D / 2)) * GROUP + (at & 3) * 8;
+    ch = at % (D / 2) / 4 * 8;
+  } else {
+    t = at / (D / 8) * 8;
+    ch = at % (D / 8) * 8;
   }
+}
+
+template <int SRC>
+__device__ __forceinline__ void load_heads8(const void* x, int64_t i, float (&v)[8]) {
+  if (SRC == QR_BF16) {
+    const u16x8 h = *reinterpret_cast<const u16x8*>(reinterpret_cast<const uint16_t*>(x) + i);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = bf16_value(h[k]);
+  } else {
+    const f32x4* p = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(x) + i);
+    const f32x4 a = p[0], b = p[1];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = a[k];
+      v[4 + k] = b[k];
+    }
+  }
+}
+
+__device__ __forceinline__ int code_of(float x) {
+  return (int)__builtin_amdgcn_fmed3f(__builtin_rintf(x), -127.0f, 127.0f);
+}
+
+__device__ __forceinline__ int code_at(const u32x2& w, int i) { return (int8_t)(w[i >> 2] >> (8 * (i & 3))); }
+
+__device__ __forceinline__ u32x2 pack8(const int (&q)[8]) {
+  u32x2 w;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t a = __builtin_amdgcn_perm((uint32_t)q[4 * h + 1], (uint32_t)q[4 * h], 0x0c0c0400u);
+    const uint32_t b = __builtin_amdgcn_perm((uint32_t)q[4 * h + 3], (uint32_t)q[4 * h + 2], 0x0c0c0400u);
+    w[h] = a | b << 16;
+  }
+  return w;
+}
+
+// How a block's scale changes with the new tokens, whose largest magnitude (as
+// bits) one thread of the workgroup knows as `top`.
+struct Growth {
+  float inv, ratio;   // factors of new values and of old codes
+  bool bad, grown;
+};
+
+__device__ __forceinline__ Growth grow(uint32_t top, int t0, float* scale, uint32_t* wave_max) {
+  const int tid = threadIdx.x;
 #pragma unroll
   for (int s = 32; s > 0; s >>= 1) {
     const uint32_t o = (uint32_t)__shfl_xor((int)top, s);
     top = o > top ? o : top;
   }
   if ((tid & (WAVE - 1)) == 0) wave_max[tid / WAVE] = top;
-  const int64_t at = (int64_t)p.id * c.n_heads + head;
-  float* scale = (values ? c.vd : c.kd) + at;
-  const float old = p.t0 > 0 ? *scale : 0.0f;
+  const float old = t0 > 0 ? *scale : 0.0f;
   __syncthreads();   // every thread has read the old scale
-#pragma unroll
-  for (int w = 0; w < RW_THREADS / WAVE; ++w) top = wave_max[w] > top ? wave_max[w] : top;
+  for (int w = 0; w < (int)blockDim.x / WAVE; ++w) top = wave_max[w] > top ? wave_max[w] : top;
   float cand = __builtin_bit_cast(float, top) / 127.0f;
   if (!(1.0f / cand < __builtin_inff())) cand = 0.0f;
-  const bool bad = top >= 0x7f800000u || old != old;
-  const float d = bad ? __builtin_nanf("") : old > cand ? old : cand;
-  float inv = 1.0f / d;
-  if (bad || !(inv < __builtin_inff())) inv = 0.0f;
-  const bool grown = p.t0 > 0 && !bad && d > old;
-  const float ratio = grown ? old / d : 1.0f;
+  Growth g;
+  g.bad = top >= 0x7f800000u || old != old;
+  const float d = g.bad ? __builtin_nanf("") : old > cand ? old : cand;
+  g.inv = 1.0f / d;
+  if (g.bad || !(g.inv < __builtin_inff())) g.inv = 0.0f;
+  g.grown = t0 > 0 && !g.bad && d > old;
+  g.ratio = g.grown ? old / d : 1.0f;
   if (tid == 0) *scale = d;
+  return g;
+}
 
-  int8_t* codes = (values ? c.v : c.k) + (at << c.shift) * D;
-  // eight codes at a time: of one token for keys, of one channel for values
-  const int first8 = grown ? 0 : p.t0;
-  if (!values) {
-    for (int e = tid; e < (p.t1 - first8) * (D / 8); e += RW_THREADS) {
-      const int t = first8 + e / (D / 8), d0 = e % (D / 8) * 8;
-      u32x2* dst = reinterpret_cast<u32x2*>(codes + (int64_t)t * D + d0);
-      uint32_t u[2] = {0, 0};
-      const u32x2 prev = t < p.t0 ? *dst : u32x2{0, 0};
+// A few tokens (a decode step): bound by the time from one load to the next
+// and by fetching the code itself, so that loops stay loops; eight codes at a
+// time, of one token for keys, of one channel for values. One token into each
+// of 32 sequences, 8 heads of 128: 5.7 us, against 8.6 us by squares.
+constexpr int FEW_TOKENS = 4;
+
+template <int SRC, int D, bool VALUES>
+__device__ __forceinline__ void append_few(const Cache& c, const Piece& p, int head, const void* __restrict__ x,
+                                           int64_t stride, uint32_t* wave_max) {
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const int64_t x0 = (int64_t)p.row * stride + (int64_t)head * D;
+  uint32_t top = 0;
+#pragma unroll 1
+  for (int e = tid; e < (p.t1 - p.t0) * D; e += threads) {
+    const uint32_t m =
+        __builtin_bit_cast(uint32_t, value_at<SRC>(x, x0 + (int64_t)(e / D) * stride + e % D)) & 0x7fffffffu;
+    top = m > top ? m : top;
+  }
+  const int64_t at_scale = (int64_t)p.id * c.n_heads + head;
+  const Growth g = grow(top, p.t0, (VALUES ? c.vd : c.kd) + at_scale, wave_max);
+  int8_t* codes = (VALUES ? c.v : c.k) + (at_scale << c.shift) * D;
+  const int first = g.grown ? 0 : p.t0;   // tokens first .. t1 - 1 get codes
+  const int n = VALUES ? ((p.t1 + 7) / 8 - first / 8) * D : (p.t1 - first) * (D / 8);
+#pragma unroll 1
+  for (int e = tid; e < n; e += threads) {
+    const int t = VALUES ? (first / 8 + e / D) * 8 : first + e / (D / 8), ch = VALUES ? e % D : e % (D / 8) * 8;
+    u32x2* to = reinterpret_cast<u32x2*>(codes + (VALUES ? v_byte<D>(t, ch) : t * D + ch));
+    const u32x2 was = *to;
+    int q[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float q;
-        if (t < p.t0) q = (float)(int8_t)(prev[i >> 2] >> (8 * (i & 3))) * ratio;
-        else q = bad ? 0.0f : value_at<SRC>(x, x0 + (int64_t)(t - p.t0) * stride + d0 + i) * inv;
-        q = __builtin_rintf(q);
-        q = q > 127.0f ? 127.0f : q < -127.0f ? -127.0f : q;
-        u[i >> 2] |= ((uint32_t)(int)q & 0xffu) << (8 * (i & 3));
+    for (int i = 0; i < 8; ++i) {
+      const int ti = VALUES ? t + i : t, ci = VALUES ? ch : ch + i;
+      q[i] = code_at(was, i);   // a token before an unchanged scale, or one behind the new ones
+      if (ti < p.t0) {
+        if (g.grown) q[i] = code_of((float)q[i] * g.ratio);
+      } else if (ti < p.t1) {
+        q[i] = g.bad ? 0 : code_of(value_at<SRC>(x, x0 + (int64_t)(ti - p.t0) * stride + ci) * g.inv);
       }
-      *dst = u32x2{u[0], u[1]};
     }
-  } else {
-    const int c8 = first8 / 8, n8 = (p.t1 + 7) / 8 - c8;
-    for (int e = tid; e < n8 * D; e += RW_THREADS) {
-      const int t = (c8 + e / D) * 8, ch = e % D;
-      u32x2* dst = reinterpret_cast<u32x2*>(codes + v_byte<D>(t, ch));
-      const u32x2 prev = *dst;
-      uint32_t u[2] = {0, 0};
+    *to = pack8(q);
+  }
+}
+
+// Each new value is read once and stays in registers between the block's
+// maximum and its codes: bound by those bytes.
+template <int SRC, int D, int SQ, bool VALUES>
+__device__ __forceinline__ void append_piece(const Cache& c, const Piece& p, int head, const void* __restrict__ x,
+                                             int64_t stride, uint32_t* wave_max) {
+  const int tid = threadIdx.x, n_squares = (D << c.shift) / 64;
+  const int64_t x0 = (int64_t)p.row * stride + (int64_t)head * D;
+  float v[SQ][8][8];
+  uint32_t top = 0;
+#pragma unroll
+  for (int s = 0; s < SQ; ++s) {
+    const int at = tid + s * (int)blockDim.x;
+    int t, ch;
+    square<D, VALUES>(at, t, ch);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (at < n_squares && t + k >= p.t0 && t + k < p.t1) {
+        load_heads8<SRC>(x, x0 + (int64_t)(t + k - p.t0) * stride + ch, v[s][k]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[s][k][i] = 0.0f;
+      }
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < SQ; ++s)
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint32_t was = (prev[i >> 2] >> (8 * (i & 3))) & 0xffu;
-        uint32_t code = was;   // a token before an unchanged scale, or one behind the new ones
-        if (t + i < p.t1 && (t + i >= p.t0 || grown)) {
-          float q;
-          if (t + i < p.t0) q = (float)(int8_t)was * ratio;
-          else q = bad ? 0.0f : value_at<SRC>(x, x0 + (int64_t)(t + i - p.t0) * stride + ch) * inv;
-          q = __builtin_rintf(q);
-          q = q > 127.0f ? 127.0f : q < -127.0f ? -127.0f : q;
-          code = (uint32_t)(int)q & 0xffu;
-        }
-        u[i >> 2] |= code << (8 * (i & 3));
+        const uint32_t m = __builtin_bit_cast(uint32_t, v[s][k][i]) & 0x7fffffffu;
+        top = m > top ? m : top;
       }
-      *dst = u32x2{u[0], u[1]};
+  const int64_t at_scale = (int64_t)p.id * c.n_heads + head;
+  int8_t* codes = (VALUES ? c.v : c.k) + (at_scale << c.shift) * D;
+  // values: eight tokens share a word pair, so that squares at the ends keep
+  // what the neighbouring tokens hold
+  u32x4 was4[SQ][4];
+  if (VALUES) {
+#pragma unroll
+    for (int s = 0; s < SQ; ++s) {
+      const int at = tid + s * (int)blockDim.x;
+      int t, ch;
+      square<D, VALUES>(at, t, ch);
+      const bool ends = at < n_squares && t < p.t1 && (t < p.t0 || t + 8 > p.t1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        was4[s][i] = ends ? *reinterpret_cast<const u32x4*>(codes + v_byte<D>(t, ch + 2 * i)) : u32x4{};
+    }
+  }
+  const Growth g = grow(top, p.t0, (VALUES ? c.vd : c.kd) + at_scale, wave_max);
+  const int first = g.grown ? 0 : p.t0;   // tokens first .. t1 - 1 get codes
+#pragma unroll
+  for (int s = 0; s < SQ; ++s) {
+    const int at = tid + s * (int)blockDim.x;
+    int t, ch;
+    square<D, VALUES>(at, t, ch);
+    if (at >= n_squares || t + 8 <= first || t >= p.t1) continue;
+    if (!VALUES) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (t + k < first || t + k >= p.t1) continue;
+        u32x2* to = reinterpret_cast<u32x2*>(codes + (t + k) * D + ch);
+        int q[8];
+        if (t + k < p.t0) {
+          const u32x2 was = *to;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) q[i] = code_of((float)code_at(was, i) * g.ratio);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) q[i] = g.bad ? 0 : code_of(v[s][k][i] * g.inv);
+        }
+        *to = pack8(q);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        u32x4* to = reinterpret_cast<u32x4*>(codes + v_byte<D>(t, ch + i));
+        const u32x4 was = was4[s][i / 2];
+        u32x2 w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const u32x2 old8 = {was[2 * h], was[2 * h + 1]};
+          int q[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            if (t + k < p.t0) q[k] = g.grown ? code_of((float)code_at(old8, k) * g.ratio) : code_at(old8, k);
+            else if (t + k >= p.t1) q[k] = code_at(old8, k);   // behind the new tokens
+            else q[k] = g.bad ? 0 : code_of(v[s][k][i + h] * g.inv);
+          }
+          w[h] = pack8(q);
+        }
+        *to = u32x4{w[0][0], w[0][1], w[1][0], w[1][1]};
+      }
     }
   }
 }
 
-// The decoder, over the same pieces.
+template <int SRC, int D, int SQ>
+__global__ __launch_bounds__(RW_THREADS) void k_kv8_append(Cache c, Batch b, const void* __restrict__ k,
+                                                           const void* __restrict__ v, int64_t k_stride,
+                                                           int64_t v_stride) {
+  __shared__ uint32_t wave_max[RW_THREADS / WAVE];
+  const Piece p = find_piece(b, c, blockIdx.x / c.n_heads);
+  if (p.id < 0 || p.t1 <= p.t0) return;
+  const int head = blockIdx.x % c.n_heads;
+  if (p.t1 - p.t0 <= FEW_TOKENS) {
+    if (blockIdx.y == 0) append_few<SRC, D, false>(c, p, head, k, k_stride, wave_max);
+    else append_few<SRC, D, true>(c, p, head, v, v_stride, wave_max);
+  } else if (blockIdx.y == 0) append_piece<SRC, D, SQ, false>(c, p, head, k, k_stride, wave_max);
+  else {
+    append_piece<SRC, D, SQ, true>(c, p, head, v, v_stride, wave_max);
+  }
+}
+
+template <int DST>
+__device__ __forceinline__ void store_heads8(void* x, int64_t i, const float (&v)[8]) {
+  store_heads<DST>(x, i, f32x4{v[0], v[1], v[2], v[3]});
+  store_heads<DST>(x, i + 4, f32x4{v[4], v[5], v[6], v[7]});
+}
+
+template <int DST, int D, bool VALUES>
+__device__ __forceinline__ void read_piece(const Cache& c, const Piece& p, int head, void* __restrict__ x,
+                                           int64_t stride) {
+  const int tid = threadIdx.x, n_squares = (D << c.shift) / 64;
+  const int64_t x0 = (int64_t)p.row * stride + (int64_t)head * D;
+  const int64_t at_scale = (int64_t)(p.id < 0 ? 0 : p.id) * c.n_heads + head;
+  const float d = p.id < 0 ? 0.0f : (VALUES ? c.vd : c.kd)[at_scale];
+  const int8_t* codes = (VALUES ? c.v : c.k) + (at_scale << c.shift) * D;
+  for (int at = tid; at < n_squares; at += (int)blockDim.x) {
+    int t, ch;
+    square<D, VALUES>(at, t, ch);
+    if (t + 8 <= p.t0 || t >= p.t1) continue;
+    u32x2 w[8] = {};   // of token k (keys), of channel ch + k (values)
+    if (p.id >= 0) {
+      if (VALUES) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const u32x4 two = *reinterpret_cast<const u32x4*>(codes + v_byte<D>(t, ch + i));
+          w[i] = u32x2{two[0], two[1]};
+          w[i + 1] = u32x2{two[2], two[3]};
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = *reinterpret_cast<const u32x2*>(codes + (t + k) * D + ch);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (t + k < p.t0 || t + k >= p.t1) continue;
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = p.id < 0 ? 0.0f : (float)(VALUES ? code_at(w[i], k) : code_at(w[k], i)) * d;
+      store_heads8<DST>(x, x0 + (int64_t)(t + k - p.t0) * stride + ch, f);
+    }
+  }
+}
+
+// The decoder, over the same pieces: bound by the values it writes.
 template <int DST, int D>
 __global__ __launch_bounds__(RW_THREADS) void k_kv8_read(Cache c, Batch b, void* __restrict__ k, void* __restrict__ v,
                                                          int64_t k_stride, int64_t v_stride) {
-  const int tid = threadIdx.x, head = blockIdx.y;
-  const bool values = blockIdx.z != 0;
-  void* x = values ? v : k;
-  const int64_t stride = values ? v_stride : k_stride;
-  Piece p = find_piece(b, c, blockIdx.x);
+  const int tid = threadIdx.x, unit = blockIdx.x / c.n_heads, head = blockIdx.x % c.n_heads;
+  const Piece p = find_piece(b, c, unit);
   if (p.t1 > p.t0) {
-    const int64_t at = (int64_t)p.id * c.n_heads + head;
-    const float d = p.id < 0 ? 0.0f : (values ? c.vd : c.kd)[at];
-    const int8_t* codes = (values ? c.v : c.k) + (at << c.shift) * D;
-    for (int e = tid; e < (p.t1 - p.t0) * D; e += RW_THREADS) {
-      const int t = p.t0 + e / D, ch = e % D;
-      float f = 0.0f;
-      if (p.id >= 0) f = (float)codes[values ? v_byte<D>(t, ch) : t * D + ch] * d;
-      store_at<DST>(x, (int64_t)(p.row + t - p.t0) * stride + (int64_t)head * D + ch, f);
-    }
+    if (blockIdx.y == 0) read_piece<DST, D, false>(c, p, head, k, k_stride);
+    else read_piece<DST, D, true>(c, p, head, v, v_stride);
   }
   // rows before position 0: the sequence's first unit clears them
   Span sp;
-  if (find_unit(b, blockIdx.x, 1, c.shift, 2, sp) == 0 && sp.len < sp.n) {
+  if (find_unit(b, unit, 1, c.shift, 2, sp) == 0 && sp.len < sp.n) {
+    void* x = blockIdx.y == 0 ? k : v;
+    const int64_t stride = blockIdx.y == 0 ? k_stride : v_stride;
     const int64_t lost = sp.len < 0 ? sp.n : (int64_t)sp.n - sp.len;
-    for (int64_t e = tid; e < lost * D; e += RW_THREADS)
+    for (int64_t e = tid; e < lost * D; e += blockDim.x)
       store_at<DST>(x, (sp.row0 + e / D) * stride + (int64_t)head * D + e % D, 0.0f);
   }
 }
@@ -913,12 +1121,7 @@ __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 
         float o[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[k] = __builtin_ldexpf(acc[d][i + k] * norm, e_ref);
-        if (SRC == QR_BF16)
-          *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + to) =
-              u32x2{(uint32_t)bf16_bits(o[0]) | (uint32_t)bf16_bits(o[1]) << 16,
-                    (uint32_t)bf16_bits(o[2]) | (uint32_t)bf16_bits(o[3]) << 16};
-        else
-          *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.out) + to) = f32x4{o[0], o[1], o[2], o[3]};
+        store_heads<SRC>(a.out, to, f32x4{o[0], o[1], o[2], o[3]});
       }
   } else {
     float* part = a.part + (((int64_t)unit * c.n_heads + head) * a.n_splits + split) * P_ROWS * (D + 2);
@@ -936,17 +1139,14 @@ __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 
   }
 }
 
-// Joins the splits of a unit of UNIT rows; a wave takes a row at a time. Lane
-// z works out the factor of split z (and z + 64); then every lane adds its
-// channels over the splits, whose loads do not wait for each other.
-constexpr int J_WAVES = 4;
-constexpr int J_BATCH = 32;
+// Joins the splits of a unit of UNIT rows. Up to J_FEW splits a thread adds
+// four channels of a row, and everything it needs is loaded at once.
+constexpr int J_THREADS = 256;
+constexpr int J_FEW = 8;
 constexpr int MAX_SPLITS = 128;
 
 template <int SRC, int D, int UNIT, int NG>
-__global__ __launch_bounds__(J_WAVES * WAVE) void k_attention_join(Cache c, Batch b, Attention a) {
-  constexpr int PER = D / WAVE;   // channels of a lane
-  typedef float f32xp __attribute__((ext_vector_type(PER == 1 ? 2 : PER)));
+__global__ __launch_bounds__(J_THREADS) void k_attention_join_few(Cache c, Batch b, Attention a) {
   const int unit = blockIdx.x / c.n_heads, head = blockIdx.x % c.n_heads;
   Span sp;
   const int u = find_unit(b, unit, a.group, UNIT == A_ROWS ? A_SHIFT : P_SHIFT_ROWS, 1, sp);
@@ -955,54 +1155,120 @@ __global__ __launch_bounds__(J_WAVES * WAVE) void k_attention_join(Cache c, Batc
   if (u < 0 || first_row >= n_rows) return;
   const int rows = (int)(n_rows - first_row < UNIT ? n_rows - first_row : UNIT);
   const Range vis = visible(sp, (int)first_row, rows, a, (int64_t)b.table_width << c.shift, NG);
-  if (vis.used <= 1) return;
-  const int lane = threadIdx.x & 63;
+  const int at = (int)(blockIdx.y * J_THREADS + threadIdx.x);
+  const int row = at / (D / 4), ch = at % (D / 4) * 4;
+  if (vis.used <= 1 || row >= rows) return;
   constexpr int64_t STEP = (int64_t)UNIT * (D + 2);
   const float* part = a.part + ((int64_t)unit * c.n_heads + head) * a.n_splits * STEP;
-  for (int row = threadIdx.x / WAVE + J_WAVES * (int)blockIdx.y; row < rows; row += J_WAVES * (int)gridDim.y) {
-    float f[2], l = 0.0f, m = NEG_INF;
+  float mz[J_FEW], lz[J_FEW];
+  f32x4 oz[J_FEW];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int z = lane + i * WAVE;
-      f[i] = z < vis.used ? part[z * STEP + UNIT * D + row] : NEG_INF;
-      m = __builtin_fmaxf(m, f[i]);
-    }
-#pragma unroll
-    for (int s = 32; s > 0; s >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, s));
-    const float ref = m == NEG_INF ? 0.0f : m;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int z = lane + i * WAVE;
-      f[i] = __builtin_amdgcn_exp2f(f[i] - ref);
-      if (z < vis.used) l = __builtin_fmaf(part[z * STEP + UNIT * D + UNIT + row], f[i], l);
-    }
-#pragma unroll
-    for (int s = 32; s > 0; s >>= 1) l += __shfl_xor(l, s);
-    float o[PER] = {};
-    for (int z0 = 0; z0 < vis.used; z0 += J_BATCH) {
-      f32xp v[J_BATCH];
-#pragma unroll
-      for (int k = 0; k < J_BATCH; ++k) {
-        const int z = z0 + k < vis.used ? z0 + k : vis.used - 1;
-        const float* pz = part + z * STEP + row * D + lane * PER;
-        if (PER == 1) v[k][0] = pz[0];
-        else v[k] = *reinterpret_cast<const f32xp*>(pz);
-      }
-#pragma unroll
-      for (int k = 0; k < J_BATCH; ++k) {
-        const int z = z0 + k;
-        const float fz = __builtin_bit_cast(
-            float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, z < WAVE ? f[0] : f[1]), z & (WAVE - 1)));
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-          if (z < vis.used) o[i] = __builtin_fmaf(v[k][i], fz, o[i]);
-      }
-    }
-    const int rr = (int)first_row + row;
-    const int64_t at = (int64_t)(sp.row0 + rr / a.group) * a.out_stride + (int64_t)(head * a.group + rr % a.group) * D + lane * PER;
-#pragma unroll
-    for (int k = 0; k < PER; ++k) store_at<SRC>(a.out, at + k, l == 0.0f ? 0.0f : o[k] / l);
+  for (int z = 0; z < J_FEW; ++z) {
+    const float* pz = part + (z < vis.used ? z : 0) * STEP;
+    mz[z] = pz[UNIT * D + row];
+    lz[z] = pz[UNIT * D + UNIT + row];
+    oz[z] = *reinterpret_cast<const f32x4*>(pz + row * D + ch);
   }
+  float m = NEG_INF, l = 0.0f;
+#pragma unroll
+  for (int z = 0; z < J_FEW; ++z)
+    if (z < vis.used) m = __builtin_fmaxf(m, mz[z]);
+  const float ref = m == NEG_INF ? 0.0f : m;
+  f32x4 o = {};
+#pragma unroll
+  for (int z = 0; z < J_FEW; ++z)
+    if (z < vis.used) {
+      const float f = __builtin_amdgcn_exp2f(mz[z] - ref);
+      l = __builtin_fmaf(lz[z], f, l);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(oz[z][i], f, o[i]);
+    }
+  const int rr = (int)first_row + row;
+  const int64_t to = (int64_t)(sp.row0 + rr / a.group) * a.out_stride + (int64_t)(head * a.group + rr % a.group) * D + ch;
+  store_heads<SRC>(a.out, to, l == 0.0f ? f32x4{} : f32x4{o[0] / l, o[1] / l, o[2] / l, o[3] / l});
+}
+
+// More splits: a workgroup per row, each of its waves on every fourth split.
+// Lane z works out the factor of split z (and z + 64); then every lane adds
+// its channels over the splits, whose loads do not wait for each other.
+template <int SRC, int D, int UNIT, int NG>
+__global__ __launch_bounds__(J_THREADS) void k_attention_join(Cache c, Batch b, Attention a) {
+  constexpr int SHARE = J_THREADS / WAVE;
+  constexpr int PER = D / WAVE;   // channels of a lane
+  constexpr int BATCH = 8;        // loads in flight
+  typedef float f32xp __attribute__((ext_vector_type(PER == 1 ? 2 : PER)));
+  __shared__ float share_o[SHARE][D];
+  const int unit = blockIdx.x / c.n_heads, head = blockIdx.x % c.n_heads;
+  Span sp;
+  const int u = find_unit(b, unit, a.group, UNIT == A_ROWS ? A_SHIFT : P_SHIFT_ROWS, 1, sp);
+  const int64_t n_rows = (int64_t)sp.n * a.group;
+  const int64_t first_row = (int64_t)u * UNIT;
+  if (u < 0 || first_row >= n_rows) return;
+  const int rows = (int)(n_rows - first_row < UNIT ? n_rows - first_row : UNIT);
+  const Range vis = visible(sp, (int)first_row, rows, a, (int64_t)b.table_width << c.shift, NG);
+  const int row = blockIdx.y;
+  if (vis.used <= 1 || row >= rows) return;
+  const int lane = threadIdx.x & 63, share = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+  constexpr int64_t STEP = (int64_t)UNIT * (D + 2);
+  const float* part = a.part + ((int64_t)unit * c.n_heads + head) * a.n_splits * STEP;
+  float f[2], l = 0.0f, m = NEG_INF;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int z = lane + i * WAVE;
+    f[i] = z < vis.used ? part[z * STEP + UNIT * D + row] : NEG_INF;
+    m = __builtin_fmaxf(m, f[i]);
+  }
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, s));
+  const float ref = m == NEG_INF ? 0.0f : m;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int z = lane + i * WAVE;
+    f[i] = __builtin_amdgcn_exp2f(f[i] - ref);
+    if (z < vis.used) l = __builtin_fmaf(part[z * STEP + UNIT * D + UNIT + row], f[i], l);
+  }
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) l += __shfl_xor(l, s);
+  float o[PER] = {};
+  for (int z0 = share; z0 < vis.used; z0 += BATCH * SHARE) {
+    f32xp v[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int z = z0 + k * SHARE < vis.used ? z0 + k * SHARE : vis.used - 1;
+      const float* pz = part + z * STEP + row * D + lane * PER;
+      if (PER == 1) v[k][0] = pz[0];
+      else v[k] = *reinterpret_cast<const f32xp*>(pz);
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int z = z0 + k * SHARE;
+      const float fz = lane_value(z < WAVE ? f[0] : f[1], z & (WAVE - 1));
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (z < vis.used) o[i] = __builtin_fmaf(v[k][i], fz, o[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) share_o[share][lane * PER + i] = o[i];
+  __syncthreads();
+  if (share > 0) return;
+#pragma unroll
+  for (int w = 1; w < SHARE; ++w)
+#pragma unroll
+    for (int i = 0; i < PER; ++i) o[i] += share_o[w][lane * PER + i];
+  const int rr = (int)first_row + row;
+  const int64_t at = (int64_t)(sp.row0 + rr / a.group) * a.out_stride + (int64_t)(head * a.group + rr % a.group) * D + lane * PER;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) store_at<SRC>(a.out, at + k, l == 0.0f ? 0.0f : o[k] / l);
+}
+
+template <int SRC, int D, int UNIT, int NG>
+void launch_join(const Cache& c, const Batch& b, const Attention& a, uint32_t blocks, hipStream_t s) {
+  if (a.n_splits <= J_FEW)
+    hipLaunchKernelGGL((k_attention_join_few<SRC, D, UNIT, NG>), dim3(blocks, (UNIT * D / 4 + J_THREADS - 1) / J_THREADS),
+                       dim3(J_THREADS), 0, s, c, b, a);
+  else
+    hipLaunchKernelGGL((k_attention_join<SRC, D, UNIT, NG>), dim3(blocks, UNIT), dim3(J_THREADS), 0, s, c, b, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -1066,7 +1332,7 @@ Cut cut_for(const qr_kv8* c, int64_t n_tok, int64_t n_seq, int64_t group, int64_
   k.units = n_tok * group / unit + n_seq;
   const int64_t busy = n_seq * ((rows + unit - 1) / unit) * c->n_heads;
   const int64_t most = (table_width * (c->block_tokens / GROUP) + A_MIN_GROUPS - 1) / A_MIN_GROUPS;
-  const int64_t want = k.many ? 512 : 1024;   // workgroups: two, four per CU
+  const int64_t want = k.many ? 512 : 2048;   // workgroups: two, eight per CU
   k.splits = (want + busy - 1) / busy;
   if (k.splits > most) k.splits = most;
   if (k.splits > MAX_SPLITS) k.splits = MAX_SPLITS;
@@ -1084,10 +1350,8 @@ int launch_attention(const Cache& c, const Batch& b, const Attention& a, const C
   if (a.n_splits > 1) {
     const int rc = qr_check_launch("k_attention_kv8");
     if (rc != QR_OK) return rc;
-    if (k.many)
-      hipLaunchKernelGGL((k_attention_join<SRC, D, P_ROWS, NG>), dim3(blocks, 8), dim3(J_WAVES * WAVE), 0, s, c, b, a);
-    else
-      hipLaunchKernelGGL((k_attention_join<SRC, D, A_ROWS, 1>), dim3(blocks), dim3(J_WAVES * WAVE), 0, s, c, b, a);
+    if (k.many) launch_join<SRC, D, P_ROWS, NG>(c, b, a, blocks, s);
+    else launch_join<SRC, D, A_ROWS, 1>(c, b, a, blocks, s);
   }
   return qr_check_launch("k_attention_kv8");
 }
@@ -1095,13 +1359,19 @@ int launch_attention(const Cache& c, const Batch& b, const Attention& a, const C
 template <int SRC, int D>
 int launch_append(const Cache& c, const Batch& b, const void* k, const void* v, int64_t ks, int64_t vs, uint32_t units,
                   hipStream_t s) {
-  hipLaunchKernelGGL((k_kv8_append<SRC, D>), dim3(units, (uint32_t)c.n_heads, 2), dim3(RW_THREADS), 0, s, c, b, k, v, ks, vs);
+  const int block = 1 << c.shift, threads = rw_threads<D>(block);
+  const dim3 grid(units * (uint32_t)c.n_heads, 2);
+  if (squares_of<D>(block) > threads)   // 128 tokens of 256 channels
+    hipLaunchKernelGGL((k_kv8_append<SRC, D, D == 256 ? 2 : 1>), grid, dim3(threads), 0, s, c, b, k, v, ks, vs);
+  else
+    hipLaunchKernelGGL((k_kv8_append<SRC, D, 1>), grid, dim3(threads), 0, s, c, b, k, v, ks, vs);
   return qr_check_launch("k_kv8_append");
 }
 
 template <int DST, int D>
 int launch_read(const Cache& c, const Batch& b, void* k, void* v, int64_t ks, int64_t vs, uint32_t units, hipStream_t s) {
-  hipLaunchKernelGGL((k_kv8_read<DST, D>), dim3(units, (uint32_t)c.n_heads, 2), dim3(RW_THREADS), 0, s, c, b, k, v, ks, vs);
+  hipLaunchKernelGGL((k_kv8_read<DST, D>), dim3(units * (uint32_t)c.n_heads, 2), dim3(rw_threads<D>(1 << c.shift)), 0, s,
+                     c, b, k, v, ks, vs);
   return qr_check_launch("k_kv8_read");
 }
 
@@ -1119,7 +1389,7 @@ int check_rows(const qr_kv8* c, int dtype, const void* k, const void* v, int64_t
   if (!k || !v || !qr_aligned(k, 16) || !qr_aligned(v, 16))
     return qr_fail(QR_EINVAL_PTR, "k and v must be non-NULL and 16-byte aligned");
   *units = piece_units(c, n_tok, n_seq);
-  if (*units > UINT32_MAX / RW_THREADS) return qr_fail(QR_EOVERFLOW, "n_tok and n_seq need too many workgroups for one launch");
+  if (*units * c->n_heads > UINT32_MAX / RW_THREADS) return qr_fail(QR_EOVERFLOW, "n_tok and n_seq need too many workgroups for one launch");
   return QR_OK;
 }
 

@@ -214,6 +214,8 @@ def test_one_long_sequence_splits(sv, bf16):
     say(f"long bf16={bf16}")
     check_attention(sv, [9001], [1], 4, 1, 128, 64, bf16, seed=3)
     check_attention(sv, [5000, 3], [2, 1], 2, 2, 64, 32, bf16, seed=4, width=400)
+    check_attention(sv, [4000], [70], 1, 1, 64, 32, bf16, seed=5)
+    check_attention(sv, [900, 2500], [60, 70], 2, 1, 128, 128, bf16, seed=6, window=1500)
 
 
 @pytest.mark.parametrize("bf16", [True, False])
