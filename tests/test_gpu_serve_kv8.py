@@ -112,7 +112,7 @@ def test_append_edges(sv):
         got = [cache.kd.cpu().numpy(), cache.vd.cpu().numpy()]
         for j in range(2):
             assert np.array_equal(np.nan_to_num(got[j], nan=-1), np.nan_to_num(ref.scales[j], nan=-1))
-        k, v = [t.cpu() for t in cache[:2]]
+        k, v = cache.k.cpu(), cache.v.cpu()
         assert torch.equal(k, ref.device_tensors()[0]) and torch.equal(v, ref.device_tensors()[1])
     assert np.isnan(got[0][7, 1]) and np.isnan(got[1][7, 0]) and np.isnan(got[0]).sum() == 1
     # reading: zeros where there is no token, rows of no sequence untouched

@@ -197,9 +197,10 @@ def test_binding_refuses_wrong_tensors(lib, monkeypatch):
         lambda: serve.qr_matmul_i8(w, z(8), x, z(4), 100, out=z(4, 8, dt=torch.float16)),
         lambda: serve.qr_kv8_append(kv, rows, host(4, 2, 64), cu, ln, tab),
         lambda: serve.qr_kv8_append(kv, rows, rows, host(3, dtype=torch.int32), ln, tab),
-        lambda: serve.qr_kv8_append(kv._replace(vd=host(8, 2)), rows, rows, cu, ln, tab),
+        lambda: serve.qr_kv8_append(serve.Kv8Cache(kv.k, kv.v, kv.kd, host(8, 2)), rows, rows, cu, ln, tab),
         lambda: serve.qr_kv8_read(kv, cu, ln, tab, 4, k=host(4, 2, 64), v=rows),
         lambda: serve.qr_attention_kv8(q, kv, cu, ln, host((2, 3), dtype=torch.int32)),
+        lambda: serve.qr_attention_kv8(q, tuple(kv), cu, ln, tab),
         lambda: serve.qr_attention_kv8(q, kv, cu, ln, tab, out=host(4, 4, 64)),
         lambda: serve.qr_attention_kv8(q, kv, cu, ln, tab_long, out=q, workspace=host(1 << 20, dtype=torch.uint8)),
     ]
@@ -219,7 +220,7 @@ def test_binding_refuses_wrong_tensors(lib, monkeypatch):
         lambda: serve.qr_matmul_i8(w, z(8), x, z(4), 100, out=dev(host(8, 4).t())),
         lambda: serve.kv8_cache(4, 2, 96, 32, "cpu"),
         lambda: serve.kv8_cache(4, 2, 64, 16, "cpu"),
-        lambda: serve.qr_kv8_append(kv._replace(v=i8(8, 2, 32, 64)), rows, rows, cu, ln, tab),
+        lambda: serve.qr_kv8_append(serve.Kv8Cache(kv.k, i8(8, 2, 32, 64), kv.kd, kv.vd), rows, rows, cu, ln, tab),
         lambda: serve.qr_kv8_append(kv, rows, rows, cu, ln, i32(3, 3)),
         lambda: serve.qr_kv8_append(kv, rows, rows, i32(2), ln, tab),
         lambda: serve.qr_kv8_append(kv, rows, rows, cu, ln, z(2, 3, dt=torch.int64)),
