@@ -14,6 +14,7 @@ namespace {
 typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int WAVE = 64;
@@ -277,101 +278,139 @@ __global__ __launch_bounds__(F_WAVES* WAVE) void k_matmul_i8_few(Product p) {
   }
 }
 
-// Many tokens: a tile of 32 NI channels x 32 NJ tokens per workgroup, a
+// Many tokens: a tile of 64 NI channels x 64 NJ tokens per workgroup, a
 // quarter of it per wave, 128 values of the sum per step through LDS. The
 // weights are the matrix instruction's left operand: a lane then ends with
-// four neighbouring channels of one token.
+// runs of four neighbouring channels of one token.
 //
-// A step's two halves of 64 values are in turn multiplied from registers
-// while the other half's operands are read from LDS; the next step's tile is
-// written to the second LDS buffer and the one after that is in flight from
-// memory. One barrier a step: it follows the reads of this step's second
-// half and the writes of the next step's tile.
+// A step is four products of 32 values. While one is multiplied, the operands
+// of the next come in from LDS; during the first three the next step's tile
+// is written to the other LDS buffer and the one after that is asked for from
+// memory. One barrier a step, before the fourth: it follows the last read of
+// this tile and the writes of the next.
 //
-// In LDS the 16-byte piece c of row r lies at r * 128 + (c ^ (r % 8)) * 16:
-// eight lanes that take one piece of neighbouring rows meet all banks.
-template <int DST, int NI, int NJ>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(NI * NJ > 32 ? 1 : 2))) void k_matmul_i8_tile(
+// In LDS the 16-byte piece c of row r lies at r * 128 + (c ^ (r / 2 % 8)) * 16:
+// sixteen lanes that take one piece of neighbouring rows meet all banks.
+template <int DST, int NI, int NJ, int KS>
+__global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(NI * NJ > 8 ? 1 : 2))) void k_matmul_i8_tile(
     Product p, int out_tiles, int tok_tiles) {
-  constexpr int TO = 32 * NI, TT = 32 * NJ;
-  __shared__ __attribute__((aligned(16))) int8_t lds[2][(TO + TT) * 128];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int li = lane & 15, lk = lane >> 4;
+  constexpr int TO = 64 * NI, TT = 64 * NJ;
+  constexpr bool LATE = NI * NJ > 8;   // ask for a tile late, between products that hide it
+  __shared__ __attribute__((aligned(16))) int8_t all_lds[KS][2][(TO + TT) * 128];
+  const int part = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+  int8_t(*lds)[(TO + TT) * 128] = all_lds[part];
+  const int tid = threadIdx.x & 255, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int li = lane & 31, lh = lane >> 5;
   int bo, bt;
   tile_of(blockIdx.x, out_tiles, tok_tiles, bo, bt);
   const int o0 = bo * TO, t0 = bt * TT;
-  const int wo = (wave & 1) * (16 * NI), wt = (wave >> 1) * (16 * NJ);
+  const int wo = (wave & 1) * (32 * NI), wt = (wave >> 1) * (32 * NJ);
   const int8_t* wbase = p.w + (int64_t)o0 * p.row_bytes;
   const int8_t* xbase = p.x + (int64_t)t0 * p.row_bytes;
   // rows behind the last repeat it: their results are not stored
+  constexpr int NQ = 2 * NI + 2 * NJ;   // 32-row pieces of the tile: weights, then tokens
   const int lr = tid >> 3, lc = (tid & 7) * 16;
-  uint32_t woff[NI], xoff[NJ];
+  uint32_t off[NQ];
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int r = o0 + lr + 32 * i < p.n_out ? lr + 32 * i : p.n_out - 1 - o0;
-    woff[i] = (uint32_t)r * (uint32_t)p.row_bytes + lc;
+  for (int q = 0; q < NQ; ++q) {
+    const int r = lr + 32 * (q < 2 * NI ? q : q - 2 * NI);
+    const int last = q < 2 * NI ? p.n_out - 1 - o0 : p.n_tok - 1 - t0;
+    off[q] = (uint32_t)(r < last ? r : last) * (uint32_t)p.row_bytes + lc;
   }
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int r = t0 + lr + 32 * j < p.n_tok ? lr + 32 * j : p.n_tok - 1 - t0;
-    xoff[j] = (uint32_t)r * (uint32_t)p.row_bytes + lc;
-  }
-  const int put = lr * 128 + ((lc >> 4) ^ (lr & 7)) * 16;
-  i32x4 rw[NI], rx[NJ];
-  auto load = [&](int s) {
-    const int8_t* wk = wbase + (int64_t)s * 128;
-    const int8_t* xk = xbase + (int64_t)s * 128;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) rw[i] = *reinterpret_cast<const i32x4*>(wk + woff[i]);
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) rx[j] = *reinterpret_cast<const i32x4*>(xk + xoff[j]);
+  const int put = lr * 128 + ((lc >> 4) ^ ((lr >> 1) & 7)) * 16;
+  i32x4 raw[NQ];
+  auto load = [&](int q, int64_t at) {
+    raw[q] = *reinterpret_cast<const i32x4*>((q < 2 * NI ? wbase : xbase) + at + off[q]);
   };
-  auto store = [&](int8_t* buf) {
+  auto store = [&](int q, int8_t* buf) { *reinterpret_cast<i32x4*>(buf + put + q * 32 * 128) = raw[q]; };
+  i32x4 a[2][NI], b[2][NJ];
+  int get[4];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) *reinterpret_cast<i32x4*>(buf + put + i * 32 * 128) = rw[i];
+  for (int k = 0; k < 4; ++k) get[k] = li * 128 + ((2 * k + lh) ^ ((li >> 1) & 7)) * 16;
+  auto read = [&](const int8_t* buf, int k, i32x4(&ra)[NI], i32x4(&rb)[NJ]) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) *reinterpret_cast<i32x4*>(buf + TO * 128 + put + j * 32 * 128) = rx[j];
+    for (int i = 0; i < NI; ++i) ra[i] = *reinterpret_cast<const i32x4*>(buf + wo * 128 + get[k] + i * 32 * 128);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) rb[j] = *reinterpret_cast<const i32x4*>(buf + (TO + wt) * 128 + get[k] + j * 32 * 128);
   };
-  i32x4 a0[NI], b0[NJ], a1[NI], b1[NJ];
-  const int get0 = li * 128 + ((lk) ^ (li & 7)) * 16, get1 = li * 128 + ((4 + lk) ^ (li & 7)) * 16;
-  auto read = [&](const int8_t* buf, int get, i32x4(&a)[NI], i32x4(&b)[NJ]) {
+  i32x16 acc[NI][NJ] = {};
+  // steps part, part + KS, ... are this part's; one behind the last is not used
+  const int all = p.row_bytes / 128, steps = (all + KS - 1) / KS;
+  auto at_step = [&](int s) { return (int64_t)(s * KS + part < all ? s * KS + part : all - 1) * 128; };
 #pragma unroll
-    for (int i = 0; i < NI; ++i) a[i] = *reinterpret_cast<const i32x4*>(buf + wo * 128 + get + i * 16 * 128);
+  for (int q = 0; q < NQ; ++q) load(q, at_step(0));
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) b[j] = *reinterpret_cast<const i32x4*>(buf + TO * 128 + wt * 128 + get + j * 16 * 128);
-  };
-  i32x4 acc[NI][NJ] = {};
-  auto multiply = [&](const i32x4(&a)[NI], const i32x4(&b)[NJ]) {
+  for (int q = 0; q < NQ; ++q) store(q, lds[0]);
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], b[j], acc[i][j], 0, 0, 0);
-  };
-  const int steps = p.row_bytes / 128;
-  load(0);
-  store(lds[0]);
-  load(steps > 1 ? 1 : 0);
+  for (int q = 0; q < NQ; ++q) load(q, at_step(1));
   __syncthreads();
-  read(lds[0], get0, a0, b0);
-  for (int s = 0; s + 1 < steps; ++s) {
-    read(lds[s & 1], get1, a1, b1);
-    store(lds[(s + 1) & 1]);
-    load(s + 2 < steps ? s + 2 : steps - 1);   // the last one twice: not used
-    multiply(a0, b0);
-    __syncthreads();
-    read(lds[(s + 1) & 1], get0, a0, b0);
-    multiply(a1, b1);
+  read(lds[0], 0, a[0], b[0]);
+  for (int s = 0; s < steps; ++s) {
+    const int8_t* cur = lds[s & 1];
+    int8_t* nxt = lds[(s + 1) & 1];
+    const int64_t ahead = at_step(s + 2);
+    const bool mine = KS == 1 || s * KS + part < all;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k == 3) __syncthreads();
+      read(k == 3 ? nxt : cur, (k + 1) & 3, a[(k + 1) & 1], b[(k + 1) & 1]);
+      if (k < 3) {
+#pragma unroll
+        for (int q = k * NQ / 3; q < (k + 1) * NQ / 3; ++q) {
+          store(q, nxt);
+          if (!LATE) load(q, ahead);
+        }
+      }
+      if (LATE && k > 0) {   // behind the stores of the same pieces
+#pragma unroll
+        for (int q = (k - 1) * NQ / 4; q < (k == 3 ? NQ : k * NQ / 4); ++q) load(q, ahead);
+      }
+      if (!mine) continue;
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[k & 1][i], b[k & 1][j], acc[i][j], 0, 0, 0);
+      // memory instructions between the products, so that the matrix core does
+      // not wait for an issue slot
+#pragma unroll
+      for (int q = 0; LATE && q < NI * NJ; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                       // product
+        if (q < NI + NJ) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);      // LDS read
+        else if (k < 3) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);       // LDS write
+        if (q >= NI + NJ && k > 0 && (k == 3 || q % 2)) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // load
+      }
+    }
   }
-  read(lds[(steps - 1) & 1], get1, a1, b1);
-  multiply(a0, b0);
-  multiply(a1, b1);
+  if constexpr (KS > 1) {
+    // the parts' sums added up, one part after the other in the same LDS
+    i32x16* sums = reinterpret_cast<i32x16*>(all_lds);   // [wave][tile][lane]
+    static_assert(4 * NI * NJ * 64 * 64 <= (int)sizeof(all_lds), "the sums fit");
+    for (int from = 1; from < KS; ++from) {
+      __syncthreads();
+      if (part == from) {
+#pragma unroll
+        for (int n = 0; n < NI * NJ; ++n) sums[(wave * NI * NJ + n) * 64 + lane] = acc[n / NJ][n % NJ];
+      }
+      __syncthreads();
+      if (part == 0) {
+#pragma unroll
+        for (int n = 0; n < NI * NJ; ++n) acc[n / NJ][n % NJ] += sums[(wave * NI * NJ + n) * 64 + lane];
+      }
+    }
+    if (part != 0) return;
+  }
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const int tok = t0 + wt + 16 * j + li;
+    const int tok = t0 + wt + 32 * j + li;
     if (tok >= p.n_tok) continue;
     const float xd = p.xd[tok];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) store_four<DST>(p, tok, o0 + wo + 16 * i + 4 * lk, acc[i][j], xd);
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        store_four<DST>(p, tok, o0 + wo + 32 * i + 2 * e + 4 * lh,
+                        i32x4{acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]}, xd);
   }
 }
 
@@ -383,26 +422,49 @@ int launch_few(const Product& p, hipStream_t s) {
   return qr_check_launch("k_matmul_i8_few");
 }
 
-template <int DST, int NI, int NJ>
+template <int DST, int NI, int NJ, int KS>
 int launch_tile(const Product& p, hipStream_t s) {
-  const int out_tiles = (p.n_out + 32 * NI - 1) / (32 * NI), tok_tiles = (p.n_tok + 32 * NJ - 1) / (32 * NJ);
+  const int out_tiles = (p.n_out + 64 * NI - 1) / (64 * NI), tok_tiles = (p.n_tok + 64 * NJ - 1) / (64 * NJ);
   const int64_t tiles = (int64_t)out_tiles * tok_tiles;
-  if (tiles > UINT32_MAX / 256) return qr_fail(QR_EOVERFLOW, "n_out and n_tok need too many tiles for one launch");
-  hipLaunchKernelGGL((k_matmul_i8_tile<DST, NI, NJ>), dim3((uint32_t)tiles), dim3(256), 0, s, p, out_tiles, tok_tiles);
+  if (tiles > UINT32_MAX / (256 * KS)) return qr_fail(QR_EOVERFLOW, "n_out and n_tok need too many tiles for one launch");
+  hipLaunchKernelGGL((k_matmul_i8_tile<DST, NI, NJ, KS>), dim3((uint32_t)tiles), dim3(256 * KS), 0, s, p, out_tiles, tok_tiles);
   return qr_check_launch("k_matmul_i8_tile");
 }
 
+int64_t tiles_of(const Product& p, int out, int tok) {
+  return (int64_t)((p.n_out + out - 1) / out) * ((p.n_tok + tok - 1) / tok);
+}
+
+// The tile: as large as leaves the chip's 256 CUs a workgroup each (an LDS
+// byte then serves more products), and below that the sum split inside a
+// workgroup, so that a CU has 8 or 16 waves at work. Measured, us (channels x
+// values 4096 x 4096 unless said), the choice first:
+//   16 tokens            k_few 1: 11      64x64 in four parts: 14
+//   24 x 11008 channels  64x64 in four: 15     k_few 2: 23
+//   48 tokens            k_few 4: 12           64x64 in four: 14
+//   64 x 11008           64x64 in four: 17     k_few 4: 34
+//   128 x 11008          64x128 in two: 21     64x64 in four: 29
+//   512                  64x128 in two: 20     64x64 in four: 27
+//   1024                 128x128 in two: 29    64x128 in two: 37
+//   1500                 128x128: 44           128x128 in two: 53
+//   4096                 256x256: 82           128x128: 96
+//   700 x 11008 (129 tiles of 256x256)         128x128: 70    256x256: 74
 template <int DST>
 int launch_product(const Product& p, hipStream_t s) {
+  constexpr int64_t CUS = 256;
   if (p.n_tok <= 16) return launch_few<DST, 1>(p, s);
-  if (p.n_tok <= 32) return launch_few<DST, 2>(p, s);
-  if (p.n_tok <= 64) return launch_few<DST, 4>(p, s);
-  // the largest tile that still gives most CUs (256) one
-  const int64_t big = (int64_t)((p.n_out + 255) / 256) * ((p.n_tok + 255) / 256);
-  if (big >= 200) return launch_tile<DST, 8, 8>(p, s);
-  const int64_t mid = (int64_t)((p.n_out + 127) / 128) * ((p.n_tok + 127) / 128);
-  if (mid >= 200) return launch_tile<DST, 4, 4>(p, s);
-  return launch_tile<DST, 2, 4>(p, s);
+  const int64_t t64 = tiles_of(p, 64, 64);
+  if (p.n_tok <= 64 && t64 < 96) {   // few channels too
+    if (p.n_tok > 32 && tiles_of(p, 16, 64) >= CUS) return launch_few<DST, 4>(p, s);
+    return launch_few<DST, 2>(p, s);
+  }
+  if (t64 <= CUS) return launch_tile<DST, 1, 1, 4>(p, s);
+  if (tiles_of(p, 64, 128) <= CUS) return launch_tile<DST, 1, 2, 2>(p, s);
+  if (tiles_of(p, 128, 128) <= CUS) return launch_tile<DST, 2, 2, 2>(p, s);
+  // 256x256 where the last round of workgroups does not leave too many idle
+  const int64_t t256 = tiles_of(p, 256, 256), rounds = (t256 + CUS - 1) / CUS;
+  if (t256 * 100 >= rounds * CUS * 65) return launch_tile<DST, 4, 4, 1>(p, s);
+  return launch_tile<DST, 2, 2, 1>(p, s);
 }
 
 }  // namespace

@@ -108,7 +108,8 @@ def check_product(sv, n_out, n_tok, n_in, dtype, bias, seed, out=None, extreme=F
 
 SHAPES = [(1, 1, 1), (5, 1, 64), (17, 3, 129), (64, 64, 128), (65, 63, 256), (200, 1, 4096), (333, 16, 1000),
           (129, 17, 640), (256, 31, 2048), (100, 32, 2500), (40, 33, 384), (130, 100, 1024), (500, 64, 4096), (257, 129, 512),
-          (300, 333, 1100), (512, 512, 256), (1000, 700, 640), (77, 2000, 192), (2304, 520, 384), (1900, 1801, 520), (3700, 3901, 200)]
+          (300, 333, 1100), (512, 512, 256), (1000, 700, 640), (77, 2000, 192), (2304, 520, 384), (1900, 1801, 520), (3700, 3901, 200), (6200, 40, 300),
+          (6145, 64, 1300), (4100, 200, 300), (2500, 2200, 140), (4096, 50, 300), (2048, 64, 700)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -118,7 +119,7 @@ def test_product(sv, n_out, n_tok, n_in, dtype):
     check_product(sv, n_out, n_tok, n_in, dtype, (n_out + n_tok) % 2 == 0, n_out + 3 * n_tok + n_in)
 
 
-@pytest.mark.parametrize("n_out,n_tok", [(70, 1), (70, 13), (140, 150)])
+@pytest.mark.parametrize("n_out,n_tok", [(70, 1), (70, 13), (70, 20), (140, 150), (6200, 30)])
 def test_product_longest_sum(sv, n_out, n_tok):
     # 131072 products of 127 * -127: the whole range of the int32 sum
     say(f"product longest {n_out}x{n_tok}")
@@ -126,7 +127,8 @@ def test_product_longest_sum(sv, n_out, n_tok):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("n_out,n_tok,pad,first", [(65, 3, 5, 0), (256, 70, 8, 8), (130, 300, 3, 1), (512, 512, 64, 0)])
+@pytest.mark.parametrize("n_out,n_tok,pad,first", [(65, 3, 5, 0), (256, 70, 8, 8), (130, 300, 3, 1), (512, 512, 64, 0),
+                                                    (4101, 200, 3, 1), (2049, 1800, 8, 4)])
 def test_product_strided_output(sv, n_out, n_tok, pad, first, dtype):
     say(f"product strided {n_out}x{n_tok} pad={pad}")
     big = torch.full((n_tok, n_out + pad), 7.0, dtype=dtype, device="cuda")
@@ -139,10 +141,10 @@ def test_product_strided_output(sv, n_out, n_tok, pad, first, dtype):
 def test_product_reproducible_and_independent_of_the_batch(sv):
     # the sum is exact: a token's outputs are the same bits in any batch
     say("product batch independence")
-    w, wd = sv.qr_quantize_rows_i8(rows(300, 1000, 1, True).cuda())
-    x, xd = sv.qr_quantize_rows_i8(rows(530, 1000, 2, True).cuda())
+    w, wd = sv.qr_quantize_rows_i8(rows(2300, 1000, 1, True).cuda())
+    x, xd = sv.qr_quantize_rows_i8(rows(2200, 1000, 2, True).cuda())
     full = sv.qr_matmul_i8(w, wd, x, xd, 1000, dtype=torch.float32)
-    for n in (1, 2, 15, 16, 17, 31, 32, 33, 64, 65, 128, 129, 256, 257):
+    for n in (1, 2, 15, 16, 17, 31, 32, 33, 64, 65, 128, 129, 256, 257, 500, 1000, 1500):
         part = sv.qr_matmul_i8(w, wd, x[:n].contiguous(), xd[:n].contiguous(), 1000, dtype=torch.float32)
         assert torch.equal(part, full[:n]), n
 
