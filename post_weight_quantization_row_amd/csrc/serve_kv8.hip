@@ -81,22 +81,28 @@ __device__ __forceinline__ int clamp_row(const Batch& b, int r) { return r < 0 ?
 // Returns the unit's number within its sequence.
 __device__ __forceinline__ int find_unit(const Batch& b, int64_t unit, int64_t mul, int shift, int pad, Span& sp) {
   const int lane = threadIdx.x & (WAVE - 1);
-  int seq = -1;
+  int seq = -1, begin = 0, end = 0, len = 0;
   for (int base = 0; base < b.n_seq; base += WAVE) {
-    bool begun = false;
-    if (base + lane < b.n_seq)
-      begun = ((int64_t)clamp_row(b, b.cu[base + lane]) * mul >> shift) + (int64_t)(base + lane) * pad <= unit;
-    const uint64_t m = __ballot(begun);
-    if (m != 0) seq = base + 63 - __builtin_clzll(m);
+    // what the sequence's span needs is asked for with what finds it
+    const int s = base + lane;
+    int from = 0, to = 0, tokens = 0;
+    if (s < b.n_seq) {
+      from = clamp_row(b, b.cu[s]);
+      to = clamp_row(b, b.cu[s + 1]);
+      tokens = b.kv_len[s];
+    }
+    const uint64_t m = __ballot(s < b.n_seq && ((int64_t)from * mul >> shift) + (int64_t)s * pad <= unit);
+    if (m != 0) {
+      const int at = 63 - __builtin_clzll(m);
+      seq = base + at;
+      begin = __builtin_amdgcn_readlane(from, at);
+      end = __builtin_amdgcn_readlane(to, at);
+      len = __builtin_amdgcn_readlane(tokens, at);
+    }
     if (m != ~0ull) break;
   }
-  seq = __builtin_amdgcn_readfirstlane(seq);
-  sp.seq = seq < 0 ? 0 : seq;
-  sp.row0 = clamp_row(b, b.cu[sp.seq]);
-  sp.n = clamp_row(b, b.cu[sp.seq + 1]) - sp.row0;
-  sp.len = b.kv_len[sp.seq];
-  if (seq < 0 || sp.n < 0) sp.n = 0;
-  return (int)(unit - (((int64_t)sp.row0 * mul >> shift) + (int64_t)sp.seq * pad));
+  sp = {seq < 0 ? 0 : seq, begin, seq < 0 || end < begin ? 0 : end - begin, len};
+  return (int)(unit - (((int64_t)begin * mul >> shift) + (int64_t)sp.seq * pad));
 }
 
 // The block in slot `slot` of a sequence's row of the table, or -1.
@@ -896,40 +902,6 @@ __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 
   const int clear_to = base + ((int)first_row + wrow) / a.group, any_to = base + ((int)first_row + wlast) / a.group;
   const int clear_from = window_of(any_to) + 1, any_from = window_of(clear_to) + 1;
 
-  h16x8 qhi[KS], qlo[F32 ? KS : 1];
-  float row_scale;
-  {
-    uint32_t top = 0;
-    float x[KS][8];
-#pragma unroll
-    for (int s = 0; s < KS; ++s)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float f = value_at<SRC>(a.q, tok * a.q_stride + (int64_t)qh * D + 16 * s + 8 * lh + i);
-        x[s][i] = f;
-        const uint32_t m = __builtin_bit_cast(uint32_t, f) & 0x7fffffffu;
-        top = m > top ? m : top;
-      }
-    const uint32_t o = (uint32_t)__shfl_xor((int)top, 32);
-    top = o > top ? o : top;
-    const bool bad = top >= 0x7f800000u;
-    const float amax = bad ? 0.0f : __builtin_bit_cast(float, top);
-    int e = 0;
-    if (amax > 0.0f) (void)__builtin_frexpf(amax, &e);
-    // the factor's sign goes to the queries: a maximum of scores is then the
-    // maximum of products
-    const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[s][i] *= sign;
-      h16x8 lo;
-      query_half<SRC>(x[s], e, qhi[s], lo);
-      if (F32) qlo[s] = lo;
-    }
-    row_scale = bad ? __builtin_nanf("") : __builtin_ldexpf(a.scale * sign, e - 14);
-  }
-
   f32x16 acc[DT] = {};
   float m_run = NEG_INF, l_run = 0.0f;
   int e_ref = E_NONE;
@@ -988,8 +960,43 @@ __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 
     }
   };
 
+  // the first tile is on its way while the queries come in
   look_up(tile0);
   fetch(tile0);
+  h16x8 qhi[KS], qlo[F32 ? KS : 1];
+  float row_scale;
+  {
+    uint32_t top = 0;
+    float x[KS][8];
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float f = value_at<SRC>(a.q, tok * a.q_stride + (int64_t)qh * D + 16 * s + 8 * lh + i);
+        x[s][i] = f;
+        const uint32_t m = __builtin_bit_cast(uint32_t, f) & 0x7fffffffu;
+        top = m > top ? m : top;
+      }
+    const uint32_t o = (uint32_t)__shfl_xor((int)top, 32);
+    top = o > top ? o : top;
+    const bool bad = top >= 0x7f800000u;
+    const float amax = bad ? 0.0f : __builtin_bit_cast(float, top);
+    int e = 0;
+    if (amax > 0.0f) (void)__builtin_frexpf(amax, &e);
+    // the factor's sign goes to the queries: a maximum of scores is then the
+    // maximum of products
+    const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[s][i] *= sign;
+      h16x8 lo;
+      query_half<SRC>(x[s], e, qhi[s], lo);
+      if (F32) qlo[s] = lo;
+    }
+    row_scale = bad ? __builtin_nanf("") : __builtin_ldexpf(a.scale * sign, e - 14);
+  }
+
   stage(0);
   fetch(tile0 + 1);
   __syncthreads();
@@ -1139,14 +1146,15 @@ __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 
   }
 }
 
-// Joins the splits of a unit of UNIT rows. Up to J_FEW splits a thread adds
-// four channels of a row, and everything it needs is loaded at once.
+// Joins the splits of a unit of UNIT rows: a thread adds four channels of a
+// row, eight splits at a time, and everything it needs of them is loaded at
+// once.
 constexpr int J_THREADS = 256;
 constexpr int J_FEW = 8;
 constexpr int MAX_SPLITS = 128;
 
 template <int SRC, int D, int UNIT, int NG>
-__global__ __launch_bounds__(J_THREADS) void k_attention_join_few(Cache c, Batch b, Attention a) {
+__global__ __launch_bounds__(J_THREADS) void k_attention_join(Cache c, Batch b, Attention a) {
   const int unit = blockIdx.x / c.n_heads, head = blockIdx.x % c.n_heads;
   Span sp;
   const int u = find_unit(b, unit, a.group, UNIT == A_ROWS ? A_SHIFT : P_SHIFT_ROWS, 1, sp);
@@ -1160,52 +1168,59 @@ __global__ __launch_bounds__(J_THREADS) void k_attention_join_few(Cache c, Batch
   if (vis.used <= 1 || row >= rows) return;
   constexpr int64_t STEP = (int64_t)UNIT * (D + 2);
   const float* part = a.part + ((int64_t)unit * c.n_heads + head) * a.n_splits * STEP;
-  float mz[J_FEW], lz[J_FEW];
-  f32x4 oz[J_FEW];
-#pragma unroll
-  for (int z = 0; z < J_FEW; ++z) {
-    const float* pz = part + (z < vis.used ? z : 0) * STEP;
-    mz[z] = pz[UNIT * D + row];
-    lz[z] = pz[UNIT * D + UNIT + row];
-    oz[z] = *reinterpret_cast<const f32x4*>(pz + row * D + ch);
-  }
   float m = NEG_INF, l = 0.0f;
-#pragma unroll
-  for (int z = 0; z < J_FEW; ++z)
-    if (z < vis.used) m = __builtin_fmaxf(m, mz[z]);
-  const float ref = m == NEG_INF ? 0.0f : m;
   f32x4 o = {};
+  for (int z0 = 0; z0 < vis.used; z0 += J_FEW) {
+    float mz[J_FEW], lz[J_FEW];
+    f32x4 oz[J_FEW];
 #pragma unroll
-  for (int z = 0; z < J_FEW; ++z)
-    if (z < vis.used) {
-      const float f = __builtin_amdgcn_exp2f(mz[z] - ref);
-      l = __builtin_fmaf(lz[z], f, l);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(oz[z][i], f, o[i]);
+    for (int k = 0; k < J_FEW; ++k) {
+      const float* pz = part + (z0 + k < vis.used ? z0 + k : z0) * STEP;
+      mz[k] = pz[UNIT * D + row];
+      lz[k] = pz[UNIT * D + UNIT + row];
+      oz[k] = *reinterpret_cast<const f32x4*>(pz + row * D + ch);
     }
+    float m_new = m;
+#pragma unroll
+    for (int k = 0; k < J_FEW; ++k) m_new = __builtin_fmaxf(m_new, mz[k]);   // (repeats change nothing)
+    const float ref = m_new == NEG_INF ? 0.0f : m_new;
+    const float down = __builtin_amdgcn_exp2f(m - ref);
+    m = m_new;
+    l *= down;
+    o *= down;
+#pragma unroll
+    for (int k = 0; k < J_FEW; ++k)
+      if (z0 + k < vis.used) {
+        const float f = __builtin_amdgcn_exp2f(mz[k] - ref);
+        l = __builtin_fmaf(lz[k], f, l);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(oz[k][i], f, o[i]);
+      }
+  }
   const int rr = (int)first_row + row;
   const int64_t to = (int64_t)(sp.row0 + rr / a.group) * a.out_stride + (int64_t)(head * a.group + rr % a.group) * D + ch;
   store_heads<SRC>(a.out, to, l == 0.0f ? f32x4{} : f32x4{o[0] / l, o[1] / l, o[2] / l, o[3] / l});
 }
 
-// More splits: a workgroup per row, each of its waves on every fourth split.
+// Many splits of 16 rows (one long sequence): a workgroup per row, each of its
+// waves on every fourth split.
 // Lane z works out the factor of split z (and z + 64); then every lane adds
 // its channels over the splits, whose loads do not wait for each other.
-template <int SRC, int D, int UNIT, int NG>
-__global__ __launch_bounds__(J_THREADS) void k_attention_join(Cache c, Batch b, Attention a) {
-  constexpr int SHARE = J_THREADS / WAVE;
+template <int SRC, int D>
+__global__ __launch_bounds__(J_THREADS) void k_attention_join_long(Cache c, Batch b, Attention a) {
+  constexpr int UNIT = A_ROWS, SHARE = J_THREADS / WAVE;
   constexpr int PER = D / WAVE;   // channels of a lane
   constexpr int BATCH = 8;        // loads in flight
   typedef float f32xp __attribute__((ext_vector_type(PER == 1 ? 2 : PER)));
   __shared__ float share_o[SHARE][D];
   const int unit = blockIdx.x / c.n_heads, head = blockIdx.x % c.n_heads;
   Span sp;
-  const int u = find_unit(b, unit, a.group, UNIT == A_ROWS ? A_SHIFT : P_SHIFT_ROWS, 1, sp);
+  const int u = find_unit(b, unit, a.group, A_SHIFT, 1, sp);
   const int64_t n_rows = (int64_t)sp.n * a.group;
   const int64_t first_row = (int64_t)u * UNIT;
   if (u < 0 || first_row >= n_rows) return;
   const int rows = (int)(n_rows - first_row < UNIT ? n_rows - first_row : UNIT);
-  const Range vis = visible(sp, (int)first_row, rows, a, (int64_t)b.table_width << c.shift, NG);
+  const Range vis = visible(sp, (int)first_row, rows, a, (int64_t)b.table_width << c.shift, 1);
   const int row = blockIdx.y;
   if (vis.used <= 1 || row >= rows) return;
   const int lane = threadIdx.x & 63, share = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
@@ -1264,11 +1279,11 @@ __global__ __launch_bounds__(J_THREADS) void k_attention_join(Cache c, Batch b, 
 
 template <int SRC, int D, int UNIT, int NG>
 void launch_join(const Cache& c, const Batch& b, const Attention& a, uint32_t blocks, hipStream_t s) {
-  if (a.n_splits <= J_FEW)
-    hipLaunchKernelGGL((k_attention_join_few<SRC, D, UNIT, NG>), dim3(blocks, (UNIT * D / 4 + J_THREADS - 1) / J_THREADS),
-                       dim3(J_THREADS), 0, s, c, b, a);
+  if (UNIT == A_ROWS && a.n_splits > J_FEW)
+    hipLaunchKernelGGL((k_attention_join_long<SRC, D>), dim3(blocks, A_ROWS), dim3(J_THREADS), 0, s, c, b, a);
   else
-    hipLaunchKernelGGL((k_attention_join<SRC, D, UNIT, NG>), dim3(blocks, UNIT), dim3(J_THREADS), 0, s, c, b, a);
+    hipLaunchKernelGGL((k_attention_join<SRC, D, UNIT, NG>), dim3(blocks, (UNIT * D / 4 + J_THREADS - 1) / J_THREADS),
+                       dim3(J_THREADS), 0, s, c, b, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -1331,7 +1346,10 @@ Cut cut_for(const qr_kv8* c, int64_t n_tok, int64_t n_seq, int64_t group, int64_
   const int64_t unit = k.many ? P_ROWS : A_ROWS;
   k.units = n_tok * group / unit + n_seq;
   const int64_t busy = n_seq * ((rows + unit - 1) / unit) * c->n_heads;
-  const int64_t most = (table_width * (c->block_tokens / GROUP) + A_MIN_GROUPS - 1) / A_MIN_GROUPS;
+  const int64_t groups = table_width * (c->block_tokens / GROUP);
+  // up to 1024 tokens one launch: 10.2 us for 700 tokens of 4 sequences,
+  // against 6.9 and 2.5 us and what lies between two launches
+  const int64_t most = !k.many && groups <= 32 ? 1 : (groups + A_MIN_GROUPS - 1) / A_MIN_GROUPS;
   const int64_t want = k.many ? 512 : 2048;   // workgroups: two, eight per CU
   k.splits = (want + busy - 1) / busy;
   if (k.splits > most) k.splits = most;
