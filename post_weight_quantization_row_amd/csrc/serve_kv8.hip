@@ -589,13 +589,14 @@ __global__ __launch_bounds__(A_WAVES * WAVE) void k_attention_kv8(Cache c, Batch
     for (int s = 0; s < KS; ++s)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
+        load_heads8<SRC>(a.q, tok * a.q_stride + (int64_t)qh * D + 64 * s + 16 * lg + 8 * h, x[2 * s + h]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float f = value_at<SRC>(a.q, tok * a.q_stride + (int64_t)qh * D + 64 * s + 16 * lg + 8 * h + i);
-          x[2 * s + h][i] = f;
-          const uint32_t m = __builtin_bit_cast(uint32_t, f) & 0x7fffffffu;
-          top = m > top ? m : top;
-        }
+    for (int s = 0; s < 2 * KS; ++s)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t m = __builtin_bit_cast(uint32_t, x[s][i]) & 0x7fffffffu;
+        top = m > top ? m : top;
+      }
 #pragma unroll
     for (int s = 16; s < 64; s <<= 1) {
       const uint32_t o = (uint32_t)__shfl_xor((int)top, s);
@@ -970,11 +971,12 @@ __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 
     float x[KS][8];
 #pragma unroll
     for (int s = 0; s < KS; ++s)
+      load_heads8<SRC>(a.q, tok * a.q_stride + (int64_t)qh * D + 16 * s + 8 * lh, x[s]);
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float f = value_at<SRC>(a.q, tok * a.q_stride + (int64_t)qh * D + 16 * s + 8 * lh + i);
-        x[s][i] = f;
-        const uint32_t m = __builtin_bit_cast(uint32_t, f) & 0x7fffffffu;
+        const uint32_t m = __builtin_bit_cast(uint32_t, x[s][i]) & 0x7fffffffu;
         top = m > top ? m : top;
       }
     const uint32_t o = (uint32_t)__shfl_xor((int)top, 32);

@@ -219,6 +219,15 @@ def test_one_long_sequence_splits(sv, bf16):
 
 
 @pytest.mark.parametrize("bf16", [True, False])
+def test_many_groups_for_one_workgroup(sv, bf16):
+    """So many sequences and heads that no tokens are split: blocks and
+    scales are looked up several times within a workgroup."""
+    say(f"unsplit bf16={bf16}")
+    check_attention(sv, [8400] + [1] * 31, [1] * 32, 1, 64, 64, 32, bf16, seed=21)
+    check_attention(sv, [2300] + [60] * 7, [130] + [60] * 7, 1, 64, 64, 64, bf16, seed=22)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
 @pytest.mark.parametrize("new", [[60, 9, 33, 100], [1, 1, 1, 1], [40, 90, 200, 100]])
 def test_absent_tokens_and_empty_rows(sv, new, bf16):
     """Evicted and out-of-range blocks, rows before position 0, a sequence
@@ -243,7 +252,34 @@ def test_negative_scale_factor_and_zero(sv):
     say("scale factors")
     for scale in (-0.2, 0.0, 1e-20):
         check_attention(sv, [130, 70], [1, 70], 2, 1, 64, 32, True, seed=2, scale=scale)
+        check_attention(sv, [130, 70], [1, 2], 2, 1, 64, 32, True, seed=2, scale=scale)
 
+
+def test_rows_before_the_first_sequence(sv):
+    """A part of a batch: cu starts behind rows of others."""
+    say("part of a batch")
+    rng = np.random.default_rng(13)
+    lens, table = [70, 40], plain.table_for([70, 40], 32, 8, rng)
+    cache = sv.kv8_cache(8, 2, 64, 32, "cuda")
+    k, v = [x.cuda() for x in make_kv(110, 2, 64, 3, True)]
+    sv.qr_kv8_append(cache, k, v, dev([0, 70, 110]), dev(lens), dev(table))
+    q = torch.randn((100, 4, 64), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    for new in ([1, 3], [30, 20]):
+        cu = plain.offsets(new)
+        want = sv.qr_attention_kv8(q[:cu[-1]], cache, dev(cu), dev(lens), dev(table))
+        shifted = torch.cat([q[:50], q[:cu[-1]]])
+        out = torch.full_like(shifted, 7.0)
+        sv.qr_attention_kv8(shifted, cache, dev([50 + c for c in cu]), dev(lens), dev(table), out=out)
+        assert bool((out[:50] == 7).all())
+        # (the two calls may take different kernels: each output within half a
+        # step of bf16 and 2^-10 of the values' size of the exact one)
+        got, ref = out[50:].double(), want.double()
+        big = float(v.abs().max())
+        assert bool(((got - ref).abs() <= 2 * (2.0 ** -8 * ref.abs() + 2.0 ** -10 * big)).all())
+        read = sv.qr_kv8_read(cache, dev([50 + c for c in cu]), dev(lens), dev(table), 50 + cu[-1], k=torch.full(
+            (50 + cu[-1], 2, 64), 7.0, device="cuda"))
+        assert bool((read[0][:50] == 7).all())
+        assert torch.equal(read[0][50:], sv.qr_kv8_read(cache, dev(cu), dev(lens), dev(table), cu[-1])[0])
 
 @pytest.mark.parametrize("new", [[1, 1], [128, 200]])
 def test_nan_blocks_reach_only_the_rows_that_see_them(sv, new):
