@@ -100,6 +100,18 @@ def _call(device, stream, fn, *args):
         _check(rc)
 
 
+def _new(shape, dtype, device, stream):
+    """A new tensor for a call on `stream`: from that stream's memory, so that
+    neither what ran on the block before nor what gets it next overlaps the
+    call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _given(t, name: str, shape, dtype, device):
     _on(t, name, device)
     if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
@@ -136,11 +148,11 @@ def qr_quantize_rows_i8(x: torch.Tensor, codes=None, scales=None, stream=None):
     # (outside 1 .. I8_MAX_IN the library refuses the call)
     row_bytes = (n + 127) // 128 * 128 if 0 < n <= I8_MAX_IN else 0
     if codes is None:
-        codes = torch.empty((n_rows, row_bytes), dtype=torch.int8, device=device)
+        codes = _new((n_rows, row_bytes), torch.int8, device, stream)
     else:
         _given(codes, "codes", (n_rows, row_bytes), torch.int8, device)
     if scales is None:
-        scales = torch.empty(n_rows, dtype=torch.float32, device=device)
+        scales = _new(n_rows, torch.float32, device, stream)
     else:
         _given(scales, "scales", (n_rows,), torch.float32, device)
     _call(device, stream, load_library().qr_quantize_rows_i8, src, x.data_ptr(), n_rows, n, stride, codes.data_ptr(),
@@ -174,7 +186,7 @@ def qr_matmul_i8(w: torch.Tensor, wd: torch.Tensor, x: torch.Tensor, xd: torch.T
     if bias is not None:
         _given(bias, "bias", (n_out,), torch.float32, device)
     if out is None:
-        out = torch.empty((n_tok, n_out), dtype=dtype, device=device)
+        out = _new((n_tok, n_out), dtype, device, stream)
         stride = n_out
     else:
         _on(out, "out", device)
@@ -305,9 +317,9 @@ def qr_kv8_read(cache: Kv8Cache, cu: torch.Tensor, kv_len: torch.Tensor, table: 
     n_seq, width = _batch(cu, kv_len, table, device)
     shape = (n_tok, cache.n_heads, cache.head_dim)
     if k is None:
-        k = torch.empty(shape, dtype=dtype, device=device)
+        k = _new(shape, dtype, device, stream)
     if v is None:
-        v = torch.empty(shape, dtype=dtype, device=device)
+        v = _new(shape, dtype, device, stream)
     ks = _heads(k, "k", *shape, device)
     vs = _heads(v, "v", *shape, device)
     dst = _dtype_id(k, "k")
@@ -341,7 +353,7 @@ def qr_attention_kv8(q: torch.Tensor, cache: Kv8Cache, cu: torch.Tensor, kv_len:
     n_tok, n_q, dim = q.shape
     qs = _heads(q, "q", n_tok, n_q, cache.head_dim, device)
     if out is None:
-        out = torch.empty((n_tok, n_q, dim), dtype=q.dtype, device=device)
+        out = _new((n_tok, n_q, dim), q.dtype, device, stream)
         os_ = n_q * dim
     else:
         os_ = _heads(out, "out", n_tok, n_q, dim, device)
@@ -357,9 +369,7 @@ def qr_attention_kv8(q: torch.Tensor, cache: Kv8Cache, cu: torch.Tensor, kv_len:
     else:
         ws_bytes = lib.qr_attention_kv8_workspace_bytes(C.byref(c), n_q, n_tok, n_seq, width)
         if ws_bytes:
-            if stream is not None:
-                raise ValueError("a call on a stream of its own needs a workspace of its own")
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+            workspace = _new(ws_bytes, torch.uint8, device, stream)
             ws = workspace.data_ptr()
     _call(device, stream, lib.qr_attention_kv8, C.byref(c), src, q.data_ptr(), qs, n_q, n_tok, n_seq, cu.data_ptr(),
           kv_len.data_ptr(), table.data_ptr(), width, dim ** -0.5 if scale is None else scale, window, out.data_ptr(),

@@ -345,6 +345,35 @@ def test_offsets_past_32_bits(sv):
     assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
 
 
+def test_calls_on_a_stream_of_their_own(sv):
+    """Outputs and scratch that the calls allocate belong to the stream they
+    are given, as a torch stream or as a handle."""
+    say("own stream")
+    heads, dim, block, n = 2, 64, 32, 1500
+    table, cu, lens = dev([np.arange(50)]), dev([0, n]), dev([n])
+    k, v = [x.cuda() for x in make_kv(n, heads, dim, 3, True)]
+    q = k.repeat(1, 2, 1)[:3].contiguous()
+    one = dev([0, 3])
+    w, wd = sv.qr_quantize_rows_i8(torch.randn((200, 4 * dim), device="cuda"))
+
+    def chain(stream):
+        cache = fresh(sv, 50, heads, dim, block)
+        torch.cuda.synchronize()
+        sv.qr_kv8_append(cache, k, v, cu, lens, table, stream=stream)
+        o = sv.qr_attention_kv8(q, cache, one, lens, table, stream=stream)
+        back = sv.qr_kv8_read(cache, cu, lens, table, n, stream=stream)
+        x, xd = sv.qr_quantize_rows_i8(o.view(3, -1), stream=stream)
+        y = sv.qr_matmul_i8(w, wd, x, xd, 4 * dim, stream=stream)
+        torch.cuda.synchronize()
+        return o, *back, x, xd, y
+
+    want = chain(None)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        for a, b in zip(chain(stream), want):
+            assert torch.equal(a, b)
+
+
 def test_graph_of_a_decode_step(sv):
     """Quantized projections, append and attention captured once and replayed
     with other lengths, against the same calls made eagerly."""

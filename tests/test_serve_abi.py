@@ -231,8 +231,6 @@ def test_binding_refuses_wrong_tensors(lib, monkeypatch):
         lambda: serve.qr_kv8_read(kv, cu, ln, tab, 4, k=z(3, 2, 64), v=z(3, 2, 64)),
         lambda: serve.qr_attention_kv8(z(4, 4, 128), kv, cu, ln, tab),
         lambda: serve.qr_attention_kv8(q, kv, cu, ln, tab, out=z(4, 2, 64)),
-        # an own stream and no workspace of its own
-        lambda: serve.qr_attention_kv8(q, kv, cu, ln, tab_long, out=q, stream=1),
     ]
     for f in values:
         with pytest.raises(ValueError):
