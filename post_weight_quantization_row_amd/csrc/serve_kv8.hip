@@ -283,7 +283,7 @@ __device__ __forceinline__ void append_few(const Cache& c, const Piece& p, int h
 }
 
 // Each new value is read once and stays in registers between the block's
-// maximum and its codes: bound by those bytes (12560 bf16 tokens of 8 heads of
+// maximum and its codes: bound by those bytes (12545 bf16 tokens of 8 heads of
 // 128: 21.8 us, 3.5 TB/s; by single elements, read twice: 45 us).
 template <int SRC, int D, int SQ, bool VALUES>
 __device__ __forceinline__ void append_piece(const Cache& c, const Piece& p, int head, const void* __restrict__ x,
@@ -441,7 +441,7 @@ __device__ __forceinline__ void read_piece(const Cache& c, const Piece& p, int h
   }
 }
 
-// The decoder, over the same pieces: bound by the values it writes (12560
+// The decoder, over the same pieces: bound by the values it writes (12545
 // tokens of 8 heads of 128 to fp32: 24.8 us, 5.2 TB/s).
 template <int DST, int D>
 __global__ __launch_bounds__(RW_THREADS) void k_kv8_read(Cache c, Batch b, void* __restrict__ k, void* __restrict__ v,

@@ -345,6 +345,34 @@ def test_offsets_past_32_bits(sv):
     assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
 
 
+@pytest.mark.parametrize("most", [1, 3, 90])
+def test_many_sequences(sv, most):
+    """More sequences than a wave looks at at once, empty ones among them, at
+    the ends too; written, read and attended to."""
+    say(f"many sequences most={most}")
+    rng = np.random.default_rng(most)
+    n_seq, heads, dim, block = 200, 1, 64, 32
+    new = rng.integers(0, most + 1, n_seq)
+    new[[0, 63, 64, 127, 128, 199]] = [0, most, 0, most, most, 0]
+    if most == 90:
+        new = np.where(rng.random(n_seq) < 0.3, 0, np.maximum(new, 75))
+    lens = new + rng.integers(0, 40, n_seq) * (new > 0)
+    n_blocks = int(sum(-(-int(n) // block) for n in lens))
+    table = plain.table_for(lens, block, n_blocks, rng)
+    cache, ref = fresh(sv, n_blocks, heads, dim, block), plain.PlainCache(n_blocks, heads, dim, block)
+    cu = plain.offsets(lens)
+    kv = make_kv(cu[-1], heads, dim, most, True)
+    sv.qr_kv8_append(cache, kv[0].cuda(), kv[1].cuda(), dev(cu), dev(lens), dev(table))
+    ref.append([x.float().numpy() for x in kv], cu, lens, table)
+    check_cache(cache, ref, slice(None))
+    got = sv.qr_kv8_read(cache, dev(cu), dev(lens), dev(table), cu[-1])
+    for j in range(2):
+        want = np.concatenate([ref.values(table[s], lens[s])[j] for s in range(n_seq)])
+        assert torch.equal(got[j].cpu(), torch.from_numpy(want.astype(np.float32)))
+    check_attention(sv, [int(n) for n in lens], [int(n) for n in new], 1, heads, dim, block, True, seed=most,
+                    table=table)
+
+
 def test_calls_on_a_stream_of_their_own(sv):
     """Outputs and scratch that the calls allocate belong to the stream they
     are given, as a torch stream or as a handle."""
