@@ -22,12 +22,12 @@
  * block_tokens], at p % block_tokens.
  *
  * Sequences and rows: a call brings n_tok rows; sequence s owns the rows
- * cu[s] .. cu[s+1]-1 (cu: int32 [n_seq+1], not descending, from 0 on), which are its
+ * cu[s] .. cu[s+1]-1 (cu: int32 [n_seq+1], not descending), which are its
  * LAST cu[s+1]-cu[s] tokens: row cu[s]+i is the token at position
  * kv_len[s] - (cu[s+1]-cu[s]) + i, kv_len[s] (int32 [n_seq]) counting the
- * sequence's tokens with the new ones. Rows from cu[n_seq] on belong to no
- * sequence: they are not read and what the call would write there is left as
- * it was (padded batches).
+ * sequence's tokens with the new ones. Rows before cu[0] and from cu[n_seq] on
+ * belong to no sequence: they are not read and what the call would write there
+ * is left as it was (parts of a batch, padded batches).
  *
  * What is not a token: a position below 0, one behind the table's width, one
  * whose table entry lies outside 0..n_blocks-1 (an evicted or unassigned
@@ -72,8 +72,10 @@ size_t qr_kv8_code_bytes(const qr_kv8 *c);
  * codes for its new tokens, and stays so until its first token is written again: the
  * rows that attend to it are NaN. Writing the same rows again leaves
  * the same bytes. Two rows must not fall on the same token of the same block
- * (a block that is written must belong to one sequence); blocks that are only
- * read may be shared.
+ * and no two workgroups on the same block: a block that is written belongs to
+ * one sequence and stands once in its row of the table; blocks that are only
+ * read may be shared. In a block whose first token is not among the rows, the
+ * tokens before them are taken to be there already.
  * Limits: n_seq, n_tok and table_width < 2^31. n_tok == 0 or n_seq == 0 is a no-op.
  */
 int qr_kv8_append(const qr_kv8 *c, int src, const void *k, const void *v,

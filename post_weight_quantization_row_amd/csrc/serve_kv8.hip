@@ -1360,7 +1360,10 @@ struct Cut {
 Cut cut_for(const qr_kv8* c, int64_t n_tok, int64_t n_seq, int64_t group, int64_t table_width) {
   Cut k;
   const int64_t rows = (n_tok * group + n_seq - 1) / n_seq;   // of a sequence, on average
-  k.many = rows > 48;
+  // two units of 16 rows read the tokens twice and still win (64 sequences of
+  // 1000 tokens, 32 rows each: 39 against 46 us); three do not (48 rows: 59
+  // against 51 us, 8 sequences of 2000: 30 against 24 us)
+  k.many = rows > 2 * A_ROWS;
   const int64_t unit = k.many ? P_ROWS : A_ROWS;
   k.units = n_tok * group / unit + n_seq;
   const int64_t busy = n_seq * ((rows + unit - 1) / unit) * c->n_heads;

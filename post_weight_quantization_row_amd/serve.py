@@ -105,6 +105,8 @@ def _new(shape, dtype, device, stream):
     neither what ran on the block before nor what gets it next overlaps the
     call."""
     if stream is None:
+        if len(shape) == 2:   # (with its strides a tensor is made faster)
+            return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
         return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
@@ -152,7 +154,7 @@ def qr_quantize_rows_i8(x: torch.Tensor, codes=None, scales=None, stream=None):
     else:
         _given(codes, "codes", (n_rows, row_bytes), torch.int8, device)
     if scales is None:
-        scales = _new(n_rows, torch.float32, device, stream)
+        scales = _new((n_rows,), torch.float32, device, stream)
     else:
         _given(scales, "scales", (n_rows,), torch.float32, device)
     _call(device, stream, load_library().qr_quantize_rows_i8, src, x.data_ptr(), n_rows, n, stride, codes.data_ptr(),
@@ -162,11 +164,11 @@ def qr_quantize_rows_i8(x: torch.Tensor, codes=None, scales=None, stream=None):
 
 def _i8_rows(codes, scales, name, row_bytes, device):
     _on(codes, name, device)
-    if codes.dtype != torch.int8 or codes.dim() != 2 or not codes.is_contiguous() or codes.shape[1] != row_bytes:
-        raise ValueError(f"{name} must be a contiguous int8 [n, {row_bytes}] tensor (qr_i8_row_bytes of n_in)")
-    n = codes.shape[0]
     _on(scales, name + "d", device)
-    if scales.dtype != torch.float32 or scales.shape != (n,) or not scales.is_contiguous():
+    n = codes.shape[0] if codes.dim() == 2 else -1
+    if codes.shape != (n, row_bytes) or codes.dtype != torch.int8 or not codes.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int8 [n, {row_bytes}] tensor (qr_i8_row_bytes of n_in)")
+    if scales.shape != (n,) or scales.dtype != torch.float32 or not scales.is_contiguous():
         raise ValueError(f"{name}d must be a contiguous float32 tensor with one scale per row of {name}")
     return n
 
@@ -369,7 +371,7 @@ def qr_attention_kv8(q: torch.Tensor, cache: Kv8Cache, cu: torch.Tensor, kv_len:
     else:
         ws_bytes = lib.qr_attention_kv8_workspace_bytes(C.byref(c), n_q, n_tok, n_seq, width)
         if ws_bytes:
-            workspace = _new(ws_bytes, torch.uint8, device, stream)
+            workspace = _new((ws_bytes,), torch.uint8, device, stream)
             ws = workspace.data_ptr()
     _call(device, stream, lib.qr_attention_kv8, C.byref(c), src, q.data_ptr(), qs, n_q, n_tok, n_seq, cu.data_ptr(),
           kv_len.data_ptr(), table.data_ptr(), width, dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
