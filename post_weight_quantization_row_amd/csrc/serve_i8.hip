@@ -11,11 +11,14 @@
 
 namespace {
 
-typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+// Vectors at any element of the caller's rows, whose strides are free: memory
+// instructions take them unaligned.
+typedef uint16_t u16x8_any __attribute__((ext_vector_type(8), aligned(2)));
+typedef uint16_t u16x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr int WAVE = 64;
 constexpr int ROW_ALIGN = 128;   // bytes: qr_i8_row_bytes
@@ -30,18 +33,17 @@ __device__ __forceinline__ uint16_t bf16_bits(float f) { return __builtin_bit_ca
 
 constexpr int RQ_THREADS = 256;
 
-// Eight values of a row from element `at` on; zeros behind n. `vec`: the row
-// starts on a 16-byte border, so that whole groups of eight load as vectors.
+// Eight values of a row from element `at` on; zeros behind n.
 template <int SRC>
-__device__ __forceinline__ void load8(const void* row, int at, int n, bool vec, float (&v)[8]) {
-  if (vec && at + 8 <= n) {
+__device__ __forceinline__ void load8(const void* row, int at, int n, float (&v)[8]) {
+  if (at + 8 <= n) {
     if (SRC == QR_BF16) {
-      const u16x8 h = *reinterpret_cast<const u16x8*>(reinterpret_cast<const uint16_t*>(row) + at);
+      const u16x8_any h = *reinterpret_cast<const u16x8_any*>(reinterpret_cast<const uint16_t*>(row) + at);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = bf16_value(h[i]);
     } else {
-      const f32x4* p = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(row) + at);
-      const f32x4 a = p[0], b = p[1];
+      const f32x4_any* p = reinterpret_cast<const f32x4_any*>(reinterpret_cast<const float*>(row) + at);
+      const f32x4_any a = p[0], b = p[1];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[i] = a[i];
@@ -84,7 +86,6 @@ __global__ __launch_bounds__(RQ_THREADS) void k_quantize_rows_i8(const void* __r
   const int tid = threadIdx.x;
   constexpr int ESIZE = SRC == QR_BF16 ? 2 : 4;
   const uint8_t* row = reinterpret_cast<const uint8_t*>(x) + r * x_stride * ESIZE;
-  const bool vec = ((uintptr_t)row & 15) == 0;
   const int n_vec = (int)(row_bytes >> 3);
   float keep[KEEP][8];
   // magnitudes compare as integers, and a NaN or an infinity beats every
@@ -92,7 +93,7 @@ __global__ __launch_bounds__(RQ_THREADS) void k_quantize_rows_i8(const void* __r
   uint32_t top = 0;
 #pragma unroll
   for (int k = 0; k < KEEP; ++k) {
-    load8<SRC>(row, (tid + k * RQ_THREADS) * 8, n, vec, keep[k]);
+    load8<SRC>(row, (tid + k * RQ_THREADS) * 8, n, keep[k]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t m = __builtin_bit_cast(uint32_t, keep[k][i]) & 0x7fffffffu;
@@ -101,7 +102,7 @@ __global__ __launch_bounds__(RQ_THREADS) void k_quantize_rows_i8(const void* __r
   }
   for (int g = tid + KEEP * RQ_THREADS; g < n_vec; g += RQ_THREADS) {
     float v[8];
-    load8<SRC>(row, g * 8, n, vec, v);
+    load8<SRC>(row, g * 8, n, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t m = __builtin_bit_cast(uint32_t, v[i]) & 0x7fffffffu;
@@ -133,7 +134,7 @@ __global__ __launch_bounds__(RQ_THREADS) void k_quantize_rows_i8(const void* __r
   }
   for (int g = tid + KEEP * RQ_THREADS; g < n_vec; g += RQ_THREADS) {
     float v[8];
-    load8<SRC>(row, g * 8, n, vec, v);
+    load8<SRC>(row, g * 8, n, v);
     *reinterpret_cast<u32x2*>(out + (int64_t)g * 8) = finite ? pack_codes(v, inv) : u32x2{0, 0};
   }
   if (tid == 0) scales[r] = d;
@@ -164,7 +165,6 @@ struct Product {
   void* y;
   int64_t y_stride;
   int n_out, n_tok, row_bytes;
-  bool vec;   // four neighbouring outputs store as one vector
 };
 
 // Which tile a workgroup takes. Workgroups are dealt to the 8 XCDs in turn;
@@ -202,16 +202,11 @@ __device__ __forceinline__ void store_four(const Product& p, int tok, int o, con
     float v[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = scaled(sum[e], xd, p.wd[o + e], p.bias ? p.bias[o + e] : 0.0f);
-    if (p.vec && DST == QR_BF16) {
-      *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(p.y) + at) =
-          u32x2{(uint32_t)bf16_bits(v[0]) | (uint32_t)bf16_bits(v[1]) << 16,
-                (uint32_t)bf16_bits(v[2]) | (uint32_t)bf16_bits(v[3]) << 16};
-    } else if (p.vec) {
-      *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p.y) + at) = f32x4{v[0], v[1], v[2], v[3]};
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) store_one<DST>(p.y, at + e, v[e]);
-    }
+    if (DST == QR_BF16)
+      *reinterpret_cast<u16x4_any*>(reinterpret_cast<uint16_t*>(p.y) + at) =
+          u16x4_any{bf16_bits(v[0]), bf16_bits(v[1]), bf16_bits(v[2]), bf16_bits(v[3])};
+    else
+      *reinterpret_cast<f32x4_any*>(reinterpret_cast<float*>(p.y) + at) = f32x4_any{v[0], v[1], v[2], v[3]};
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -523,8 +518,7 @@ int qr_matmul_i8(const int8_t* w, const float* wd, const int8_t* x, const float*
   if (!qr_aligned(w, 16) || !qr_aligned(x, 16) || !qr_aligned(wd, 4) || !qr_aligned(xd, 4) || !qr_aligned(bias, 4) ||
       !qr_aligned(y, dst == QR_BF16 ? 2 : 4))
     return qr_fail(QR_EINVAL_PTR, "codes must be 16-byte aligned, wd, xd, bias and y to their elements");
-  const uintptr_t four = dst == QR_BF16 ? 8 : 16;
-  const Product p = {w, x, wd, xd, bias, y, y_stride, (int)n_out, (int)n_tok, (int)rb, qr_aligned(y, four) && y_stride % 4 == 0};
+  const Product p = {w, x, wd, xd, bias, y, y_stride, (int)n_out, (int)n_tok, (int)rb};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   return dst == QR_BF16 ? launch_product<QR_BF16>(p, s) : launch_product<QR_F32>(p, s);
 }
