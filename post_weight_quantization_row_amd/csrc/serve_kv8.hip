@@ -534,6 +534,11 @@ __device__ __forceinline__ Range visible(const Span& sp, int first_row, int rows
   return r;
 }
 
+// A float of one lane, for all.
+__device__ __forceinline__ float lane_value(float x, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
+
 // Eight query values of one row as fp16 operands: the row is scaled by 2^-e
 // (its largest magnitude then lies in [2^13, 2^14)), and fp32 rows keep a
 // second part for the bits that the first one lost.
@@ -565,7 +570,7 @@ __global__ __launch_bounds__(A_WAVES * WAVE) void k_attention_kv8(Cache c, Batch
   constexpr bool F32 = SRC == QR_F32;
   __shared__ float join_o[A_WAVES][A_ROWS][D + 4];
   __shared__ float join_m[A_WAVES][A_ROWS], join_l[A_WAVES][A_ROWS];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, lg = lane >> 4;
   const int unit = blockIdx.x / c.n_heads, head = blockIdx.x % c.n_heads, split = blockIdx.y;
 
@@ -644,8 +649,8 @@ __global__ __launch_bounds__(A_WAVES * WAVE) void k_attention_kv8(Cache c, Batch
   float kd = 0.0f, vd = 0.0f;
   auto fetch = [&](int it) {
     id = __builtin_amdgcn_readlane(ids, it);
-    kd = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, kds), it));
-    vd = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, vds), it));
+    kd = lane_value(kds, it);
+    vd = lane_value(vds, it);
   };
   auto load = [&](int g) {
     if (id < 0) return;
@@ -830,11 +835,6 @@ struct Index {
 template <int D>
 __device__ __forceinline__ int k_swizzle(int r) { return D == 64 ? (r >> 1) & 7 : r & 15; }
 __device__ __forceinline__ int v_swizzle(int e) { return (e & 1) << 3 | e >> 1; }
-
-// A float of one lane, for all.
-__device__ __forceinline__ float lane_value(float x, int lane) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
-}
 
 // The value that the lane 32 further (or nearer) holds.
 __device__ __forceinline__ float other_half(float x) {
