@@ -122,8 +122,9 @@ size_t qr_attention_kv8_workspace_bytes(const qr_kv8 *c, int64_t n_q_heads,
  * exact there too (scaled by a power of two per row; elements below 2^-28 of the row's
  * largest lose bits); fp32 ones are split into two fp16 parts (22 bits). Scores, maxima, sums and outputs are fp32. The
  * weights exp(s - max) enter the second product in fp16 (bf16 rows; 2^-11
- * each) or as two fp16 parts (fp32 rows; 2^-22), and to 2^-35 of the largest
- * weight where those are smaller; their sum is taken in fp32. The result does
+ * each) or as two fp16 parts (fp32 rows; 2^-22), and to 2^-31 of the largest
+ * weight where those are smaller, whatever the scales of the blocks (up to
+ * factors of 2^70 between them); their sum is taken in fp32. The result does
  * not depend on timing; which kernel and how many splits of the tokens a call
  * takes goes by its shapes (n_tok, n_seq, heads, table_width). A batch that mixes
  * whole prompts with single tokens is right in one call and faster in two:

@@ -823,6 +823,14 @@ struct ValueScale {
 };
 
 constexpr int E_NONE = -100000;
+// A weight carries the exponent of its value scale, from 2^0 to 2^-P_FOLD of
+// the reference: with P_SHIFT, whose largest weight is 2^10, fp16 then still
+// counts weights of 2^-31 of the largest (half its smallest step is 2^-25, and
+// the scale's mantissa takes another 2^-1).
+constexpr int P_FOLD = 3;
+// How far the reference may lie below the largest scale met: outputs, below
+// 2^53 of the reference (2^31 tokens of 127 * 2^15), then stay below 2^126.
+constexpr int P_REACH = 73;
 
 template <int V>
 struct Index {
@@ -863,10 +871,12 @@ __device__ __forceinline__ ValueScale value_scale(float vd) {
 // the first product are the ones that it brings to the second.
 //
 // The value scale of a group of 32 tokens goes into the exponent of its
-// weights, relative to a power of two per row (e_ref) that follows the largest scale
-// met: no second pass over the outputs. Their sum takes the factor out again.
-// The outputs are rescaled only when a score passes the reference maximum by
-// 2^5 (the weights, at most 2^15, still fit fp16).
+// weights, relative to a power of two per wave (e_ref): no second pass over the
+// outputs. Their sum takes the factor out again. The outputs are rescaled only
+// when a score passes the reference maximum by 2^5 (the weights, at most 2^15,
+// still fit fp16), or where a group's scale lies above e_ref or more than
+// 2^P_FOLD below it: e_ref then follows, so that a group's weights keep their
+// bits whatever the scales of others.
 //
 // Bound by instruction issue: per wave, 32 rows and 64 tokens, 375 vector and 98
 // scalar instructions beside 32 products. Prompts of 4 sequences of up to 4096
@@ -921,7 +931,7 @@ __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 
 
   f32x16 acc[DT] = {};
   float m_run = NEG_INF, l_run = 0.0f;
-  int e_ref = E_NONE;
+  int e_ref = E_NONE, e_most = E_NONE;
 
   const int tile0 = vis.g0 / NG + split * vis.per;
   const int tile_end = vis.g0 / NG + (vis.n < (split + 1) * vis.per ? vis.n : (split + 1) * vis.per);
@@ -1048,8 +1058,8 @@ __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 
     if (idle) return;
     // s[g][i]: token t0 + 16 (i / 8) + 8 lh + i % 8 of this lane's row
     float f[NG], top = NEG_INF;
-    ValueScale vs[NG];
-    int e_top = e_ref;
+    float lm[NG], inv[NG];   // of the value scales, with their exponents
+    int ex[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const int t0 = tile_t0 + g * GROUP;
@@ -1059,8 +1069,9 @@ __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 
       const bool have = __builtin_amdgcn_readlane(ids, from) >= 0;
       f[g] = row_scale * lane_value(kds, from);
       f[g] = f[g] < 1e-30f ? 1e-30f : f[g];
-      vs[g] = {__builtin_amdgcn_readlane(vds.e, from), lane_value(vds.lm, from), lane_value(vds.inv, from)};
-      bool seen_any = true;
+      ex[g] = __builtin_amdgcn_readlane(vds.e, from);
+      lm[g] = lane_value(vds.lm, from);
+      inv[g] = lane_value(vds.inv, from);
       if (!have || t0 < clear_from || t0 + GROUP - 1 > clear_to) {
         // the row sees the group's tokens lo + 1 .. hi
         const int hi = have && pos >= t0 ? pos - t0 : -1, lo = low >= t0 ? low - t0 : -1;
@@ -1071,10 +1082,10 @@ __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 
           const int j = 16 * (i >> 3) + (i & 7);
           s[g][i] = (uint32_t)(j - first) < count ? s[g][i] : NEG_INF;
         }
-        seen_any = hi >= 0 && lo < GROUP - 1;
+        const bool seen_any = hi >= 0 && lo < GROUP - 1;
         if (!seen_any) {   // the group's scales, which may be NaN, stay out
           f[g] = 1.0f;
-          vs[g].lm = 0.0f;
+          lm[g] = 0.0f;
         }
       }
       float t = s[g][0];
@@ -1082,26 +1093,32 @@ __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 
       for (int i = 1; i < 16; ++i) t = __builtin_elementwise_maximum(t, s[g][i]);
       t *= f[g];
       top = t > top ? t : top;
-      e_top = seen_any && vs[g].e > e_top ? vs[g].e : e_top;
     }
     const float across = other_half(top);
     top = across > top ? across : top;
-    if (__any(top > m_run + P_LAZY || e_top > e_ref)) {
+    // outputs to the new maximum, and to a reference that serves exponent e
+    auto serves = [&](int e) { return (e <= e_ref) & ((e >= e_ref - P_FOLD) | (e == E_NONE)); };
+    auto rescale = [&](int e) __attribute__((always_inline)) {
       const float m_new = top > m_run ? top : m_run;
       const float alpha = __builtin_amdgcn_exp2f(m_run - (m_new == NEG_INF ? 0.0f : m_new));
-      const float down = __builtin_ldexpf(alpha, e_ref - e_top);
       m_run = m_new;
-      e_ref = e_top;
       l_run *= alpha;
+      e_most = e > e_most ? e : e_most;
+      int to = serves(e) ? e_ref : e;
+      to = to < e_most - P_REACH ? e_most - P_REACH : to;
+      const float by = __builtin_ldexpf(alpha, e_ref - to);
 #pragma unroll
-      for (int d = 0; d < DT; ++d) acc[d] *= down;
-    }
-    const float ref = (m_run == NEG_INF ? 0.0f : m_run) - P_SHIFT;
+      for (int d = 0; d < DT; ++d) acc[d] *= by;
+      e_ref = to;
+    };
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      int de = vs[g].e - e_ref;
-      de = de < -100 ? -100 : de > 0 ? 0 : de;
-      const float off = ((float)de + vs[g].lm) - ref;
+      // (one branch that is all but never taken)
+      if (__builtin_expect((g == 0 && __ballot(top > m_run + P_LAZY) != 0) | !serves(ex[g]), 0)) rescale(ex[g]);
+      const float ref = (m_run == NEG_INF ? 0.0f : m_run) - P_SHIFT;
+      // (no scale, or one out of reach: at most 2^-100)
+      const int de = ex[g] - e_ref < -100 ? -100 : ex[g] - e_ref;
+      const float off = ((float)de + lm[g]) - ref;
       float sum[2] = {0.0f, 0.0f};
       h16x8 phi[2], plo[2];
 #pragma unroll
@@ -1111,7 +1128,7 @@ __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 
         phi[i >> 3][i & 7] = (_Float16)p;
         if (F32) plo[i >> 3][i & 7] = (_Float16)(p - (float)phi[i >> 3][i & 7]);
       }
-      l_run = __builtin_fmaf(sum[0] + sum[1], __builtin_ldexpf(vs[g].inv, -de), l_run);
+      l_run = __builtin_fmaf(sum[0] + sum[1], __builtin_ldexpf(inv[g], -de), l_run);
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
