@@ -110,7 +110,8 @@ size_t qr_attention_kv8_workspace_bytes(const qr_kv8 *c, int64_t n_q_heads,
  *  src      QR_F32 or QR_BF16: element type of q and out.
  *  q, out   [n_tok, n_q_heads, head_dim], token t at element t * q_stride (t *
  *           out_stride), a multiple of 8, at least n_q_heads * head_dim. They
- *           must not overlap.
+ *           must not overlap (refused; parts of one buffer may lie side by
+ *           side).
  *  n_q_heads  a positive multiple of n_heads (g: see the limits).
  *  scale    finite factor of the scores (1 / sqrt(head_dim) as a rule).
  *  window   0: all positions up to the row's own; else the last `window`.

@@ -1350,6 +1350,24 @@ int check_stride(const char* what, int64_t stride, int64_t least, int64_t n_tok)
   return QR_OK;
 }
 
+// Whether any of n rows of `row` bytes, a_step bytes apart, shares memory with
+// one of the rows at b: parts of one buffer lie between each other without
+// meeting.
+bool rows_meet(const void* a_ptr, int64_t a_step, const void* b_ptr, int64_t b_step, int64_t row, int64_t n) {
+  uintptr_t a = (uintptr_t)a_ptr, b = (uintptr_t)b_ptr;
+  if (a + (uintptr_t)((n - 1) * a_step + row) <= b || b + (uintptr_t)((n - 1) * b_step + row) <= a) return false;
+  if (a_step == b_step) {
+    const int64_t apart = (int64_t)((a < b ? b - a : a - b) % (uintptr_t)a_step);
+    return apart < row || a_step - apart < row;
+  }
+  for (int64_t i = 0, j = 0; i < n && j < n;) {   // both ascend: the one that ends first goes on
+    if (a + row <= b) a += a_step, ++i;
+    else if (b + row <= a) b += b_step, ++j;
+    else return true;
+  }
+  return false;
+}
+
 int check_pointers(const qr_kv8* c, const int32_t* cu, const int32_t* kv_len, const int32_t* table, int64_t table_width) {
   if (!cu || !kv_len || (!table && table_width > 0)) return qr_fail(QR_EINVAL_PTR, "cu, kv_len and table must be non-NULL");
   if (!qr_aligned(cu, 4) || !qr_aligned(kv_len, 4) || !qr_aligned(table, 4))
@@ -1539,6 +1557,9 @@ int qr_attention_kv8(const qr_kv8* c, int src, const void* q, int64_t q_stride, 
     return qr_fail(QR_EINVAL_PTR, "workspace must be non-NULL and 256-byte aligned");
   if (workspace_bytes < need)
     return qr_fail(QR_EINVAL_SHAPE, "workspace has %zu bytes, %zu are needed", workspace_bytes, need);
+  const int64_t esize = src == QR_BF16 ? 2 : 4;
+  if (rows_meet(q, q_stride * esize, out, out_stride * esize, n_q_heads * c->head_dim * esize, n_tok))
+    return qr_fail(QR_EINVAL_PTR, "q and out must not overlap");
   const Cache cc = device_cache(c);
   const Batch b = {cu, kv_len, table, (int)table_width, (int)n_seq, (int)n_tok};
   const Attention a = {q, out, reinterpret_cast<float*>(workspace), q_stride, out_stride, scale * 1.44269504088896340736f,

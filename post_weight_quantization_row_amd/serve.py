@@ -344,8 +344,8 @@ def qr_attention_kv8(q: torch.Tensor, cache: Kv8Cache, cu: torch.Tensor, kv_len:
     qr_kv8_append, scale 1/sqrt(head_dim) by default, window 0 or the number
     of last tokens that a row sees. workspace: a CUDA uint8 tensor of at least
     qr_attention_kv8_workspace_bytes bytes, or None to have one allocated
-    here. Rows from cu[n_seq] on are left as they were in `out` (undefined in
-    a new one)."""
+    here. out must not overlap q. Rows from cu[n_seq] on are left as they were
+    in `out` (undefined in a new one)."""
     device = _device(q, "q")
     c = _cache(cache, device)
     n_seq, width = _batch(cu, kv_len, table, device)
