@@ -86,7 +86,7 @@ int qr_kv8_append(const qr_kv8 *c, int src, const void *k, const void *v,
 /*
  * qr_kv8_read -- the decoder: the values of the same rows, scale * code
  * rounded to dst (QR_F32 or QR_BF16), into k and v [n_tok, n_heads, head_dim]
- * (strides as in qr_kv8_append). With cu counting whole sequences it returns
+ * (strides as in qr_kv8_append), which must not overlap. With cu counting whole sequences it returns
  * the whole cache of each.
  */
 int qr_kv8_read(const qr_kv8 *c, int dst, void *k, void *v, int64_t k_stride,

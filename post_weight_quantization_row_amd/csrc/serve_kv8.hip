@@ -1504,6 +1504,9 @@ int qr_kv8_read(const qr_kv8* c, int dst, void* k, void* v, int64_t k_stride, in
   int64_t units;
   const int rc = check_rows(c, dst, k, v, k_stride, v_stride, n_tok, n_seq, cu, kv_len, table, table_width, &units);
   if (rc != QR_OK || units == 0) return rc;
+  const int64_t esize = dst == QR_BF16 ? 2 : 4;
+  if (rows_meet(k, k_stride * esize, v, v_stride * esize, c->n_heads * c->head_dim * esize, n_tok))
+    return qr_fail(QR_EINVAL_PTR, "k and v must not overlap");
   const Cache cc = device_cache(c);
   const Batch b = {cu, kv_len, table, (int)table_width, (int)n_seq, (int)n_tok};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);

@@ -47,3 +47,17 @@ def test_attention_refuses_an_output_over_its_queries(src, esize):
 
     met = [check(call, n, 256, sa, sb, at, esize) for n, sa, sb, at in CASES]
     assert any(met) and not all(met)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: only where no GPU can reach them")
+@pytest.mark.parametrize("dst,esize", [(0, 4), (1, 2)])
+def test_read_refuses_keys_over_values(dst, esize):
+    L = serve.load_library()
+
+    def call(f, k, v, n, ks, vs):
+        return f(C.byref(cache(n_heads=4)), dst, k, v, ks, vs, n, 2, FAKE, FAKE, FAKE, 3, None)
+
+    met = [check(lambda *a: call(L.qr_kv8_read, *a), n, 256, sa, sb, at, esize) for n, sa, sb, at in CASES]
+    assert any(met) and not all(met)
+    # what is only read may be shared
+    assert call(L.qr_kv8_append, C.c_void_p(BASE), C.c_void_p(BASE), 3, 256, 256) == QR_EDEVICE
