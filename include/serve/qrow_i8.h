@@ -68,8 +68,10 @@ int qr_quantize_rows_i8(int src, const void *x, int64_t n_rows,
  * they are: -128 is allowed in codes made elsewhere up to n_in = 131071.
  * Codes behind n_in up to the row's end must be zero, as qr_quantize_rows_i8
  * writes them.
- * Limits: 1 <= n_in <= QR_I8_MAX_IN; n_out, n_tok < 2^31. n_out == 0 or
- * n_tok == 0 is a no-op.
+ * Limits: 1 <= n_in <= QR_I8_MAX_IN; n_out, n_tok < 2^31 - 256, and what one
+ * launch holds: n_out <= 16 * (2^23 - 1) with up to 16 tokens, else
+ * ceil(n_out / 256) * ceil(n_tok / 256) < 2^24. n_out == 0 or n_tok == 0 is a
+ * no-op.
  */
 int qr_matmul_i8(const int8_t *w, const float *wd, const int8_t *x,
                  const float *xd, const float *bias, int64_t n_out,

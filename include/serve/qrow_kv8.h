@@ -76,7 +76,9 @@ size_t qr_kv8_code_bytes(const qr_kv8 *c);
  * one sequence and stands once in its row of the table; blocks that are only
  * read may be shared. In a block whose first token is not among the rows, the
  * tokens before them are taken to be there already.
- * Limits: n_seq, n_tok and table_width < 2^31. n_tok == 0 or n_seq == 0 is a no-op.
+ * Limits: n_seq, n_tok and table_width < 2^31, and what one launch holds:
+ * (n_tok / block_tokens + 2 * n_seq) * n_heads < 2^24. n_tok == 0 or n_seq == 0
+ * is a no-op.
  */
 int qr_kv8_append(const qr_kv8 *c, int src, const void *k, const void *v,
                   int64_t k_stride, int64_t v_stride, int64_t n_tok,
@@ -86,7 +88,7 @@ int qr_kv8_append(const qr_kv8 *c, int src, const void *k, const void *v,
 /*
  * qr_kv8_read -- the decoder: the values of the same rows, scale * code
  * rounded to dst (QR_F32 or QR_BF16), into k and v [n_tok, n_heads, head_dim]
- * (strides as in qr_kv8_append), which must not overlap. With cu counting whole sequences it returns
+ * (strides and limits as in qr_kv8_append), which must not overlap. With cu counting whole sequences it returns
  * the whole cache of each.
  */
 int qr_kv8_read(const qr_kv8 *c, int dst, void *k, void *v, int64_t k_stride,
@@ -118,7 +120,10 @@ size_t qr_attention_kv8_workspace_bytes(const qr_kv8 *c, int64_t n_q_heads,
  *  workspace  at least qr_attention_kv8_workspace_bytes(...) bytes, 256-byte
  *           aligned, not shared by calls that may overlap; contents do not
  *           matter and are clobbered.
- * Limits: 1 <= g <= 1024; n_tok * n_q_heads < 2^31.
+ * Limits: 1 <= g <= 1024; n_tok * n_q_heads < 2^31; n_seq, n_tok and
+ * table_width < 2^31, and what one launch holds: (n_tok * g / 128 + n_seq) *
+ * n_heads < 2^24, with 16 in place of 128 where the sequences have up to 32
+ * rows (tokens times g) on average.
  * Numerics: the codes are exact as fp16 matrix operands. bf16 queries are
  * exact there too (scaled by a power of two per row; elements below 2^-28 of the row's
  * largest lose bits); fp32 ones are split into two fp16 parts (22 bits). Scores, maxima, sums and outputs are fp32. The
