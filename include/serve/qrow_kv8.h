@@ -87,7 +87,7 @@ int qr_kv8_append(const qr_kv8 *c, int src, const void *k, const void *v,
 
 /*
  * qr_kv8_read -- the decoder: the values of the same rows, scale * code
- * rounded to dst (QR_F32 or QR_BF16), into k and v [n_tok, n_heads, head_dim]
+ * rounded to fp32 and then to dst (QR_F32 or QR_BF16), into k and v [n_tok, n_heads, head_dim]
  * (strides and limits as in qr_kv8_append), which must not overlap. With cu counting whole sequences it returns
  * the whole cache of each.
  */
@@ -130,7 +130,9 @@ size_t qr_attention_kv8_workspace_bytes(const qr_kv8 *c, int64_t n_q_heads,
  * weights exp(s - max) enter the second product in fp16 (bf16 rows; 2^-11
  * each) or as two fp16 parts (fp32 rows; 2^-22), and to 2^-31 of the largest
  * weight where those are smaller, whatever the scales of the blocks (up to
- * factors of 2^70 between them); their sum is taken in fp32. The result does
+ * factors of 2^70 between them); their sum is taken in fp32. Sums are held
+ * undivided, with weights of up to 2^15: values above 2^112 / (tokens that the
+ * row sees) may give infinities. The result does
  * not depend on timing; which kernel and how many splits of the tokens a call
  * takes goes by its shapes (n_tok, n_seq, heads, table_width). A batch that mixes
  * whole prompts with single tokens is right in one call and faster in two:
