@@ -61,6 +61,12 @@ def load_library():
 # The checks below read each property once and build nothing: a decode step
 # makes many small calls, and their time on the host counts.
 
+# The handle of a device's current stream. The public call builds an object for
+# it first: 1.9 us a call, against 0.1 us.
+_current_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                   or (lambda index: torch.cuda.current_stream(index).cuda_stream))
+
+
 def _device(t, name: str):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
@@ -87,11 +93,10 @@ def _call(device, stream, fn, *args):
     """fn(*args, stream) with `device` current, as a launch on its stream
     needs; stream None is torch's current one on the device."""
     if stream is None:
-        # (torch.cuda.current_stream builds an object for the same handle)
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
+        handle = _current_stream(device.index)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch._C._cuda_getDevice() == device.index:
+    if torch.cuda.current_device() == device.index:
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(device):
