@@ -27,7 +27,7 @@ def dev(a, dtype=torch.int32):
     return torch.tensor(np.asarray(a), dtype=dtype, device="cuda")
 
 
-def attention(q, ref, n_new, length, table_row, scale, window, fp16_weights):
+def attention(q, ref, n_new, length, table_row, scale, window, fp16_weights, floor=2.0 ** -31):
     """(out, bound) of the last n_new tokens of one sequence in 64 bits, q
     float64 [n_new, n_q, dim].
 
@@ -56,7 +56,7 @@ def attention(q, ref, n_new, length, table_row, scale, window, fp16_weights):
             e = (2 * dim + 12) * u * mag + u * (spread * 1.5 + 11) + (3 * (len(idx) // 32 + 2) + 608) * u
             e += 2.0 ** -11 if fp16_weights else 2.0 ** -22
             bound[i, h] = (e * ((w @ np.abs(vv)) / tot + np.abs(out[i, h]))
-                           + 2.0 ** -31 / tot * np.sum(np.abs(vv), axis=0))
+                           + floor / tot * np.sum(np.abs(vv), axis=0))
     step = 2.0 ** -8 if fp16_weights else 2.0 ** -24     # the output type's
     return out, bound + step * (np.abs(out) + bound)
 
@@ -160,3 +160,51 @@ def test_weights_of_quiet_tokens_one_by_one(sv, far, loud):
         want = np.where(seen[:, None], value / (seen.sum() + others), 0.0).T.repeat(group, axis=0)
         off = np.abs(got[i] - want) / np.where(want > 0, want, 1.0)
         assert off.max() <= 2.0 ** -22 + 83 * 2.0 ** -24, f"row {i}: {off.max():.3g}"
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("n_new", [120, 50, 1])
+@pytest.mark.parametrize("zero", [[0], [2], [0, 1, 2], [4], [0, 1, 2, 3, 4]])
+def test_blocks_of_scale_zero(sv, zero, n_new, bf16):
+    """Their codes stand for zeros, whatever they are."""
+    say(f"zero blocks={zero} bf16={bf16} new={n_new}")
+    for dim in (64, 128, 256):
+        rng = np.random.default_rng(dim)
+        ref = plain.PlainCache(5, 1, dim, 32)
+        for j in range(2):
+            ref.codes[j][:] = rng.integers(-127, 128, ref.codes[j].shape)
+            ref.scales[j][:] = 0.01 * np.exp(rng.standard_normal(ref.scales[j].shape))
+        ref.scales[1][zero] = 0
+        table = np.arange(5, dtype=np.int32)[None]
+        q = torch.randn((n_new, 2, dim), generator=torch.Generator().manual_seed(n_new))
+        q = q.to(torch.bfloat16) if bf16 else q
+        cache = sv.Kv8Cache(*[t.cuda() for t in ref.device_tensors()])
+        out = sv.qr_attention_kv8(q.cuda(), cache, dev([0, n_new]), dev([155]), dev(table))
+        want, bound = attention(q.double().numpy(), ref, n_new, 155, table[0], dim ** -0.5, 0, bf16)
+        assert np.all(np.abs(out.double().cpu().numpy() - want) <= bound)
+
+
+@pytest.mark.parametrize("loud", [0, 2, 4])
+@pytest.mark.parametrize("far", [80, 95, 120])
+def test_scales_out_of_reach_of_each_other(sv, far, loud):
+    """Beyond factors of 2^70 weights lose a bit for each bit of distance, and
+    nothing overflows."""
+    for n_new, away in ((50, 42.0), (50, 0.5), (1, 42.0)):
+        say(f"out of reach far={far} slot={loud} new={n_new}")
+        dim, heads = 128, 1
+        rng = np.random.default_rng(far)
+        ref = plain.PlainCache(5, heads, dim, 32)
+        for j in range(2):
+            ref.codes[j][:] = rng.integers(-127, 128, ref.codes[j].shape)
+            ref.scales[j][:] = 0.01
+        ref.codes[0][loud] = -127
+        ref.scales[0][loud] = away / (127 * dim ** 0.5)
+        ref.scales[1][:] = np.float32(2.0 ** -far)
+        ref.scales[1][loud] = 1.0
+        table = np.arange(5, dtype=np.int32)[None]
+        q = torch.ones((n_new, 2, dim))
+        cache = sv.Kv8Cache(*[t.cuda() for t in ref.device_tensors()])
+        out = sv.qr_attention_kv8(q.cuda(), cache, dev([0, n_new]), dev([155]), dev(table)).double().cpu().numpy()
+        floor = min(1.0, 2.0 ** (-31 + far - 70))
+        want, bound = attention(q.double().numpy(), ref, n_new, 155, table[0], dim ** -0.5, 0, False, floor)
+        assert np.all(np.isfinite(out)) and np.all(np.abs(out - want) <= bound)
