@@ -64,8 +64,8 @@ size_t qr_kv8_code_bytes(const qr_kv8 *c);
  *  k, v     [n_tok, n_heads, head_dim], token t at element t * k_stride (t *
  *           v_stride), a multiple of 8, at least n_heads * head_dim.
  * Per block and head, for k and v apart: amax = max |x| of the new tokens in
- * the block, cand = amax / 127 (0 if 1 / cand is not finite). In a block whose first token is new the scale
- * becomes cand. Otherwise scale = max(old, cand), and where it grew the codes
+ * the block, cand = amax / 127 (0 if 1 / cand is not finite). In a block whose
+ * first token is new the scale becomes cand. Otherwise scale = max(old, cand), and where it grew the codes
  * c of the tokens before become rint(c * (old / scale)). The new codes are rint(x * (1 / scale)),
  * clamped to -127..127 (0 where the scale is 0). Every operation is rounded
  * to fp32 once. A block that gets an infinity or a NaN gets scale NaN and zero
@@ -125,16 +125,18 @@ size_t qr_attention_kv8_workspace_bytes(const qr_kv8 *c, int64_t n_q_heads,
  * n_heads < 2^24, with 16 in place of 128 where the sequences have up to 32
  * rows (tokens times g) on average.
  * Numerics: the codes are exact as fp16 matrix operands. bf16 queries are
- * exact there too (scaled by a power of two per row; elements below 2^-28 of the row's
- * largest lose bits); fp32 ones are split into two fp16 parts (22 bits). Scores, maxima, sums and outputs are fp32. The
- * weights exp(s - max) enter the second product in fp16 (bf16 rows; 2^-11
- * each) or as two fp16 parts (fp32 rows; 2^-22), and to 2^-31 of the largest
- * weight where those are smaller, whatever the scales of the blocks (up to
- * factors of 2^70 between them); their sum is taken in fp32. Sums are held
- * undivided, with weights of up to 2^15: values above 2^112 / (tokens that the
- * row sees) may give infinities. The result does
- * not depend on timing; which kernel and how many splits of the tokens a call
- * takes goes by its shapes (n_tok, n_seq, heads, table_width). A batch that mixes
+ * exact there too (scaled by a power of two per row; elements below 2^-28 of
+ * the row's largest lose bits); fp32 ones are split into two fp16 parts (22
+ * bits). Scores, maxima, sums and outputs are fp32. The weights exp(s - max)
+ * enter the second product in fp16 (bf16 rows; 2^-11 each) or as two fp16 parts
+ * (fp32 rows; 2^-22), and to 2^-31 of the largest weight where those are
+ * smaller, whatever the scales of the blocks (up to factors of 2^70 between
+ * them); their sum is taken in fp32. Sums are held undivided, with weights of
+ * up to 2^15: values above 2^112 / (tokens that the row sees) may give
+ * infinities. The result does not depend on timing; which kernel and how many
+ * splits of the tokens a call takes goes by its shapes (n_tok, n_seq, heads,
+ * table_width): a table no wider than its sequences need is faster where they
+ * are short, and gives the same result up to the order of sums. A batch that mixes
  * whole prompts with single tokens is right in one call and faster in two:
  * cu + s, kv_len + s and table + s * table_width describe the sequences from
  * s on, whose rows keep their numbers.

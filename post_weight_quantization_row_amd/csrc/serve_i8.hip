@@ -75,7 +75,7 @@ __device__ __forceinline__ u32x2 pack_codes(const float (&v)[8], float inv) {
 
 // One workgroup per row. A row of up to 256 * 8 * KEEP values stays in
 // registers between its maximum and its codes; what is longer is read again.
-// Bound by one pass over memory: 8192 rows of 4096 bf16 values in 20 us, 5.0
+// Bound by one pass over memory: 8192 rows of 4096 bf16 values in 21 us, 4.8
 // TB/s; a single row in 2.2 us, the time of its dependent loads.
 template <int SRC, int KEEP>
 __global__ __launch_bounds__(RQ_THREADS) void k_quantize_rows_i8(const void* __restrict__ x, int n, int64_t x_stride,
@@ -231,7 +231,7 @@ __device__ __forceinline__ void store_four(const Product& p, int tok, int o, con
 // its waves in chunks of 128 values, every operand loaded straight into the
 // registers that the matrix instruction reads (row li, 16 bytes at 16 lk). The
 // weights pass the chip once: bound by their bytes (16 tokens, 11008 x 4096:
-// 14 us, 3.2 TB/s; one token, 4096 x 4096: 5.6 us). From some 24 tokens on
+// 14 us, 3.3 TB/s; one token, 4096 x 4096: 5.4 us). From some 24 tokens on
 // every workgroup's reading of the tokens costs more, and tiles in LDS win.
 constexpr int F_WAVES = 8;
 constexpr int F_BATCH = 4;   // chunks of a wave whose loads are in flight together
@@ -304,10 +304,11 @@ __global__ __launch_bounds__(F_WAVES* WAVE) void k_matmul_i8_few(Product p) {
 // sixteen lanes that take one piece of neighbouring rows meet all banks.
 //
 // 32x32x32 products: with 16x16x64 ones the compiler moved 350 accumulators a
-// step between registers. 8192^3: 519 us, 2117 TOP/s (57% of the cycles busy at
-// the clock this load leaves); with the loads and stores not dealt between
-// the products 606 us, with the loads right behind the stores 570 us. The
-// small tiles, several to a CU, keep loads early (68 against 61 us).
+// step between registers. 8192^3: 1940 to 2130 TOP/s by card (a library product
+// 2270 to 2510); 8192 x 11008 x 4096: 446 to 477 us. With the loads and stores
+// not dealt between the products 8192^3 took 17% longer, with the loads right
+// behind the stores 10%. The small tiles, several to a CU, keep loads early
+// (11% slower otherwise).
 //
 // KS parts of a workgroup take every KS-th step, each with its own LDS, and
 // add their sums up at the end: where there are few tiles a CU then has

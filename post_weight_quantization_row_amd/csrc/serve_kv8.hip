@@ -242,7 +242,7 @@ __device__ __forceinline__ Growth grow(uint32_t top, int t0, float* scale, uint3
 // A few tokens (a decode step): bound by the time from one load to the next
 // and by fetching the code itself, so that loops stay loops; eight codes at a
 // time, of one token for keys, of one channel for values. One token into each
-// of 32 sequences, 8 heads of 128: 5.7 us, against 8.6 us by squares.
+// of 32 sequences, 8 heads of 128: 5 us (by squares 3 us more).
 constexpr int FEW_TOKENS = 4;
 
 template <int SRC, int D, bool VALUES>
@@ -284,7 +284,7 @@ __device__ __forceinline__ void append_few(const Cache& c, const Piece& p, int h
 
 // Each new value is read once and stays in registers between the block's
 // maximum and its codes: bound by those bytes (12545 bf16 tokens of 8 heads of
-// 128: 21.8 us, 3.5 TB/s; by single elements, read twice: 45 us).
+// 128: 22.8 us, 3.4 TB/s; by single elements, read twice: 45 us).
 template <int SRC, int D, int SQ, bool VALUES>
 __device__ __forceinline__ void append_piece(const Cache& c, const Piece& p, int head, const void* __restrict__ x,
                                              int64_t stride, uint32_t* wave_max) {
@@ -442,7 +442,7 @@ __device__ __forceinline__ void read_piece(const Cache& c, const Piece& p, int h
 }
 
 // The decoder, over the same pieces: bound by the values it writes (12545
-// tokens of 8 heads of 128 to fp32: 24.8 us, 5.2 TB/s).
+// tokens of 8 heads of 128 to fp32: 25.4 us, 5.1 TB/s).
 template <int DST, int D>
 __global__ __launch_bounds__(RW_THREADS) void k_kv8_read(Cache c, Batch b, void* __restrict__ k, void* __restrict__ v,
                                                          int64_t k_stride, int64_t v_stride) {
@@ -561,8 +561,9 @@ __device__ __forceinline__ void query_half(const float (&x)[8], int e, h16x8& hi
 // what the second product, O' = V' P', takes as its right operand.
 //
 // Bound by the codes: one token each of 64 sequences of up to 8192, 32 heads
-// over 8 of 128: 140 us, 5.2 TB/s (186 us without loading ahead, 149 us with half
-// the splits). 700 tokens of 4 sequences: 10 us, dependent loads.
+// over 8 of 128: 148 to 151 us by card, 4.8 TB/s (148 against 156 us with half
+// the splits; without loading ahead a third more). 700 tokens of 4 sequences:
+// 10.6 us, dependent loads.
 template <int SRC, int D>
 __global__ __launch_bounds__(A_WAVES * WAVE) void k_attention_kv8(Cache c, Batch b, Attention a) {
   constexpr int KS = D / 64;   // 64-channel steps of the first product
@@ -839,7 +840,9 @@ struct Index {
 
 // Where a 16-byte piece lies in LDS: piece p of K row r at p ^ k_swizzle(r),
 // channel d of the V tokens 8 e .. at d ^ v_swizzle(e). Sixteen lanes that read
-// or write side by side then meet sixteen different pieces of 256 bytes.
+// or write side by side then meet sixteen different pieces of 256 bytes. (The
+// counters still show 83k conflict cycles per CU in the prompts' case below, a
+// tenth of its time; which access they belong to is not known.)
 template <int D>
 __device__ __forceinline__ int k_swizzle(int r) { return D == 64 ? (r >> 1) & 7 : r & 15; }
 __device__ __forceinline__ int v_swizzle(int e) { return (e & 1) << 3 | e >> 1; }
@@ -878,14 +881,15 @@ __device__ __forceinline__ ValueScale value_scale(float vd) {
 // 2^P_FOLD below it: e_ref then follows, so that a group's weights keep their
 // bits whatever the scales of others.
 //
-// Bound by instruction issue: per wave, 32 rows and 64 tokens, 375 vector and 98
-// scalar instructions beside 32 products. Prompts of 4 sequences of up to 4096
-// tokens, 32 heads over 8 of 128: 443 us, 770 TFLOP/s. Steps on the way: 721 us
-// with the group's block and scales looked up and worked out in every wave and tile, 563 us with two
-// groups to a rescale test, 507 us with lookups in lanes, 443 us with the heads of a
-// unit side by side. 64-token tiles (32 for 256 channels, whose two buffers
-// fill the same LDS) and 128 rows: 32-token tiles at three waves a SIMD took 550 us
-// and more, 256 rows in eight waves 485 us against 474 us on the same card.
+// Prompts of 4 sequences of up to 4096 tokens, 32 heads over 8 of 128: 455 to
+// 488 us by card, 700 to 750 TFLOP/s. Of a SIMD's 915k busy cycles 333k are
+// products, and its 119k vector instructions take four cycles each: together
+// 809k, so that the two units seem to work in turn more than at once, with two
+// waves a SIMD. Heads of a unit side by side: 12% off the time; blocks and
+// scales looked up in lanes, not by every wave in every tile: 25%. Following
+// the value scales down as well as up costs 2% (fp32: 5%). 64-token tiles (32
+// for 256 channels, whose two buffers fill the same LDS) and 128 rows: 32-token
+// tiles at three waves a SIMD took 20% longer, 256 rows in eight waves 2%.
 template <int SRC, int D, int NG>
 __global__ __launch_bounds__(P_WAVES * WAVE, D == 256 || (SRC == QR_F32 && D == 128) ? 1 : 2) void k_attention_kv8_rows(Cache c, Batch b, Attention a) {
   constexpr int THREADS = P_WAVES * WAVE;
@@ -1386,7 +1390,11 @@ Cache device_cache(const qr_kv8* c) {
 int64_t piece_units(const qr_kv8* c, int64_t n_tok, int64_t n_seq) { return n_tok / c->block_tokens + 2 * n_seq; }
 
 // How a call of attention is cut: units of 16 or 128 rows, and splits of the
-// tokens where that leaves CUs without work.
+// tokens where that leaves CUs without work. The rules go by what the host
+// knows, the table's width and averages over the sequences: a table much wider
+// than its sequences costs short ones a second launch, one long sequence among
+// many short ones is split as little as they are, and prompts mixed with
+// single tokens take one kernel for both.
 struct Cut {
   bool many;        // the kernel for many rows
   int64_t units, splits;
