@@ -64,8 +64,9 @@ int qr_quantize_rows_i8(int src, const void *x, int64_t n_rows,
  * then wd[r], and the bias added, each rounded to fp32 once, then rounded to
  * dst: within 4 * 2^-24 of the magnitude |product| + |bias| before that last
  * rounding (2^-149 more where the product is subnormal; infinite only where
- * the product or the output is). The result does not depend on the launch shape. Codes are read as
- * they are: -128 is allowed in codes made elsewhere up to n_in = 131071.
+ * the product or the output is). The result does not depend on the launch
+ * shape. Codes are read as they are: -128 is allowed in codes made elsewhere up
+ * to n_in = 131071.
  * Codes behind n_in up to the row's end must be zero, as qr_quantize_rows_i8
  * writes them.
  * Limits: 1 <= n_in <= QR_I8_MAX_IN; n_out, n_tok < 2^31 - 256, and what one

@@ -65,9 +65,10 @@ size_t qr_kv8_code_bytes(const qr_kv8 *c);
  *           v_stride), a multiple of 8, at least n_heads * head_dim.
  * Per block and head, for k and v apart: amax = max |x| of the new tokens in
  * the block, cand = amax / 127 (0 if 1 / cand is not finite). In a block whose
- * first token is new the scale becomes cand. Otherwise scale = max(old, cand), and where it grew the codes
- * c of the tokens before become rint(c * (old / scale)). The new codes are rint(x * (1 / scale)),
- * clamped to -127..127 (0 where the scale is 0). Every operation is rounded
+ * first token is new the scale becomes cand. Otherwise scale = max(old, cand),
+ * and where it grew the codes c of the tokens before become rint(c * (old /
+ * scale)). The new codes are rint(x * (1 / scale)), clamped to -127..127 (0
+ * where the scale is 0). Every operation is rounded
  * to fp32 once. A block that gets an infinity or a NaN gets scale NaN and zero
  * codes for its new tokens, and stays so until its first token is written again: the
  * rows that attend to it are NaN. Writing the same rows again leaves
@@ -87,9 +88,9 @@ int qr_kv8_append(const qr_kv8 *c, int src, const void *k, const void *v,
 
 /*
  * qr_kv8_read -- the decoder: the values of the same rows, scale * code
- * rounded to fp32 and then to dst (QR_F32 or QR_BF16), into k and v [n_tok, n_heads, head_dim]
- * (strides and limits as in qr_kv8_append), which must not overlap. With cu counting whole sequences it returns
- * the whole cache of each.
+ * rounded to fp32 and then to dst (QR_F32 or QR_BF16), into k and v [n_tok,
+ * n_heads, head_dim] (strides and limits as in qr_kv8_append), which must not
+ * overlap. With cu counting whole sequences it returns the whole cache of each.
  */
 int qr_kv8_read(const qr_kv8 *c, int dst, void *k, void *v, int64_t k_stride,
                 int64_t v_stride, int64_t n_tok, int64_t n_seq,
