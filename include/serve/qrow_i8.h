@@ -79,6 +79,49 @@ int qr_matmul_i8(const int8_t *w, const float *wd, const int8_t *x,
                  int64_t n_tok, int64_t n_in, int dst, void *y,
                  int64_t y_stride, void *stream);
 
+/* Activations of qr_matmul_i8_ex and of the experts in qrow_moe.h. */
+enum {
+    QR_ACT_NONE = 0,
+    QR_ACT_RELU = 1,
+    QR_ACT_SILU = 2,       /* x / (1 + exp(-x))                              */
+    QR_ACT_GELU = 3,       /* x / 2 * (1 + erf(x / sqrt 2))                  */
+    QR_ACT_GELU_TANH = 4   /* x / 2 * (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) */
+};
+
+/* What qr_matmul_i8_ex does with its products. */
+typedef struct {
+    int64_t act;               /* QR_ACT_*                                       */
+    const int8_t *up;          /* a second set of weight rows, or NULL           */
+    const float *upd;          /* its scales                                     */
+    const float *up_bias;      /* and its bias, or NULL                          */
+    const void *residual;      /* added at the end, of type dst, or NULL         */
+    int64_t residual_stride;   /* token t at element t * residual_stride         */
+} qr_i8_epilogue;
+
+/*
+ * qr_matmul_i8_ex -- qr_matmul_i8 with an epilogue:
+ *   y[t][r] = act(p(w)) * p(up) + residual[t][r],
+ * p(w) = xd[t] * wd[r] * sum_k x[t][k] * w[r][k] + bias[r] as in qr_matmul_i8
+ * and p(up) the same product with up [n_out, qr_i8_row_bytes(n_in)], upd and
+ * up_bias (left out where up is NULL): a gated projection in one pass over x,
+ * without the two products in memory.
+ * epilogue   NULL: qr_matmul_i8.
+ * residual   [n_tok, n_out] of type dst, rows residual_stride >= n_out elements
+ *            apart. It may be y itself (the same pointer and stride: added in
+ *            place); otherwise the two must not overlap (refused).
+ * Every step is in fp32: the two products each as in qr_matmul_i8; the
+ * activation, within 8 * 2^-24 of |p(w)| (and 2^-110 where exp overflows) for
+ * the fp32 p(w) it is given; the gate's product and the residual's addition
+ * rounded once each; then the rounding to dst.
+ * Limits: those of qr_matmul_i8, with up those for 2 * n_out; act one of the
+ * above.
+ */
+int qr_matmul_i8_ex(const int8_t *w, const float *wd, const int8_t *x,
+                    const float *xd, const float *bias,
+                    const qr_i8_epilogue *epilogue, int64_t n_out,
+                    int64_t n_tok, int64_t n_in, int dst, void *y,
+                    int64_t y_stride, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -9,7 +9,9 @@ SOURCES = [os.path.join(HERE, "csrc", "qrow.hip"),
            os.path.join(HERE, "csrc", "matmul.hip"),
            os.path.join(HERE, "csrc", "stats.hip"),
            os.path.join(HERE, "csrc", "serve_i8.hip"),
-           os.path.join(HERE, "csrc", "serve_kv8.hip")]
+           os.path.join(HERE, "csrc", "serve_kv8.hip"),
+           os.path.join(HERE, "csrc", "serve_norm.hip"),
+           os.path.join(HERE, "csrc", "serve_moe.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libqrow.so")
 # measurement only: VALU issue rates of the instruction classes the kernels

@@ -8,70 +8,20 @@
 #include "qr_internal.h"
 #include "qrow.h"
 #include "serve/qrow_i8.h"
+#include "serve_internal.h"
 
 namespace {
 
+using namespace serve;
+
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-// Vectors at any element of the caller's rows, whose strides are free: memory
-// instructions take them unaligned.
-typedef uint16_t u16x8_any __attribute__((ext_vector_type(8), aligned(2)));
-typedef uint16_t u16x4_any __attribute__((ext_vector_type(4), aligned(2)));
-typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
-
-constexpr int WAVE = 64;
 constexpr int ROW_ALIGN = 128;   // bytes: qr_i8_row_bytes
-
-__device__ __forceinline__ float bf16_value(uint16_t h) { return __builtin_bit_cast(float, (uint32_t)h << 16); }
-
-// fp32 to bf16, round to nearest even (NaN stays NaN).
-__device__ __forceinline__ uint16_t bf16_bits(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
 
 // ---------------------------------------------------------------------------
 // the row quantizer
 
 constexpr int RQ_THREADS = 256;
-
-// Eight values of a row from element `at` on; zeros behind n.
-template <int SRC>
-__device__ __forceinline__ void load8(const void* row, int at, int n, float (&v)[8]) {
-  if (at + 8 <= n) {
-    if (SRC == QR_BF16) {
-      const u16x8_any h = *reinterpret_cast<const u16x8_any*>(reinterpret_cast<const uint16_t*>(row) + at);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = bf16_value(h[i]);
-    } else {
-      const f32x4_any* p = reinterpret_cast<const f32x4_any*>(reinterpret_cast<const float*>(row) + at);
-      const f32x4_any a = p[0], b = p[1];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = a[i];
-        v[4 + i] = b[i];
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = 0.0f;
-      if (at + i < n)
-        v[i] = SRC == QR_BF16 ? bf16_value(reinterpret_cast<const uint16_t*>(row)[at + i])
-                              : reinterpret_cast<const float*>(row)[at + i];
-    }
-  }
-}
-
-__device__ __forceinline__ u32x2 pack_codes(const float (&v)[8], float inv) {
-  u32x2 o;
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    uint32_t u = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u |= ((uint32_t)(int)__builtin_rintf(v[4 * w + i] * inv) & 0xffu) << (8 * i);
-    o[w] = u;
-  }
-  return o;
-}
 
 // One workgroup per row. A row of up to 256 * 8 * KEEP values stays in
 // registers between its maximum and its codes; what is longer is read again.
@@ -118,26 +68,19 @@ __global__ __launch_bounds__(RQ_THREADS) void k_quantize_rows_i8(const void* __r
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < RQ_THREADS / WAVE; ++w) top = wave_max[w] > top ? wave_max[w] : top;
-  const float amax = __builtin_bit_cast(float, top);
-  const bool finite = top < 0x7f800000u;
-  float inv = 127.0f / amax;
-  float d = amax / 127.0f;
-  if (!finite || !(inv < __builtin_inff())) {
-    inv = 0.0f;
-    d = finite ? 0.0f : __builtin_nanf("");
-  }
+  const CodeScale c = code_scale(top);
   int8_t* out = codes + r * row_bytes;
 #pragma unroll
   for (int k = 0; k < KEEP; ++k) {
     const int g = tid + k * RQ_THREADS;
-    if (g < n_vec) *reinterpret_cast<u32x2*>(out + (int64_t)g * 8) = finite ? pack_codes(keep[k], inv) : u32x2{0, 0};
+    if (g < n_vec) *reinterpret_cast<u32x2*>(out + (int64_t)g * 8) = c.finite ? pack_codes(keep[k], c.inv) : u32x2{0, 0};
   }
   for (int g = tid + KEEP * RQ_THREADS; g < n_vec; g += RQ_THREADS) {
     float v[8];
     load8<SRC>(row, g * 8, n, v);
-    *reinterpret_cast<u32x2*>(out + (int64_t)g * 8) = finite ? pack_codes(v, inv) : u32x2{0, 0};
+    *reinterpret_cast<u32x2*>(out + (int64_t)g * 8) = c.finite ? pack_codes(v, c.inv) : u32x2{0, 0};
   }
-  if (tid == 0) scales[r] = d;
+  if (tid == 0) scales[r] = c.d;
 }
 
 template <int SRC>
@@ -167,6 +110,19 @@ struct Product {
   int n_out, n_tok, row_bytes;
 };
 
+// What comes behind the sums (EPI): nothing but scales and bias, an activation
+// and a residual, or those and the gate's second product.
+enum { PLAIN, ACT, GATED };
+
+struct Epilogue {
+  const int8_t* up;
+  const float* upd;
+  const float* up_bias;
+  const void* residual;
+  int64_t residual_stride;
+  int act;
+};
+
 // Which tile a workgroup takes. Workgroups are dealt to the 8 XCDs in turn;
 // each XCD gets a run of neighbouring tiles, so that its L2 holds what they
 // share, and walks it in bands of GROUP_T token tiles.
@@ -190,31 +146,40 @@ __device__ __forceinline__ void store_one(void* y, int64_t at, float v) {
   else reinterpret_cast<float*>(y)[at] = v;
 }
 
-// A token's scale as xd * back: above 2^96 it is lowered by 2^32, so that a sum
-// (up to 2^31) times it does not overflow before the channel's scale comes.
-// Powers of two round nothing (8192 tokens, 11008 x 4096: 453 -> 459 us). At
-// the other end a whole number times a scale loses no bits.
-struct TokenScale {
-  float d, back;
-};
-
-__device__ __forceinline__ TokenScale token_scale(float xd) {
-  const bool high = __builtin_fabsf(xd) > 0x1p96f;
-  return {high ? xd * 0x1p-32f : xd, high ? 0x1p32f : 1.0f};
+template <int SRC>
+__device__ __forceinline__ float load_one(const void* x, int64_t at) {
+  return SRC == QR_BF16 ? bf16_value(reinterpret_cast<const uint16_t*>(x)[at]) : reinterpret_cast<const float*>(x)[at];
 }
 
-__device__ __forceinline__ float scaled(int sum, const TokenScale& xd, float wd, float bias) {
-  return (((float)sum * xd.d) * wd) * xd.back + bias;
+// One output before its rounding to the output's type, without the residual.
+template <int EPI>
+__device__ __forceinline__ float output(const Product& p, const Epilogue& ep, int o, int sum, int up, const TokenScale& xd) {
+  float v = scaled(sum, xd, p.wd[o], p.bias ? p.bias[o] : 0.0f);
+  if (EPI != PLAIN) v = activation(ep.act, v);
+  if (EPI == GATED) v *= scaled(up, xd, ep.upd[o], ep.up_bias ? ep.up_bias[o] : 0.0f);
+  return v;
 }
 
-// Stores four neighbouring channels of one token.
-template <int DST>
-__device__ __forceinline__ void store_four(const Product& p, int tok, int o, const i32x4& sum, const TokenScale& xd) {
-  const int64_t at = (int64_t)tok * p.y_stride + o;
+// Stores four neighbouring channels of one token; up: the gate's second sums.
+template <int DST, int EPI>
+__device__ __forceinline__ void store_four(const Product& p, const Epilogue& ep, int tok, int o, const i32x4& sum,
+                                           const i32x4& up, const TokenScale& xd) {
+  const int64_t at = (int64_t)tok * p.y_stride + o, from = (int64_t)tok * ep.residual_stride + o;
   if (o + 4 <= p.n_out) {
     float v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = scaled(sum[e], xd, p.wd[o + e], p.bias ? p.bias[o + e] : 0.0f);
+    for (int e = 0; e < 4; ++e) v[e] = output<EPI>(p, ep, o + e, sum[e], up[e], xd);
+    if (EPI != PLAIN && ep.residual) {
+      if (DST == QR_BF16) {
+        const u16x4_any r = *reinterpret_cast<const u16x4_any*>(reinterpret_cast<const uint16_t*>(ep.residual) + from);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += bf16_value(r[e]);
+      } else {
+        const f32x4_any r = *reinterpret_cast<const f32x4_any*>(reinterpret_cast<const float*>(ep.residual) + from);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += r[e];
+      }
+    }
     if (DST == QR_BF16)
       *reinterpret_cast<u16x4_any*>(reinterpret_cast<uint16_t*>(p.y) + at) =
           u16x4_any{bf16_bits(v[0]), bf16_bits(v[1]), bf16_bits(v[2]), bf16_bits(v[3])};
@@ -222,8 +187,12 @@ __device__ __forceinline__ void store_four(const Product& p, int tok, int o, con
       *reinterpret_cast<f32x4_any*>(reinterpret_cast<float*>(p.y) + at) = f32x4_any{v[0], v[1], v[2], v[3]};
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (o + e < p.n_out) store_one<DST>(p.y, at + e, scaled(sum[e], xd, p.wd[o + e], p.bias ? p.bias[o + e] : 0.0f));
+    for (int e = 0; e < 4; ++e) {
+      if (o + e >= p.n_out) continue;
+      float v = output<EPI>(p, ep, o + e, sum[e], up[e], xd);
+      if (EPI != PLAIN && ep.residual) v += load_one<DST>(ep.residual, from + e);
+      store_one<DST>(p.y, at + e, v);
+    }
   }
 }
 
@@ -236,16 +205,19 @@ __device__ __forceinline__ void store_four(const Product& p, int tok, int o, con
 constexpr int F_WAVES = 8;
 constexpr int F_BATCH = 4;   // chunks of a wave whose loads are in flight together
 
-template <int DST, int TT>
-__global__ __launch_bounds__(F_WAVES* WAVE) void k_matmul_i8_few(Product p) {
-  __shared__ i32x4 part[F_WAVES][TT][WAVE];
+template <int DST, int TT, int EPI>
+__global__ __launch_bounds__(F_WAVES* WAVE) void k_matmul_i8_few(Product p, Epilogue ep) {
+  constexpr int G = EPI == GATED ? 2 : 1;   // weight rows per channel: gate and up
+  __shared__ i32x4 part[F_WAVES][G][TT][WAVE];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int li = lane & 15, lk = lane >> 4;
   const int out_tiles = (p.n_out + 15) / 16;
   const int o0 = (int)(blockIdx.x % out_tiles) * 16, t0 = (int)(blockIdx.x / out_tiles) * 16 * TT;
   // rows behind the last repeat it: their results are not stored
   const int wr = o0 + li < p.n_out ? o0 + li : p.n_out - 1;
-  const int8_t* w = p.w + (int64_t)wr * p.row_bytes + 16 * lk;
+  const int8_t* w[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) w[g] = (g ? ep.up : p.w) + (int64_t)wr * p.row_bytes + 16 * lk;
   const int8_t* x[TT];
 #pragma unroll
   for (int j = 0; j < TT; ++j) {
@@ -253,15 +225,16 @@ __global__ __launch_bounds__(F_WAVES* WAVE) void k_matmul_i8_few(Product p) {
     x[j] = p.x + (int64_t)xr * p.row_bytes + 16 * lk;
   }
   const int chunks = p.row_bytes / 128;
-  i32x4 acc[TT] = {};
+  i32x4 acc[G][TT] = {};
   for (int c0 = wave; c0 < chunks; c0 += F_WAVES * F_BATCH) {
-    i32x4 a[F_BATCH][2], b[F_BATCH][2][TT];
+    i32x4 a[F_BATCH][2][G], b[F_BATCH][2][TT];
 #pragma unroll
     for (int u = 0; u < F_BATCH; ++u) {
       const int c = c0 + u * F_WAVES < chunks ? c0 + u * F_WAVES : c0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        a[u][h] = *reinterpret_cast<const i32x4*>(w + c * 128 + 64 * h);
+#pragma unroll
+        for (int g = 0; g < G; ++g) a[u][h][g] = *reinterpret_cast<const i32x4*>(w[g] + c * 128 + 64 * h);
 #pragma unroll
         for (int j = 0; j < TT; ++j) b[u][h][j] = *reinterpret_cast<const i32x4*>(x[j] + c * 128 + 64 * h);
       }
@@ -273,19 +246,27 @@ __global__ __launch_bounds__(F_WAVES* WAVE) void k_matmul_i8_few(Product p) {
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int j = 0; j < TT; ++j)
-            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u][h], b[u][h][j], acc[j], 0, 0, 0);
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+              acc[g][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u][h][g], b[u][h][j], acc[g][j], 0, 0, 0);
       }
     }
   }
 #pragma unroll
-  for (int j = 0; j < TT; ++j) part[wave][j][lane] = acc[j];
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int j = 0; j < TT; ++j) part[wave][g][j][lane] = acc[g][j];
   __syncthreads();
   if (wave < TT) {
-    i32x4 sum = part[0][wave][lane];
+    i32x4 sum[2];
 #pragma unroll
-    for (int v = 1; v < F_WAVES; ++v) sum += part[v][wave][lane];
+    for (int g = 0; g < G; ++g) {
+      sum[g] = part[0][g][wave][lane];
+#pragma unroll
+      for (int v = 1; v < F_WAVES; ++v) sum[g] += part[v][g][wave][lane];
+    }
     const int tok = t0 + 16 * wave + li;
-    if (tok < p.n_tok) store_four<DST>(p, tok, o0 + 4 * lk, sum, token_scale(p.xd[tok]));
+    if (tok < p.n_tok) store_four<DST, EPI>(p, ep, tok, o0 + 4 * lk, sum[0], sum[G - 1], token_scale(p.xd[tok]));
   }
 }
 
@@ -313,9 +294,13 @@ __global__ __launch_bounds__(F_WAVES* WAVE) void k_matmul_i8_few(Product p) {
 // KS parts of a workgroup take every KS-th step, each with its own LDS, and
 // add their sums up at the end: where there are few tiles a CU then has
 // 8 or 16 waves at work on one.
-template <int DST, int NI, int NJ, int KS>
+//
+// With a gate a piece of 32 weight rows is 16 of gate and the same 16 channels'
+// of up: a lane's accumulators e and e + 8 are then the two sums of a channel,
+// and a tile has half as many channels.
+template <int DST, int NI, int NJ, int KS, int EPI>
 __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(NI * NJ > 8 ? 1 : 2))) void k_matmul_i8_tile(
-    Product p, int out_tiles, int tok_tiles) {
+    Product p, Epilogue ep, int out_tiles, int tok_tiles) {
   constexpr int TO = 64 * NI, TT = 64 * NJ;
   constexpr bool LATE = NI * NJ > 8;   // ask for a tile late, between products that hide it
   __shared__ __attribute__((aligned(16))) int8_t all_lds[KS][2][(TO + TT) * 128];
@@ -325,9 +310,11 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(NI * N
   const int li = lane & 31, lh = lane >> 5;
   int bo, bt;
   tile_of(blockIdx.x, out_tiles, tok_tiles, bo, bt);
-  const int o0 = bo * TO, t0 = bt * TT;
+  constexpr int PIECE = EPI == GATED ? 16 : 32;   // channels of 32 weight rows
+  const int o0 = bo * (2 * NI * PIECE), t0 = bt * TT;
   const int wo = (wave & 1) * (32 * NI), wt = (wave >> 1) * (32 * NJ);
-  const int8_t* wbase = p.w + (int64_t)o0 * p.row_bytes;
+  // (the lanes of a wave stage eight rows: gate's or up's)
+  const int8_t* wbase = (EPI == GATED && wave >= 2 ? ep.up : p.w) + (int64_t)o0 * p.row_bytes;
   const int8_t* xbase = p.x + (int64_t)t0 * p.row_bytes;
   // rows behind the last repeat it: their results are not stored
   constexpr int NQ = 2 * NI + 2 * NJ;   // 32-row pieces of the tile: weights, then tokens
@@ -335,7 +322,7 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(NI * N
   uint32_t off[NQ];
 #pragma unroll
   for (int q = 0; q < NQ; ++q) {
-    const int r = lr + 32 * (q < 2 * NI ? q : q - 2 * NI);
+    const int r = q < 2 * NI ? lr % PIECE + PIECE * q : lr + 32 * (q - 2 * NI);
     const int last = q < 2 * NI ? p.n_out - 1 - o0 : p.n_tok - 1 - t0;
     off[q] = (uint32_t)(r < last ? r : last) * (uint32_t)p.row_bytes + lc;
   }
@@ -420,41 +407,80 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(NI * N
         for (int n = 0; n < NI * NJ; ++n) acc[n / NJ][n % NJ] += sums[(wave * NI * NJ + n) * 64 + lane];
       }
     }
+    if (EPI != PLAIN) __syncthreads();   // the sums have been read
     if (part != 0) return;
+  } else if constexpr (EPI != PLAIN) {
+    __syncthreads();                     // the last tile has been read
   }
+  if constexpr (EPI == PLAIN) {
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int tok = t0 + wt + 32 * j + li;
-    if (tok >= p.n_tok) continue;
-    const TokenScale xd = token_scale(p.xd[tok]);
+    for (int j = 0; j < NJ; ++j) {
+      const int tok = t0 + wt + 32 * j + li;
+      if (tok >= p.n_tok) continue;
+      const TokenScale xd = token_scale(p.xd[tok]);
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+      for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; e += 4)
-        store_four<DST>(p, tok, o0 + wo + 32 * i + 2 * e + 4 * lh,
-                        i32x4{acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]}, xd);
+        for (int e = 0; e < 16; e += 4) {
+          const i32x4 sum = {acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]};
+          store_four<DST, EPI>(p, ep, tok, o0 + wo + 32 * i + 2 * e + 4 * lh, sum, sum, xd);
+        }
+    }
+  } else {
+    // 32 tokens at a time through the wave's own part of LDS: the epilogue is
+    // then one short loop over neighbouring channels (unrolled over the
+    // accumulators it was too long for the compiler to keep them in registers)
+    constexpr int W = 32 * NI, PITCH = W + 4, FOURS = W / (EPI == GATED ? 8 : 4);
+    static_assert(4 * 32 * PITCH * 4 <= (int)sizeof(all_lds), "the waves' sums fit");
+    int* sums = reinterpret_cast<int*>(all_lds) + wave * (32 * PITCH);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      if (t0 + wt + 32 * j >= p.n_tok) break;
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+          *reinterpret_cast<i32x4*>(sums + li * PITCH + 32 * i + 2 * e + 4 * lh) =
+              i32x4{acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]};
+      wave_sync();
+#pragma unroll 1
+      for (int at = lane; at < 32 * FOURS; at += 64) {
+        const int t = at / FOURS, four = at % FOURS, tok = t0 + wt + 32 * j + t;
+        const int piece = four * 4 / PIECE, o = o0 + (wo / 32 + piece) * PIECE + four * 4 % PIECE;
+        if (tok >= p.n_tok || o >= p.n_out) continue;
+        const int* from = sums + t * PITCH + 32 * piece + four * 4 % PIECE;
+        store_four<DST, EPI>(p, ep, tok, o, *reinterpret_cast<const i32x4*>(from),
+                             *reinterpret_cast<const i32x4*>(from + (EPI == GATED ? 16 : 0)), token_scale(p.xd[tok]));
+      }
+      wave_sync();
+    }
   }
 }
 
-template <int DST, int TT>
-int launch_few(const Product& p, hipStream_t s) {
+template <int DST, int TT, int EPI>
+int launch_few(const Product& p, const Epilogue& ep, hipStream_t s) {
   const int64_t tiles = (int64_t)((p.n_out + 15) / 16) * ((p.n_tok + 16 * TT - 1) / (16 * TT));
   if (tiles > UINT32_MAX / (F_WAVES * WAVE)) return qr_fail(QR_EOVERFLOW, "n_out and n_tok need too many tiles for one launch");
-  hipLaunchKernelGGL((k_matmul_i8_few<DST, TT>), dim3((uint32_t)tiles), dim3(F_WAVES * WAVE), 0, s, p);
+  hipLaunchKernelGGL((k_matmul_i8_few<DST, TT, EPI>), dim3((uint32_t)tiles), dim3(F_WAVES * WAVE), 0, s, p, ep);
   return qr_check_launch("k_matmul_i8_few");
 }
 
-template <int DST, int NI, int NJ, int KS>
-int launch_tile(const Product& p, hipStream_t s) {
-  const int out_tiles = (p.n_out + 64 * NI - 1) / (64 * NI), tok_tiles = (p.n_tok + 64 * NJ - 1) / (64 * NJ);
+template <int DST, int NI, int NJ, int KS, int EPI>
+int launch_tile(const Product& p, const Epilogue& ep, hipStream_t s) {
+  constexpr int TO = EPI == GATED ? 32 * NI : 64 * NI;   // channels of a tile
+  const int out_tiles = (p.n_out + TO - 1) / TO, tok_tiles = (p.n_tok + 64 * NJ - 1) / (64 * NJ);
   const int64_t tiles = (int64_t)out_tiles * tok_tiles;
   if (tiles > UINT32_MAX / (256 * KS)) return qr_fail(QR_EOVERFLOW, "n_out and n_tok need too many tiles for one launch");
-  hipLaunchKernelGGL((k_matmul_i8_tile<DST, NI, NJ, KS>), dim3((uint32_t)tiles), dim3(256 * KS), 0, s, p, out_tiles, tok_tiles);
+  hipLaunchKernelGGL((k_matmul_i8_tile<DST, NI, NJ, KS, EPI>), dim3((uint32_t)tiles), dim3(256 * KS), 0, s, p, ep,
+                     out_tiles, tok_tiles);
   return qr_check_launch("k_matmul_i8_tile");
 }
 
+// Tiles of `out` weight rows x `tok` tokens; a gate has two rows per channel.
+template <int EPI>
 int64_t tiles_of(const Product& p, int out, int tok) {
-  return (int64_t)((p.n_out + out - 1) / out) * ((p.n_tok + tok - 1) / tok);
+  const int64_t rows = EPI == GATED ? 2 * (int64_t)p.n_out : p.n_out;
+  return ((rows + out - 1) / out) * ((p.n_tok + tok - 1) / tok);
 }
 
 // The tile: as large as leaves the chip's 256 CUs a workgroup each (an LDS
@@ -471,22 +497,46 @@ int64_t tiles_of(const Product& p, int out, int tok) {
 //   1500                 128x128: 44           128x128 in two: 53
 //   4096                 256x256: 82           128x128: 96
 //   700 x 11008 (129 tiles of 256x256)         128x128: 70    256x256: 74
-template <int DST>
-int launch_product(const Product& p, hipStream_t s) {
+template <int DST, int EPI>
+int launch_product(const Product& p, const Epilogue& ep, hipStream_t s) {
   constexpr int64_t CUS = 256;
-  if (p.n_tok <= 16) return launch_few<DST, 1>(p, s);
-  const int64_t t64 = tiles_of(p, 64, 64);
+  if (p.n_tok <= 16) return launch_few<DST, 1, EPI>(p, ep, s);
+  const int64_t t64 = tiles_of<EPI>(p, 64, 64);
   if (p.n_tok <= 64 && t64 < 96) {   // few channels too
-    if (p.n_tok > 32 && tiles_of(p, 16, 64) >= CUS) return launch_few<DST, 4>(p, s);
-    return launch_few<DST, 2>(p, s);
+    if (p.n_tok > 32 && tiles_of<EPI>(p, 16, 64) >= CUS) return launch_few<DST, 4, EPI>(p, ep, s);
+    return launch_few<DST, 2, EPI>(p, ep, s);
   }
-  if (t64 <= CUS) return launch_tile<DST, 1, 1, 4>(p, s);
-  if (tiles_of(p, 64, 128) <= CUS) return launch_tile<DST, 1, 2, 2>(p, s);
-  if (tiles_of(p, 128, 128) <= CUS) return launch_tile<DST, 2, 2, 2>(p, s);
+  if (t64 <= CUS) return launch_tile<DST, 1, 1, 4, EPI>(p, ep, s);
+  if (tiles_of<EPI>(p, 64, 128) <= CUS) return launch_tile<DST, 1, 2, 2, EPI>(p, ep, s);
+  if (tiles_of<EPI>(p, 128, 128) <= CUS) return launch_tile<DST, 2, 2, 2, EPI>(p, ep, s);
   // 256x256 where the last round of workgroups does not leave too many idle
-  const int64_t t256 = tiles_of(p, 256, 256), rounds = (t256 + CUS - 1) / CUS;
-  if (t256 * 100 >= rounds * CUS * 65) return launch_tile<DST, 4, 4, 1>(p, s);
-  return launch_tile<DST, 2, 2, 1>(p, s);
+  const int64_t t256 = tiles_of<EPI>(p, 256, 256), rounds = (t256 + CUS - 1) / CUS;
+  if (t256 * 100 >= rounds * CUS * 65) return launch_tile<DST, 4, 4, 1, EPI>(p, ep, s);
+  return launch_tile<DST, 2, 2, 1, EPI>(p, ep, s);
+}
+
+template <int EPI>
+int launch_to(int dst, const Product& p, const Epilogue& ep, hipStream_t s) {
+  return dst == QR_BF16 ? launch_product<QR_BF16, EPI>(p, ep, s) : launch_product<QR_F32, EPI>(p, ep, s);
+}
+
+// The checks that both products share; QR_OK with *none set: nothing to do.
+int check_product(const int8_t* w, const float* wd, const int8_t* x, const float* xd, const float* bias, int64_t n_out,
+                  int64_t n_tok, int64_t n_in, int dst, const void* y, int64_t y_stride, bool* none) {
+  *none = false;
+  if (dst != QR_F32 && dst != QR_BF16) return qr_fail(QR_EINVAL_TYPE, "output type %d is not QR_F32 or QR_BF16", dst);
+  if (qr_i8_row_bytes(n_in) == 0) return qr_fail(QR_EINVAL_SHAPE, "n_in=%lld must be in 1..%d", (long long)n_in, QR_I8_MAX_IN);
+  if (n_out < 0 || n_tok < 0 || y_stride < n_out)
+    return qr_fail(QR_EINVAL_SHAPE, "negative n_out or n_tok, or y_stride below n_out");
+  *none = n_out == 0 || n_tok == 0;
+  if (*none) return QR_OK;
+  if (n_out > INT32_MAX - 256 || n_tok > INT32_MAX - 256 || y_stride > INT64_MAX / 4 / n_tok)
+    return qr_fail(QR_EOVERFLOW, "n_out or n_tok too large");
+  if (!w || !wd || !x || !xd || !y) return qr_fail(QR_EINVAL_PTR, "w, wd, x, xd and y must be non-NULL");
+  if (!qr_aligned(w, 16) || !qr_aligned(x, 16) || !qr_aligned(wd, 4) || !qr_aligned(xd, 4) || !qr_aligned(bias, 4) ||
+      !qr_aligned(y, dst == QR_BF16 ? 2 : 4))
+    return qr_fail(QR_EINVAL_PTR, "codes must be 16-byte aligned, wd, xd, bias and y to their elements");
+  return QR_OK;
 }
 
 }  // namespace
@@ -519,22 +569,39 @@ int qr_quantize_rows_i8(int src, const void* x, int64_t n_rows, int64_t n_per_ro
 
 int qr_matmul_i8(const int8_t* w, const float* wd, const int8_t* x, const float* xd, const float* bias, int64_t n_out,
                  int64_t n_tok, int64_t n_in, int dst, void* y, int64_t y_stride, void* stream) {
+  return qr_matmul_i8_ex(w, wd, x, xd, bias, nullptr, n_out, n_tok, n_in, dst, y, y_stride, stream);
+}
+
+int qr_matmul_i8_ex(const int8_t* w, const float* wd, const int8_t* x, const float* xd, const float* bias,
+                    const qr_i8_epilogue* e, int64_t n_out, int64_t n_tok, int64_t n_in, int dst, void* y,
+                    int64_t y_stride, void* stream) {
   qr_clear_error();
-  if (dst != QR_F32 && dst != QR_BF16) return qr_fail(QR_EINVAL_TYPE, "output type %d is not QR_F32 or QR_BF16", dst);
-  const int64_t rb = (int64_t)qr_i8_row_bytes(n_in);
-  if (rb == 0) return qr_fail(QR_EINVAL_SHAPE, "n_in=%lld must be in 1..%d", (long long)n_in, QR_I8_MAX_IN);
-  if (n_out < 0 || n_tok < 0 || y_stride < n_out)
-    return qr_fail(QR_EINVAL_SHAPE, "negative n_out or n_tok, or y_stride below n_out");
-  if (n_out == 0 || n_tok == 0) return QR_OK;
-  if (n_out > INT32_MAX - 256 || n_tok > INT32_MAX - 256 || y_stride > INT64_MAX / 4 / n_tok)
-    return qr_fail(QR_EOVERFLOW, "n_out or n_tok too large");
-  if (!w || !wd || !x || !xd || !y) return qr_fail(QR_EINVAL_PTR, "w, wd, x, xd and y must be non-NULL");
-  if (!qr_aligned(w, 16) || !qr_aligned(x, 16) || !qr_aligned(wd, 4) || !qr_aligned(xd, 4) || !qr_aligned(bias, 4) ||
-      !qr_aligned(y, dst == QR_BF16 ? 2 : 4))
-    return qr_fail(QR_EINVAL_PTR, "codes must be 16-byte aligned, wd, xd, bias and y to their elements");
-  const Product p = {w, x, wd, xd, bias, y, y_stride, (int)n_out, (int)n_tok, (int)rb};
+  bool none;
+  const int rc = check_product(w, wd, x, xd, bias, n_out, n_tok, n_in, dst, y, y_stride, &none);
+  if (rc != QR_OK) return rc;
+  if (e && (e->act < QR_ACT_NONE || e->act > QR_ACT_GELU_TANH))
+    return qr_fail(QR_EINVAL_TYPE, "activation %lld is not one of QR_ACT_*", (long long)e->act);
+  if (e && e->residual && e->residual_stride < n_out) return qr_fail(QR_EINVAL_SHAPE, "residual_stride is below n_out");
+  if (none) return QR_OK;
+  const Product p = {w, x, wd, xd, bias, y, y_stride, (int)n_out, (int)n_tok, (int)qr_i8_row_bytes(n_in)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  return dst == QR_BF16 ? launch_product<QR_BF16>(p, s) : launch_product<QR_F32>(p, s);
+  if (!e || (e->act == QR_ACT_NONE && !e->up && !e->residual)) return launch_to<PLAIN>(dst, p, Epilogue{}, s);
+  if (e->up) {
+    if (n_out > (INT32_MAX - 256) / 2) return qr_fail(QR_EOVERFLOW, "n_out or n_tok too large");
+    if (!e->upd) return qr_fail(QR_EINVAL_PTR, "up needs upd");
+    if (!qr_aligned(e->up, 16) || !qr_aligned(e->upd, 4) || !qr_aligned(e->up_bias, 4))
+      return qr_fail(QR_EINVAL_PTR, "up must be 16-byte aligned, upd and up_bias to their elements");
+  }
+  if (e->residual) {
+    const int64_t esize = dst == QR_BF16 ? 2 : 4;
+    if (e->residual_stride > INT64_MAX / 4 / n_tok) return qr_fail(QR_EOVERFLOW, "residual_stride is too large");
+    if (!qr_aligned(e->residual, (uintptr_t)esize)) return qr_fail(QR_EINVAL_PTR, "residual must be aligned to its elements");
+    const bool in_place = e->residual == y && (n_tok == 1 || e->residual_stride == y_stride);
+    if (!in_place && rows_meet(y, y_stride * esize, e->residual, e->residual_stride * esize, n_out * esize, n_tok))
+      return qr_fail(QR_EINVAL_PTR, "y and residual must be the same rows or not overlap");
+  }
+  const Epilogue ep = {e->up, e->upd, e->up_bias, e->residual, e->residual_stride, (int)e->act};
+  return e->up ? launch_to<GATED>(dst, p, ep, s) : launch_to<ACT>(dst, p, ep, s);
 }
 
 }  // extern "C"

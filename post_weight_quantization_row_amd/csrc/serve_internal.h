@@ -1,0 +1,170 @@
+// serve_internal.h -- what the serving translation units of libqrow.so share
+// (not part of the C-ABI).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "qrow.h"
+#include "serve/qrow_i8.h"
+
+namespace serve {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+// Vectors at any element of the caller's rows, whose strides are free: memory
+// instructions take them unaligned.
+typedef uint16_t u16x8_any __attribute__((ext_vector_type(8), aligned(2)));
+typedef uint16_t u16x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+constexpr int WAVE = 64;
+
+__device__ __forceinline__ float bf16_value(uint16_t h) { return __builtin_bit_cast(float, (uint32_t)h << 16); }
+
+// fp32 to bf16, round to nearest even (NaN stays NaN).
+__device__ __forceinline__ uint16_t bf16_bits(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+
+// What a wave's lanes wrote to LDS is there for its other lanes.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Eight values of a row from element `at` on; zeros behind n.
+template <int SRC>
+__device__ __forceinline__ void load8(const void* row, int at, int n, float (&v)[8]) {
+  if (at + 8 <= n) {
+    if (SRC == QR_BF16) {
+      const u16x8_any h = *reinterpret_cast<const u16x8_any*>(reinterpret_cast<const uint16_t*>(row) + at);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = bf16_value(h[i]);
+    } else {
+      const f32x4_any* p = reinterpret_cast<const f32x4_any*>(reinterpret_cast<const float*>(row) + at);
+      const f32x4_any a = p[0], b = p[1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = a[i];
+        v[4 + i] = b[i];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = 0.0f;
+      if (at + i < n)
+        v[i] = SRC == QR_BF16 ? bf16_value(reinterpret_cast<const uint16_t*>(row)[at + i])
+                              : reinterpret_cast<const float*>(row)[at + i];
+    }
+  }
+}
+
+// Eight values rounded to codes, in eight bytes.
+__device__ __forceinline__ u32x2 pack_codes(const float (&v)[8], float inv) {
+  u32x2 o;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    uint32_t u = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u |= ((uint32_t)(int)__builtin_rintf(v[4 * w + i] * inv) & 0xffu) << (8 * i);
+    o[w] = u;
+  }
+  return o;
+}
+
+// The scale of codes whose largest magnitude has the bits `top`, and the
+// factor that makes the codes: zero where there are none to make.
+struct CodeScale {
+  float d, inv;
+  bool finite;
+};
+
+__device__ __forceinline__ CodeScale code_scale(uint32_t top) {
+  const float amax = __builtin_bit_cast(float, top);
+  CodeScale s = {amax / 127.0f, 127.0f / amax, top < 0x7f800000u};
+  if (!s.finite || !(s.inv < __builtin_inff())) {
+    s.inv = 0.0f;
+    s.d = s.finite ? 0.0f : __builtin_nanf("");
+  }
+  return s;
+}
+
+// A token's scale as xd * back: above 2^96 it is lowered by 2^32, so that a sum
+// (up to 2^31) times it does not overflow before the channel's scale comes.
+// Powers of two round nothing (8192 tokens, 11008 x 4096: 453 -> 459 us). At
+// the other end a whole number times a scale loses no bits.
+struct TokenScale {
+  float d, back;
+};
+
+__device__ __forceinline__ TokenScale token_scale(float xd) {
+  const bool high = __builtin_fabsf(xd) > 0x1p96f;
+  return {high ? xd * 0x1p-32f : xd, high ? 0x1p32f : 1.0f};
+}
+
+__device__ __forceinline__ float scaled(int sum, const TokenScale& xd, float wd, float bias) {
+  return (((float)sum * xd.d) * wd) * xd.back + bias;
+}
+
+// x / (1 + exp(t)) in fp32. The hardware's exp2 and reciprocal are good to a
+// last place each; the bits that t log2(e) loses are carried on (they count
+// |t| times), and one step mends the quotient. Some 14 instructions; the exact
+// division and exp of the math library take three times that.
+__device__ __forceinline__ float over_one_plus_exp(float x, float t) {
+  const float hi = t * 1.44269502162933349609375f;
+  const float lo = __builtin_fmaf(t, 1.92596299112661746887e-8f, __builtin_fmaf(t, 1.44269502162933349609375f, -hi));
+  const float p = __builtin_amdgcn_exp2f(hi);
+  const float d = 1.0f + __builtin_fmaf(p, lo * 0.693147180559945309417f, p);
+  const float r = __builtin_amdgcn_rcpf(d);
+  const float q = x * r;
+  // (beyond, exp(t) is no number any more, and what is left of x subnormal)
+  return t > 88.0f ? x * 0.0f : t < -88.0f ? x : __builtin_fmaf(__builtin_fmaf(-d, q, x), r, q);
+}
+__device__ __forceinline__ double over_one_plus_exp(double x, double t) { return x / (1.0 + exp(t)); }
+
+// Activations (QR_ACT_*). GELU is x times half erfc(-x / sqrt 2): one plus erf
+// would lose the bits of what is left of it at negative x. Its tanh form is
+// x / (1 + exp(-2u)), since (1 + tanh u) / 2 = 1 / (1 + exp(-2u)).
+template <typename T>
+__device__ __forceinline__ T activation(int act, T x) {
+  switch (act) {
+    case QR_ACT_RELU: return x > T(0) || x != x ? x : T(0);
+    case QR_ACT_SILU: return over_one_plus_exp(x, -x);
+    case QR_ACT_GELU: return x * (T(0.5) * erfc(x * T(-0.70710678118654752440)));
+    case QR_ACT_GELU_TANH:
+      return over_one_plus_exp(x, x * (T(-1.59576912160573071176) - T(0.07135481627260025) * x * x));
+    default: return x;
+  }
+}
+
+// Whether any of n rows of `row` bytes, a_step bytes apart, shares memory with
+// one of the rows at b: parts of one buffer lie between each other without
+// meeting.
+inline bool rows_meet(const void* a_ptr, int64_t a_step, const void* b_ptr, int64_t b_step, int64_t row, int64_t n) {
+  uintptr_t a = (uintptr_t)a_ptr, b = (uintptr_t)b_ptr;
+  if (a + (uintptr_t)((n - 1) * a_step + row) <= b || b + (uintptr_t)((n - 1) * b_step + row) <= a) return false;
+  if (a_step == b_step) {
+    const int64_t apart = (int64_t)((a < b ? b - a : a - b) % (uintptr_t)a_step);
+    return apart < row || a_step - apart < row;
+  }
+  for (int64_t i = 0, j = 0; i < n && j < n;) {   // both ascend: the one that ends first goes on
+    if (a + row <= b) a += a_step, ++i;
+    else if (b + row <= a) b += b_step, ++j;
+    else return true;
+  }
+  return false;
+}
+
+// Whether the n rows of `row` bytes at a, a_step bytes apart, share memory with
+// the `bytes` bytes at b.
+inline bool rows_meet_range(const void* a_ptr, int64_t a_step, int64_t row, int64_t n, const void* b_ptr,
+                            int64_t bytes) {
+  const uintptr_t a = (uintptr_t)a_ptr, b = (uintptr_t)b_ptr, e = b + (uintptr_t)bytes;
+  if (n == 0 || bytes == 0 || e <= a || a + (uintptr_t)((n - 1) * a_step + row) <= b) return false;
+  if (b <= a) return true;                            // reaches into the first row
+  const int64_t into = (int64_t)((b - a) % (uintptr_t)a_step);
+  return into < row || (int64_t)(e - b) > a_step - into;   // (a row follows: the range starts before the last one's end)
+}
+
+}  // namespace serve

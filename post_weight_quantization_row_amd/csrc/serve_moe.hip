@@ -1,0 +1,718 @@
+// serve_moe.hip -- gfx950 kernels and C-ABI of a mixture of experts in 8 bits:
+// the router and the experts of a few tokens (declared in serve/qrow_moe.h).
+
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "qr_internal.h"
+#include "qrow.h"
+#include "serve/qrow_moe.h"
+#include "serve_internal.h"
+
+namespace {
+
+using namespace serve;
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// ---------------------------------------------------------------------------
+// the router
+
+struct Route {
+  const void* x;
+  const void* w;
+  const float* bias;
+  double* logits;        // [splits][n_tok][n_experts]
+  int32_t* ids;
+  float* weights;
+  int64_t x_stride;
+  int n_experts, n_tok, n_in, top_k, splits, score, renorm;
+  float factor;
+};
+
+constexpr int R_CHUNK = 32;      // values of the sum that a wave takes at a time
+constexpr int R_WAVES = 4;
+
+// Logits: 16 TE experts x 16 TT tokens per workgroup, the sum split over its
+// waves (and, with few tiles, over workgroups) in chunks of 32 values. Products
+// of fp32 values are exact in 64 bits, and so are the 64-bit matrix
+// instructions' operands: row li, element lk of each four. A lane loads eight
+// neighbouring values and feeds them to eight instructions, both sides alike.
+template <int SRC, int WSRC, int TE, int TT>
+__global__ __launch_bounds__(R_WAVES* WAVE) void k_route_logits(Route p, int expert_tiles, int token_tiles) {
+  __shared__ f64x4 part[R_WAVES][TE][TT][WAVE];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int li = lane & 15, lk = lane >> 4;
+  int block = (int)blockIdx.x;
+  const int be = block % expert_tiles;
+  block /= expert_tiles;
+  const int bt = block % token_tiles, split = block / token_tiles;
+  const uint8_t *xr[TT], *wr[TE];
+#pragma unroll
+  for (int j = 0; j < TT; ++j) {
+    const int t = (bt * TT + j) * 16 + li;
+    xr[j] = reinterpret_cast<const uint8_t*>(p.x) + (int64_t)(t < p.n_tok ? t : p.n_tok - 1) * p.x_stride * (SRC == QR_BF16 ? 2 : 4);
+  }
+#pragma unroll
+  for (int i = 0; i < TE; ++i) {
+    const int e = (be * TE + i) * 16 + li;
+    wr[i] = reinterpret_cast<const uint8_t*>(p.w) + (int64_t)(e < p.n_experts ? e : p.n_experts - 1) * p.n_in * (WSRC == QR_BF16 ? 2 : 4);
+  }
+  f64x4 acc[TE][TT] = {};
+  const int step = R_WAVES * p.splits * R_CHUNK;
+  for (int k = (split * R_WAVES + wave) * R_CHUNK; k < p.n_in; k += step) {
+    float a[TE][8], b[TT][8];
+#pragma unroll
+    for (int i = 0; i < TE; ++i) load8<WSRC>(wr[i], k + 8 * lk, p.n_in, a[i]);
+#pragma unroll
+    for (int j = 0; j < TT; ++j) load8<SRC>(xr[j], k + 8 * lk, p.n_in, b[j]);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int i = 0; i < TE; ++i)
+#pragma unroll
+        for (int j = 0; j < TT; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)a[i][u], (double)b[j][u], acc[i][j], 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < TE; ++i)
+#pragma unroll
+    for (int j = 0; j < TT; ++j) part[wave][i][j][lane] = acc[i][j];
+  __syncthreads();
+  for (int n = wave; n < TE * TT; n += R_WAVES) {
+    const int i = n / TT, j = n % TT;
+    f64x4 sum = part[0][i][j][lane];
+#pragma unroll
+    for (int v = 1; v < R_WAVES; ++v) sum += part[v][i][j][lane];
+    const int t = (bt * TT + j) * 16 + li;
+    if (t >= p.n_tok) continue;
+    double* out = p.logits + ((int64_t)split * p.n_tok + t) * p.n_experts;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int e = (be * TE + i) * 16 + 4 * v + lk;
+      if (e < p.n_experts) out[e] = sum[v];
+    }
+  }
+}
+
+// 64-bit values in the order of their keys: a NaN above everything, nothing
+// (key 0) below.
+__device__ __forceinline__ uint64_t order_key(double v) {
+  if (v != v) return ~0ull;
+  const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0);   // (-0 as 0)
+  return u >> 63 ? ~u : u | 1ull << 63;
+}
+
+// One wave per token, expert lane + 64 j in its slot j.
+template <int J>
+__global__ __launch_bounds__(256) void k_route_choose(Route p) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= p.n_tok) return;
+  double v[J];
+  uint64_t key[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int e = lane + 64 * j;
+    v[j] = 0.0;
+    if (e < p.n_experts)
+      for (int s = 0; s < p.splits; ++s) v[j] += p.logits[((int64_t)s * p.n_tok + t) * p.n_experts + e];
+  }
+  if (p.score == QR_SCORE_SIGMOID) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) v[j] = 1.0 / (1.0 + exp(-v[j]));
+  } else {
+    double top = -__builtin_inf();
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (lane + 64 * j < p.n_experts) top = v[j] > top ? v[j] : top;
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) {
+      const double o = __shfl_xor(top, s);
+      top = o > top ? o : top;
+    }
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      v[j] = exp(v[j] - top);
+      if (lane + 64 * j < p.n_experts) sum += v[j];
+    }
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) sum += __shfl_xor(sum, s);
+#pragma unroll
+    for (int j = 0; j < J; ++j) v[j] /= sum;
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int e = lane + 64 * j;
+    const float b = p.bias && e < p.n_experts ? p.bias[e] : 0.0f;
+    key[j] = e < p.n_experts && b != -__builtin_inff() ? order_key(v[j] + (double)b) : 0;
+  }
+  // lane r keeps what the r-th round chose
+  int chosen = -1;
+  double score = 0.0;
+  for (int r = 0; r < p.top_k; ++r) {
+    uint64_t best = 0;
+    int at = 0;
+    double mine = 0.0;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (key[j] > best) {
+        best = key[j];
+        at = lane + 64 * j;
+        mine = v[j];
+      }
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) {
+      const uint64_t o = (uint64_t)__shfl_xor((unsigned long long)best, s);
+      const int oa = __shfl_xor(at, s);
+      if (o > best || (o == best && oa < at)) {
+        best = o;
+        at = oa;
+      }
+    }
+    if (best == 0) break;
+    const double won = __shfl(mine, at & 63);
+    if (lane == r) {
+      chosen = at;
+      score = won;
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (lane + 64 * j == at) key[j] = 0;
+  }
+  if (p.renorm) {
+    double sum = score;
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) sum += __shfl_xor(sum, s);
+    score = sum == 0.0 ? 0.0 : score / sum;
+  }
+  if (lane < p.top_k) {
+    p.ids[t * p.top_k + lane] = chosen;
+    p.weights[t * p.top_k + lane] = chosen < 0 ? 0.0f : (float)(score * (double)p.factor);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the experts
+
+struct Moe {
+  const int8_t *gate, *up, *down;
+  const float *gated, *upd, *downd;
+  const int8_t* x;
+  const float* xd;
+  const int32_t* ids;
+  const float* weights;
+  int8_t* h;             // [pairs][64 * blocks] hidden codes
+  float* hd;             // [pairs][scale_pitch] their scales
+  const void* residual;
+  void* y;
+  int64_t expert_rows, residual_stride, y_stride;
+  int n_experts, n_in, n_mid, in_bytes, mid_bytes, blocks, scale_pitch, n_tok, top_k, act;
+};
+
+constexpr int M_WAVES = 8;
+constexpr int M_BLOCK = 64;            // hidden channels of one scale
+constexpr int NO_EXPERT = 0xffff;
+constexpr int MASK_WORDS = QR_MOE_MAX_EXPERTS / 32;
+
+// The rank-th expert of the set, or -1.
+__device__ __forceinline__ int expert_of_rank(const uint32_t* mask, int rank) {
+  int e = -1;
+#pragma unroll 8
+  for (int w = 0; w < MASK_WORDS; ++w) {
+    uint32_t bits = mask[w];
+    const int n = __builtin_popcount(bits);
+    if (rank >= 0 && rank < n) {
+      for (int i = 0; i < rank; ++i) bits &= bits - 1;
+      e = 32 * w + __builtin_ctz(bits);
+    }
+    rank -= n;
+  }
+  return e;
+}
+
+// The choices of n pairs into LDS, and the set of experts that they meet.
+__device__ __forceinline__ void read_choices(const Moe& m, int first, int n, uint16_t* ids, uint32_t* mask) {
+  for (int i = threadIdx.x; i < MASK_WORDS; i += M_WAVES * WAVE) mask[i] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += M_WAVES * WAVE) {
+    const int id = m.ids[first + i];
+    const bool is = (uint32_t)id < (uint32_t)m.n_experts;
+    ids[i] = (uint16_t)(is ? id : NO_EXPERT);
+    if (is) atomicOr(&mask[id >> 5], 1u << (id & 31));
+  }
+  __syncthreads();
+}
+
+// Gate and up products of one block of 64 hidden channels for 16 TT pairs of
+// one expert, and their 8-bit hidden values. Waves 0-3 have 16 channels each and
+// every other 128 values of the sum, waves 4-7 the others.
+template <int TT>
+__device__ __forceinline__ void hidden_block(const Moe& m, int expert, int block, const uint16_t* list, int n,
+                                             i32x4 (*part)[2][4][WAVE], uint32_t (*tops)[64]) {
+  constexpr int BATCH = TT == 4 ? 1 : 2;   // chunks of 128 whose loads are in flight together
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int li = lane & 15, lk = lane >> 4, group = wave & 3, half = wave >> 2;
+  const int c0 = M_BLOCK * block + 16 * group;
+  const int row = c0 + li < m.n_mid ? c0 + li : m.n_mid - 1;   // rows behind the last repeat it
+  const int64_t at = ((int64_t)expert * m.expert_rows + row) * m.in_bytes + 16 * lk;
+  const int8_t *gate = m.gate + at, *up = m.up + at;
+  const int8_t* x[TT];
+#pragma unroll
+  for (int j = 0; j < TT; ++j) {
+    const int i = 16 * j + li < n ? 16 * j + li : n - 1;
+    x[j] = m.x + (int64_t)(list[i] / m.top_k) * m.in_bytes + 16 * lk;
+  }
+  const int chunks = m.in_bytes / 128;
+  i32x4 acc[2][TT] = {};
+  for (int k = half; k < chunks; k += 2 * BATCH) {
+    i32x4 a[BATCH][2][2], b[BATCH][2][TT];
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      const int c = k + 2 * u < chunks ? k + 2 * u : k;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        a[u][s][0] = *reinterpret_cast<const i32x4*>(gate + c * 128 + 64 * s);
+        a[u][s][1] = *reinterpret_cast<const i32x4*>(up + c * 128 + 64 * s);
+#pragma unroll
+        for (int j = 0; j < TT; ++j) b[u][s][j] = *reinterpret_cast<const i32x4*>(x[j] + c * 128 + 64 * s);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      if (k + 2 * u >= chunks) continue;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < TT; ++j)
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+            acc[g][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u][s][g], b[u][s][j], acc[g][j], 0, 0, 0);
+    }
+  }
+  if (half) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int j = 0; j < TT; ++j) part[group][g][j][lane] = acc[g][j];
+  }
+  __syncthreads();
+  float v[TT][4];
+  if (!half) {
+    float gd[4], ud[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int c = c0 + 4 * lk + e;
+      const int64_t r = (int64_t)expert * m.expert_rows + (c < m.n_mid ? c : m.n_mid - 1);
+      gd[e] = m.gated[r];
+      ud[e] = m.upd[r];
+    }
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+      const i32x4 gs = acc[0][j] + part[group][0][j][lane], us = acc[1][j] + part[group][1][j][lane];
+      const int i = 16 * j + li < n ? 16 * j + li : n - 1;
+      const TokenScale xd = token_scale(m.xd[list[i] / m.top_k]);
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        // in 64 bits, so that the codes that are made of it do not hang on the
+        // last place of an exp
+        const double g = (double)scaled(gs[e], xd, gd[e], 0.0f), u = (double)scaled(us[e], xd, ud[e], 0.0f);
+        v[j][e] = c0 + 4 * lk + e < m.n_mid ? (float)(activation(m.act, g) * u) : 0.0f;
+        const uint32_t mag = __builtin_bit_cast(uint32_t, v[j][e]) & 0x7fffffffu;
+        top = mag > top ? mag : top;
+      }
+#pragma unroll
+      for (int s = 16; s < 64; s <<= 1) {
+        const uint32_t o = (uint32_t)__shfl_xor((int)top, s);
+        top = o > top ? o : top;
+      }
+      if (lk == 0) tops[group][16 * j + li] = top;
+    }
+  }
+  __syncthreads();
+  if (!half) {
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+      if (16 * j + li >= n) continue;
+      uint32_t top = 0;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint32_t o = tops[g][16 * j + li];
+        top = o > top ? o : top;
+      }
+      const CodeScale s = code_scale(top);
+      const int pair = list[16 * j + li];
+      uint32_t codes = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        codes |= s.finite ? ((uint32_t)(int)__builtin_rintf(v[j][e] * s.inv) & 0xffu) << (8 * e) : 0u;
+      *reinterpret_cast<uint32_t*>(m.h + ((int64_t)pair * m.blocks + block) * M_BLOCK + 16 * group + 4 * lk) = codes;
+      if (group == 0 && lk == 0) m.hd[(int64_t)pair * m.scale_pitch + block] = s.d;
+    }
+  }
+  __syncthreads();
+}
+
+// One workgroup per expert that is met and block of hidden channels: it finds
+// its expert and the expert's pairs in the choices by itself (a captured call
+// replays with other choices).
+template <int MOST>
+__global__ __launch_bounds__(M_WAVES* WAVE) void k_moe_hidden(Moe m) {
+  extern __shared__ uint16_t dynamic[];
+  __shared__ uint32_t mask[MASK_WORDS];
+  __shared__ int counts[M_WAVES];
+  __shared__ i32x4 part[4][2][4][WAVE];
+  __shared__ uint32_t tops[4][64];
+  const int pairs = m.n_tok * m.top_k;
+  uint16_t *ids = dynamic, *list = dynamic + pairs;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int block = (int)(blockIdx.x % (uint32_t)m.blocks);
+  read_choices(m, 0, pairs, ids, mask);
+  const int expert = expert_of_rank(mask, (int)(blockIdx.x / (uint32_t)m.blocks));
+  if (expert < 0) return;
+  // its pairs in their order: every wave looks through a run of them
+  const int run = ((pairs + M_WAVES - 1) / M_WAVES + 63) & ~63;
+  const int from = wave * run, to = from + run < pairs ? from + run : pairs;
+  int mine = 0;
+  for (int i = from; i < to; i += 64) mine += __builtin_popcountll(__ballot(i + lane < to && ids[i + lane] == expert));
+  if (lane == 0) counts[wave] = mine;
+  __syncthreads();
+  int n = 0, put = 0;
+#pragma unroll
+  for (int w = 0; w < M_WAVES; ++w) {
+    put += w < wave ? counts[w] : 0;
+    n += counts[w];
+  }
+  for (int i = from; i < to; i += 64) {
+    const bool is = i + lane < to && ids[i + lane] == expert;
+    const uint64_t all = __ballot(is);
+    if (is) list[put + __builtin_popcountll(all & ((1ull << lane) - 1))] = (uint16_t)(i + lane);
+    put += __builtin_popcountll(all);
+  }
+  __syncthreads();
+  for (int at = 0; at < n;) {
+    const int left = n - at;
+    if (MOST == 1 || left <= 16) {
+      hidden_block<1>(m, expert, block, list + at, left < 16 ? left : 16, part, tops);
+      at += 16;
+    } else if (MOST == 2 || left <= 32) {
+      hidden_block<2>(m, expert, block, list + at, left < 32 ? left : 32, part, tops);
+      at += 32;
+    } else {
+      hidden_block<4>(m, expert, block, list + at, left < 64 ? left : 64, part, tops);
+      at += 64;
+    }
+  }
+}
+
+constexpr int D_SLOTS = 512;     // partial sums of 16 channels that a workgroup holds
+
+// One expert's sums of 16 output channels over blocks of hidden channels, for
+// 16 TT pairs: exact per block, times the block's scale in fp32.
+template <int TT>
+__device__ __forceinline__ void down_block(const Moe& m, int expert, int c0, int from, int to, const uint16_t* list, int n,
+                                           int first_pair, float (*sums)[16]) {
+  const int lane = threadIdx.x & 63;
+  const int li = lane & 15, lk = lane >> 4;
+  const int64_t row = (int64_t)expert * m.n_in + (c0 + li < m.n_in ? c0 + li : m.n_in - 1);
+  const int8_t* w = m.down + row * m.mid_bytes + 16 * lk;
+  const int8_t* h[TT];
+  const float* hd[TT];
+#pragma unroll
+  for (int j = 0; j < TT; ++j) {
+    const int64_t pair = first_pair + list[16 * j + li < n ? 16 * j + li : n - 1];
+    h[j] = m.h + pair * m.blocks * M_BLOCK + 16 * lk;
+    hd[j] = m.hd + pair * m.scale_pitch;
+  }
+  f32x4 acc[TT] = {};
+  for (int k = from; k < to; k += 4) {
+    i32x4 a[4], b[4][TT];
+    f32x4 d[TT];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int c = k + u < m.blocks ? k + u : m.blocks - 1;
+      a[u] = *reinterpret_cast<const i32x4*>(w + c * 64);
+#pragma unroll
+      for (int j = 0; j < TT; ++j) b[u][j] = *reinterpret_cast<const i32x4*>(h[j] + c * 64);
+    }
+#pragma unroll
+    for (int j = 0; j < TT; ++j) d[j] = *reinterpret_cast<const f32x4*>(hd[j] + k);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (k + u >= m.blocks) continue;
+#pragma unroll
+      for (int j = 0; j < TT; ++j) {
+        const i32x4 s = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u], b[u][j], i32x4{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] += d[j][u] * (float)s[e];
+      }
+    }
+  }
+  float wd[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int c = c0 + 4 * lk + e;
+    wd[e] = m.downd[(int64_t)expert * m.n_in + (c < m.n_in ? c : m.n_in - 1)];
+  }
+#pragma unroll
+  for (int j = 0; j < TT; ++j)
+    if (16 * j + li < n) {
+      f32x4 o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = acc[j][e] * wd[e];
+      *reinterpret_cast<f32x4*>(&sums[list[16 * j + li]][4 * lk]) = o;
+    }
+}
+
+template <int DST>
+__device__ __forceinline__ float value_at(const void* x, int64_t i) {
+  return DST == QR_BF16 ? bf16_value(reinterpret_cast<const uint16_t*>(x)[i]) : reinterpret_cast<const float*>(x)[i];
+}
+
+// 16 output channels of a run of tokens per workgroup. Its waves take the
+// experts that these tokens meet in turn (with fewer than eight of them, parts
+// of an expert's sum), every pair's sums go to LDS, and a token's are added up
+// in the order of its slots.
+template <int DST, int MOST>
+__global__ __launch_bounds__(M_WAVES* WAVE) void k_moe_down(Moe m, int tokens_each) {
+  __shared__ uint32_t mask[MASK_WORDS];
+  __shared__ uint16_t ids[D_SLOTS];
+  __shared__ uint16_t lists[M_WAVES][D_SLOTS];
+  __shared__ float sums[D_SLOTS][16];
+  const int tiles = (m.n_in + 15) / 16;
+  const int c0 = (int)(blockIdx.x % (uint32_t)tiles) * 16, t0 = (int)(blockIdx.x / (uint32_t)tiles) * tokens_each;
+  const int tokens = m.n_tok - t0 < tokens_each ? m.n_tok - t0 : tokens_each;
+  const int first = t0 * m.top_k, pairs = tokens * m.top_k;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  read_choices(m, first, pairs, ids, mask);
+  int met = 0;
+#pragma unroll 8
+  for (int w = 0; w < MASK_WORDS; ++w) met += __builtin_popcount(mask[w]);
+  // parts of a sum in groups of four blocks
+  const int groups = m.scale_pitch / 4;
+  int parts = 1;
+  if (met > 0 && met < M_WAVES) {
+    parts = M_WAVES / met;
+    if (parts > D_SLOTS / pairs) parts = D_SLOTS / pairs;
+    if (parts > groups) parts = groups;
+  }
+  uint16_t* list = lists[wave];
+  for (int item = wave; item < met * parts; item += M_WAVES) {
+    const int part = item % parts;
+    const int expert = expert_of_rank(mask, item / parts);
+    int n = 0;
+    for (int i = 0; i < pairs; i += 64) {
+      const bool is = i + lane < pairs && ids[i + lane] == expert;
+      const uint64_t all = __ballot(is);
+      if (is) list[n + __builtin_popcountll(all & ((1ull << lane) - 1))] = (uint16_t)(i + lane);
+      n += __builtin_popcountll(all);
+    }
+    wave_sync();
+    const int from = groups * part / parts * 4, to = groups * (part + 1) / parts * 4;
+    float(*out)[16] = sums + part * pairs;
+    for (int at = 0; at < n;) {
+      const int left = n - at;
+      if (MOST == 1 || left <= 16) {
+        down_block<1>(m, expert, c0, from, to, list + at, left < 16 ? left : 16, first, out);
+        at += 16;
+      } else {
+        down_block<2>(m, expert, c0, from, to, list + at, left < 32 ? left : 32, first, out);
+        at += 32;
+      }
+    }
+    wave_sync();
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < tokens * 16; i += M_WAVES * WAVE) {
+    const int t = i >> 4, c = c0 + (i & 15);
+    if (c >= m.n_in) continue;
+    float v = 0.0f;
+    for (int j = 0; j < m.top_k; ++j) {
+      const int pair = t * m.top_k + j;
+      if (ids[pair] == NO_EXPERT) continue;
+      float s = sums[pair][i & 15];
+      for (int q = 1; q < parts; ++q) s += sums[q * pairs + pair][i & 15];
+      v += m.weights[first + pair] * s;
+    }
+    if (m.residual) v += value_at<DST>(m.residual, (int64_t)(t0 + t) * m.residual_stride + c);
+    const int64_t at = (int64_t)(t0 + t) * m.y_stride + c;
+    if (DST == QR_BF16) reinterpret_cast<uint16_t*>(m.y)[at] = bf16_bits(v);
+    else reinterpret_cast<float*>(m.y)[at] = v;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+
+struct RoutePlan {
+  bool wide;
+  int expert_tiles, token_tiles, splits;
+};
+
+// Tiles of 32 x 32 where they fill the chip, else of 16 x 16 with the sum split
+// until there are some 512 workgroups.
+RoutePlan route_plan(int64_t n_experts, int64_t n_tok, int64_t n_in) {
+  RoutePlan r;
+  r.wide = ((n_experts + 31) / 32) * ((n_tok + 31) / 32) >= 256;
+  const int64_t tile = r.wide ? 32 : 16;
+  r.expert_tiles = (int)((n_experts + tile - 1) / tile);
+  r.token_tiles = (int)((n_tok + tile - 1) / tile);
+  const int64_t most = (n_in + R_CHUNK * R_WAVES - 1) / (R_CHUNK * R_WAVES);
+  int64_t s = 512 / ((int64_t)r.expert_tiles * r.token_tiles);
+  s = s > 16 ? 16 : s;
+  s = s > most ? most : s;
+  r.splits = (int)(s < 1 ? 1 : s);
+  return r;
+}
+
+template <int SRC, int WSRC>
+int launch_route(const Route& p, const RoutePlan& r, hipStream_t s) {
+  const dim3 grid((uint32_t)(r.expert_tiles * (int64_t)r.token_tiles * r.splits)), block(R_WAVES * WAVE);
+  if (r.wide) hipLaunchKernelGGL((k_route_logits<SRC, WSRC, 2, 2>), grid, block, 0, s, p, r.expert_tiles, r.token_tiles);
+  else hipLaunchKernelGGL((k_route_logits<SRC, WSRC, 1, 1>), grid, block, 0, s, p, r.expert_tiles, r.token_tiles);
+  int rc = qr_check_launch("k_route_logits");
+  if (rc != QR_OK) return rc;
+  const dim3 tokens((uint32_t)((p.n_tok + 3) / 4));
+  if (p.n_experts <= 64) hipLaunchKernelGGL((k_route_choose<1>), tokens, dim3(256), 0, s, p);
+  else if (p.n_experts <= 256) hipLaunchKernelGGL((k_route_choose<4>), tokens, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((k_route_choose<16>), tokens, dim3(256), 0, s, p);
+  return qr_check_launch("k_route_choose");
+}
+
+bool route_shapes(int64_t n_experts, int64_t n_tok, int64_t n_in) {
+  return n_experts >= 1 && n_experts <= QR_MOE_MAX_EXPERTS && n_tok >= 0 && n_tok < 1 << 22 && n_in >= 1 && n_in <= QR_I8_MAX_IN;
+}
+
+bool valid_moe(const qr_moe* m) {
+  return m && m->n_experts >= 1 && m->n_experts <= QR_MOE_MAX_EXPERTS && qr_i8_row_bytes(m->n_in) &&
+         qr_i8_row_bytes(m->n_mid) && m->expert_rows >= m->n_mid && m->expert_rows <= INT64_MAX / 4 / QR_MOE_MAX_EXPERTS / QR_I8_MAX_IN;
+}
+
+bool valid_pairs(int64_t n_tok, int64_t top_k) {
+  return top_k >= 1 && top_k <= QR_MOE_MAX_TOP_K && n_tok >= 0 && n_tok <= QR_MOE_MAX_PAIRS / top_k;
+}
+
+int64_t scale_pitch(int64_t blocks) { return (blocks + 3) / 4 * 4; }
+
+// Bytes of the hidden codes, whole cache lines.
+int64_t code_bytes(int64_t pairs, int64_t blocks) { return (pairs * blocks * M_BLOCK + 255) / 256 * 256; }
+
+template <int DST>
+int launch_moe(const Moe& m, hipStream_t s) {
+  const int64_t pairs = (int64_t)m.n_tok * m.top_k;
+  const int64_t met = pairs < m.n_experts ? pairs : m.n_experts;
+  const dim3 grid((uint32_t)(met * m.blocks)), block(M_WAVES * WAVE);
+  const size_t lds = (size_t)pairs * 2 * sizeof(uint16_t);
+  const int64_t each = (pairs + m.n_experts - 1) / m.n_experts;   // pairs of an expert on average
+  if (each <= 6) hipLaunchKernelGGL((k_moe_hidden<1>), grid, block, lds, s, m);
+  else if (each <= 16) hipLaunchKernelGGL((k_moe_hidden<2>), grid, block, lds, s, m);
+  else hipLaunchKernelGGL((k_moe_hidden<4>), grid, block, lds, s, m);
+  const int rc = qr_check_launch("k_moe_hidden");
+  if (rc != QR_OK) return rc;
+  const int tokens_each = D_SLOTS / m.top_k < 64 ? D_SLOTS / m.top_k : 64;
+  const dim3 tiles((uint32_t)((m.n_in + 15) / 16) * (uint32_t)((m.n_tok + tokens_each - 1) / tokens_each));
+  if (each <= 6) hipLaunchKernelGGL((k_moe_down<DST, 1>), tiles, block, 0, s, m, tokens_each);
+  else hipLaunchKernelGGL((k_moe_down<DST, 2>), tiles, block, 0, s, m, tokens_each);
+  return qr_check_launch("k_moe_down");
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qr_moe_route_workspace_bytes(int64_t n_experts, int64_t n_tok, int64_t n_in) {
+  if (!route_shapes(n_experts, n_tok, n_in) || n_tok == 0) return 0;
+  return (size_t)route_plan(n_experts, n_tok, n_in).splits * (size_t)n_tok * (size_t)n_experts * sizeof(double);
+}
+
+int qr_moe_route(int src, const void* x, int64_t x_stride, int wtype, const void* w, const float* bias,
+                 int64_t n_experts, int64_t n_tok, int64_t n_in, int64_t top_k, int score, int renorm, float factor,
+                 int32_t* ids, float* weights, void* workspace, size_t workspace_bytes, void* stream) {
+  qr_clear_error();
+  if (src != QR_F32 && src != QR_BF16) return qr_fail(QR_EINVAL_TYPE, "source type %d is not QR_F32 or QR_BF16", src);
+  if (wtype != QR_F32 && wtype != QR_BF16) return qr_fail(QR_EINVAL_TYPE, "weight type %d is not QR_F32 or QR_BF16", wtype);
+  if (score != QR_SCORE_SOFTMAX && score != QR_SCORE_SIGMOID) return qr_fail(QR_EINVAL_TYPE, "score %d is not one of QR_SCORE_*", score);
+  if (n_experts < 1 || n_experts > QR_MOE_MAX_EXPERTS)
+    return qr_fail(QR_EINVAL_SHAPE, "n_experts=%lld must be in 1..%d", (long long)n_experts, QR_MOE_MAX_EXPERTS);
+  if (n_in < 1 || n_in > QR_I8_MAX_IN) return qr_fail(QR_EINVAL_SHAPE, "n_in=%lld must be in 1..%d", (long long)n_in, QR_I8_MAX_IN);
+  if (top_k < 1 || top_k > n_experts || top_k > QR_MOE_MAX_TOP_K)
+    return qr_fail(QR_EINVAL_SHAPE, "top_k=%lld must be in 1..min(n_experts, %d)", (long long)top_k, QR_MOE_MAX_TOP_K);
+  if (n_tok < 0 || x_stride < n_in) return qr_fail(QR_EINVAL_SHAPE, "negative n_tok, or x_stride below n_in");
+  if (!(factor - factor == 0.0f)) return qr_fail(QR_EINVAL_SHAPE, "factor must be finite");
+  if (n_tok == 0) return QR_OK;
+  if (!route_shapes(n_experts, n_tok, n_in) || x_stride > INT64_MAX / 4 / n_tok)
+    return qr_fail(QR_EOVERFLOW, "n_tok or x_stride too large");
+  if (!x || !w || !ids || !weights) return qr_fail(QR_EINVAL_PTR, "x, w, ids and weights must be non-NULL");
+  if (!qr_aligned(x, src == QR_BF16 ? 2 : 4) || !qr_aligned(w, wtype == QR_BF16 ? 2 : 4) || !qr_aligned(bias, 4) ||
+      !qr_aligned(ids, 4) || !qr_aligned(weights, 4))
+    return qr_fail(QR_EINVAL_PTR, "x, w, bias, ids and weights must be aligned to their elements");
+  const size_t need = qr_moe_route_workspace_bytes(n_experts, n_tok, n_in);
+  if (!workspace || !qr_aligned(workspace, 256)) return qr_fail(QR_EINVAL_PTR, "workspace must be non-NULL and 256-byte aligned");
+  if (workspace_bytes < need) return qr_fail(QR_EINVAL_SHAPE, "workspace has %zu bytes, %zu are needed", workspace_bytes, need);
+  const RoutePlan r = route_plan(n_experts, n_tok, n_in);
+  const Route p = {x, w, bias, reinterpret_cast<double*>(workspace), ids, weights, x_stride, (int)n_experts, (int)n_tok,
+                   (int)n_in, (int)top_k, r.splits, score, renorm, factor};
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (src == QR_BF16) return wtype == QR_BF16 ? launch_route<QR_BF16, QR_BF16>(p, r, s) : launch_route<QR_BF16, QR_F32>(p, r, s);
+  return wtype == QR_BF16 ? launch_route<QR_F32, QR_BF16>(p, r, s) : launch_route<QR_F32, QR_F32>(p, r, s);
+}
+
+size_t qr_moe_i8_workspace_bytes(const qr_moe* m, int64_t n_tok, int64_t top_k) {
+  if (!valid_moe(m) || !valid_pairs(n_tok, top_k)) return 0;
+  const int64_t pairs = n_tok * top_k, blocks = (m->n_mid + M_BLOCK - 1) / M_BLOCK;
+  return (size_t)(code_bytes(pairs, blocks) + pairs * scale_pitch(blocks) * (int64_t)sizeof(float));
+}
+
+int qr_moe_i8(const qr_moe* m, const int8_t* x, const float* xd, const int32_t* ids, const float* weights,
+              int64_t n_tok, int64_t top_k, int act, const void* residual, int64_t residual_stride, int dst, void* y,
+              int64_t y_stride, void* workspace, size_t workspace_bytes, void* stream) {
+  qr_clear_error();
+  if (!valid_moe(m))
+    return qr_fail(QR_EINVAL_SHAPE, "the experts must number 1..%d, n_in and n_mid lie in 1..%d, expert_rows not below n_mid",
+                   QR_MOE_MAX_EXPERTS, QR_I8_MAX_IN);
+  if (dst != QR_F32 && dst != QR_BF16) return qr_fail(QR_EINVAL_TYPE, "output type %d is not QR_F32 or QR_BF16", dst);
+  if (act < QR_ACT_NONE || act > QR_ACT_GELU_TANH) return qr_fail(QR_EINVAL_TYPE, "activation %d is not one of QR_ACT_*", act);
+  if (top_k < 1 || top_k > QR_MOE_MAX_TOP_K) return qr_fail(QR_EINVAL_SHAPE, "top_k=%lld must be in 1..%d", (long long)top_k, QR_MOE_MAX_TOP_K);
+  if (n_tok < 0 || y_stride < m->n_in || (residual && residual_stride < m->n_in))
+    return qr_fail(QR_EINVAL_SHAPE, "negative n_tok, or y_stride or residual_stride below n_in");
+  if (n_tok == 0) return QR_OK;
+  if (!valid_pairs(n_tok, top_k)) return qr_fail(QR_EOVERFLOW, "n_tok * top_k must be at most %d", QR_MOE_MAX_PAIRS);
+  if (y_stride > INT64_MAX / 4 / n_tok || (residual && residual_stride > INT64_MAX / 4 / n_tok))
+    return qr_fail(QR_EOVERFLOW, "y_stride or residual_stride too large");
+  if (!m->gate || !m->up || !m->down || !m->gated || !m->upd || !m->downd || !x || !xd || !ids || !weights || !y)
+    return qr_fail(QR_EINVAL_PTR, "the experts' arrays, x, xd, ids, weights and y must be non-NULL");
+  const int64_t esize = dst == QR_BF16 ? 2 : 4;
+  if (!qr_aligned(m->gate, 16) || !qr_aligned(m->up, 16) || !qr_aligned(m->down, 16) || !qr_aligned(m->gated, 4) ||
+      !qr_aligned(m->upd, 4) || !qr_aligned(m->downd, 4) || !qr_aligned(x, 16) || !qr_aligned(xd, 4) || !qr_aligned(ids, 4) ||
+      !qr_aligned(weights, 4) || !qr_aligned(y, (uintptr_t)esize) || !qr_aligned(residual, (uintptr_t)esize))
+    return qr_fail(QR_EINVAL_PTR, "codes must be 16-byte aligned, everything else to its elements");
+  const size_t need = qr_moe_i8_workspace_bytes(m, n_tok, top_k);
+  if (!workspace || !qr_aligned(workspace, 256)) return qr_fail(QR_EINVAL_PTR, "workspace must be non-NULL and 256-byte aligned");
+  if (workspace_bytes < need) return qr_fail(QR_EINVAL_SHAPE, "workspace has %zu bytes, %zu are needed", workspace_bytes, need);
+  const int64_t row = m->n_in * esize, pairs = n_tok * top_k, in_bytes = (int64_t)qr_i8_row_bytes(m->n_in);
+  if (residual && !(residual == y && (n_tok == 1 || residual_stride == y_stride)) &&
+      rows_meet(y, y_stride * esize, residual, residual_stride * esize, row, n_tok))
+    return qr_fail(QR_EINVAL_PTR, "y and residual must be the same rows or not overlap");
+  if (rows_meet_range(y, y_stride * esize, row, n_tok, x, n_tok * in_bytes) ||
+      rows_meet_range(y, y_stride * esize, row, n_tok, xd, n_tok * 4) ||
+      rows_meet_range(y, y_stride * esize, row, n_tok, ids, pairs * 4) ||
+      rows_meet_range(y, y_stride * esize, row, n_tok, weights, pairs * 4) ||
+      rows_meet_range(y, y_stride * esize, row, n_tok, workspace, (int64_t)need))
+    return qr_fail(QR_EINVAL_PTR, "y must not overlap x, xd, ids, weights or the workspace");
+  const int64_t blocks = (m->n_mid + M_BLOCK - 1) / M_BLOCK;
+  int8_t* h = reinterpret_cast<int8_t*>(workspace);
+  const Moe a = {m->gate, m->up, m->down, m->gated, m->upd, m->downd, x, xd, ids, weights, h,
+                 reinterpret_cast<float*>(h + code_bytes(pairs, blocks)), residual, y, m->expert_rows, residual_stride,
+                 y_stride, (int)m->n_experts, (int)m->n_in, (int)m->n_mid, (int)in_bytes,
+                 (int)qr_i8_row_bytes(m->n_mid), (int)blocks, (int)scale_pitch(blocks), (int)n_tok, (int)top_k, act};
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  return dst == QR_BF16 ? launch_moe<QR_BF16>(a, s) : launch_moe<QR_F32>(a, s);
+}
+
+}  // extern "C"
