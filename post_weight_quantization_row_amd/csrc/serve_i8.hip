@@ -14,7 +14,6 @@ namespace {
 
 using namespace serve;
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 constexpr int ROW_ALIGN = 128;   // bytes: qr_i8_row_bytes
 

@@ -12,6 +12,7 @@
 namespace serve {
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 // Vectors at any element of the caller's rows, whose strides are free: memory
 // instructions take them unaligned.
 typedef uint16_t u16x8_any __attribute__((ext_vector_type(8), aligned(2)));
@@ -30,6 +31,71 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Operands are loaded from buffers: a base and a step in scalar registers, a
+// lane's place in one 32-bit register that never changes (64-bit addresses, and
+// the registers they were made in, had loads wait for the ones before).
+typedef __amdgpu_buffer_rsrc_t Buffer;
+
+__device__ __forceinline__ Buffer buffer_of(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
+}
+
+// A place behind every buffer: such a lane gets zeros and asks for nothing.
+constexpr uint32_t NOWHERE = 0x80000000u;
+
+__device__ __forceinline__ i32x4 load16(Buffer b, uint32_t lane_at, uint32_t at) {
+  return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, lane_at, at, 0));
+}
+
+// Weights are read once: loads that leave no trace in the caches, of whole
+// 128-byte lines (eight rows a wave's instruction). They pass at 7.0 TB/s, the
+// same lines in halves, 16 rows at a time as the matrix instruction takes them,
+// at 6.0, and both at 6.3 through the caches (3.8 GB, nothing else done).
+__device__ __forceinline__ i32x4 load16_once(Buffer b, uint32_t lane_at, uint32_t at) {
+  constexpr int NONTEMPORAL = 2;
+  return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, lane_at, at, NONTEMPORAL));
+}
+
+// multiply(stage, k) for k = from, from + step, ... below to, with the loads
+// DEPTH stages ahead: every stage is asked for again as soon as it is used.
+template <int DEPTH, typename Stage, typename Load, typename Multiply>
+__device__ __forceinline__ void pipeline(int from, int to, int step, Load load, Multiply multiply) {
+  Stage stage[DEPTH];
+#pragma unroll
+  for (int s = 0; s < DEPTH; ++s)
+    if (from + s * step < to) load(stage[s], from + s * step);
+  int k = from;
+  for (; k + (2 * DEPTH - 1) * step < to; k += DEPTH * step) {
+#pragma unroll
+    for (int s = 0; s < DEPTH; ++s) {
+      multiply(stage[s], k + s * step);
+      load(stage[s], k + (s + DEPTH) * step);
+      __builtin_amdgcn_sched_barrier(0);   // or the loads of all stages are waited for together
+    }
+  }
+  for (; k < to; k += DEPTH * step) {
+#pragma unroll
+    for (int s = 0; s < DEPTH; ++s) {
+      if (k + s * step < to) multiply(stage[s], k + s * step);
+      if (k + (s + DEPTH) * step < to) load(stage[s], k + (s + DEPTH) * step);
+    }
+  }
+}
+
+// 128 bytes of 16 rows: `low` has rows 0-7, `high` rows 8-15, lanes li < 8 of
+// each their first 64 bytes, the others their last. As the matrix instruction
+// takes them (row li, bytes 16 lk): the first halves into `low`, the last ones
+// into `high`, by a turn of half the lanes of each.
+__device__ __forceinline__ void turn(i32x4& low, i32x4& high) {
+  constexpr int ROR8 = 0x128;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int a = low[i], b = high[i];
+    low[i] = __builtin_amdgcn_update_dpp(a, b, ROR8, 0xf, 0xc, false);
+    high[i] = __builtin_amdgcn_update_dpp(b, a, ROR8, 0xf, 0x3, false);
+  }
 }
 
 // Eight values of a row from element `at` on; zeros behind n.

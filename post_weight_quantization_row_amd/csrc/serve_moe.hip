@@ -14,7 +14,6 @@ namespace {
 
 using namespace serve;
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -220,7 +219,40 @@ constexpr int M_BLOCK = 64;            // hidden channels of one scale
 constexpr int NO_EXPERT = 0xffff;
 constexpr int MASK_WORDS = QR_MOE_MAX_EXPERTS / 32;
 
-// The rank-th expert of the set, or -1.
+// The pairs (a token and a slot) of a run that meet one expert.
+struct Met {
+  int expert;            // -1: none
+  int n;
+  uint64_t set;          // up to 64 pairs: which they are
+  const uint16_t* list;  // more: their numbers
+};
+
+// Up to 64 pairs: a wave holds a choice per lane, finds the rank-th expert (in
+// the order in which they first appear) and its pairs with ballots alone.
+__device__ __forceinline__ int choice_of(const Moe& m, int first, int n) {
+  const int lane = threadIdx.x & 63;
+  const int id = lane < n ? m.ids[first + lane] : -1;
+  return (uint32_t)id < (uint32_t)m.n_experts ? id : -1;
+}
+
+__device__ __forceinline__ Met met_of_few(int choice, int rank) {
+  uint64_t left = __ballot(choice >= 0);
+  Met r = {-1, 0, 0, nullptr};
+  for (; left; --rank) {
+    const int e = __builtin_amdgcn_readlane(choice, __builtin_ctzll(left));
+    const uint64_t set = __ballot(choice == e);
+    if (rank == 0) {
+      r.expert = e;
+      r.n = __builtin_popcountll(set);
+      r.set = set;
+      break;
+    }
+    left &= ~set;
+  }
+  return r;
+}
+
+// The rank-th expert of a set in LDS, or -1.
 __device__ __forceinline__ int expert_of_rank(const uint32_t* mask, int rank) {
   int e = -1;
 #pragma unroll 8
@@ -249,163 +281,190 @@ __device__ __forceinline__ void read_choices(const Moe& m, int first, int n, uin
   __syncthreads();
 }
 
+// The at-th of the expert's pairs, the last one again behind them.
+template <bool FEW>
+__device__ __forceinline__ int pair_of(const Met& r, int at) {
+  if (at > r.n - 1) at = r.n - 1;
+  if (!FEW) return r.list[at];
+  // the at-th set bit, halving the words that it may lie in
+  uint32_t word = (uint32_t)r.set;
+  int found = 0, below = __builtin_popcount(word);
+  if (at >= below) {
+    at -= below;
+    word = (uint32_t)(r.set >> 32);
+    found = 32;
+  }
+#pragma unroll
+  for (int width = 16; width > 0; width >>= 1) {
+    below = __builtin_popcount(word & ((1u << width) - 1));
+    if (at >= below) {
+      at -= below;
+      word >>= width;
+      found += width;
+    }
+  }
+  return found;
+}
+
 // Gate and up products of one block of 64 hidden channels for 16 TT pairs of
 // one expert, and their 8-bit hidden values. Waves 0-3 have 16 channels each and
-// every other 128 values of the sum, waves 4-7 the others.
-template <int TT>
-__device__ __forceinline__ void hidden_block(const Moe& m, int expert, int block, const uint16_t* list, int n,
-                                             i32x4 (*part)[2][4][WAVE], uint32_t (*tops)[64]) {
-  constexpr int BATCH = TT == 4 ? 1 : 2;   // chunks of 128 whose loads are in flight together
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// the first half of the sum, waves 4-7 the second; a wave holds one batch of
+// loads while the next is on its way.
+template <int TT, int MOST, bool FEW>
+__device__ __forceinline__ void hidden_block(const Moe& m, const Met& met, int first, int block,
+                                             i32x4 (*part)[4][2][MOST][WAVE]) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 15, lk = lane >> 4, group = wave & 3, half = wave >> 2;
   const int c0 = M_BLOCK * block + 16 * group;
-  const int row = c0 + li < m.n_mid ? c0 + li : m.n_mid - 1;   // rows behind the last repeat it
-  const int64_t at = ((int64_t)expert * m.expert_rows + row) * m.in_bytes + 16 * lk;
-  const int8_t *gate = m.gate + at, *up = m.up + at;
-  const int8_t* x[TT];
+  const int64_t rows = (int64_t)__builtin_amdgcn_readfirstlane(met.expert) * m.expert_rows;
+  const int first_row = c0 < m.n_mid ? c0 : m.n_mid - 1, row_left = m.n_mid - 1 - first_row < 15 ? m.n_mid - 1 - first_row : 15;
+  const Buffer gate = buffer_of(m.gate + (rows + first_row) * m.in_bytes, (uint32_t)(row_left + 1) * (uint32_t)m.in_bytes);
+  const Buffer up = buffer_of(m.up + (rows + first_row) * m.in_bytes, (uint32_t)(row_left + 1) * (uint32_t)m.in_bytes);
+  const Buffer xs = buffer_of(m.x, (uint32_t)m.n_tok * (uint32_t)m.in_bytes);
+  uint32_t at[2], x[TT];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = 8 * h + (li & 7);        // rows behind the last repeat it
+    at[h] = (uint32_t)(r < row_left ? r : row_left) * (uint32_t)m.in_bytes + 64 * (li >> 3) + 16 * lk;
+  }
 #pragma unroll
   for (int j = 0; j < TT; ++j) {
-    const int i = 16 * j + li < n ? 16 * j + li : n - 1;
-    x[j] = m.x + (int64_t)(list[i] / m.top_k) * m.in_bytes + 16 * lk;
+    const int i = first + 16 * j + li;
+    x[j] = i < met.n ? (uint32_t)(pair_of<FEW>(met, i) / m.top_k) * (uint32_t)m.in_bytes + 16 * lk : NOWHERE;
   }
-  const int chunks = m.in_bytes / 128;
+  // what the epilogue needs: two channels of one pair per lane
+  const int hc = M_BLOCK * block + 2 * (lane & 31);
+  float gd[2], ud[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int64_t r = rows + (hc + e < m.n_mid ? hc + e : m.n_mid - 1);
+    gd[e] = m.gated[r];
+    ud[e] = m.upd[r];
+  }
+  const int chunks = m.in_bytes / 128, middle = (chunks + 1) / 2;
+  const int from = half ? middle : 0, to = half ? chunks : middle;
   i32x4 acc[2][TT] = {};
-  for (int k = half; k < chunks; k += 2 * BATCH) {
-    i32x4 a[BATCH][2][2], b[BATCH][2][TT];
+  struct Stage {
+    i32x4 a[2][2], b[2][TT];
+  };
+  pipeline<TT == 1 ? 4 : 2, Stage>(from, to, 1,
+      [&](Stage& s, int k) {
 #pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      const int c = k + 2 * u < chunks ? k + 2 * u : k;
+        for (int h = 0; h < 2; ++h) {
+          s.a[0][h] = load16_once(gate, at[h], k * 128);
+          s.a[1][h] = load16_once(up, at[h], k * 128);
+        }
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        a[u][s][0] = *reinterpret_cast<const i32x4*>(gate + c * 128 + 64 * s);
-        a[u][s][1] = *reinterpret_cast<const i32x4*>(up + c * 128 + 64 * s);
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < TT; ++j) b[u][s][j] = *reinterpret_cast<const i32x4*>(x[j] + c * 128 + 64 * s);
-      }
-    }
+          for (int j = 0; j < TT; ++j) s.b[h][j] = load16(xs, x[j], k * 128 + 64 * h);
+      },
+      [&](Stage& s, int) {
 #pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      if (k + 2 * u >= chunks) continue;
+        for (int g = 0; g < 2; ++g) {
+          turn(s.a[g][0], s.a[g][1]);
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < TT; ++j)
+            for (int j = 0; j < TT; ++j)
+              acc[g][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(s.a[g][h], s.b[h][j], acc[g][j], 0, 0, 0);
+        }
+      });
 #pragma unroll
-          for (int g = 0; g < 2; ++g)
-            acc[g][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u][s][g], b[u][s][j], acc[g][j], 0, 0, 0);
-    }
-  }
-  if (half) {
+  for (int g = 0; g < 2; ++g)
 #pragma unroll
-    for (int g = 0; g < 2; ++g)
-#pragma unroll
-      for (int j = 0; j < TT; ++j) part[group][g][j][lane] = acc[g][j];
-  }
+    for (int j = 0; j < TT; ++j) part[half][group][g][j][lane] = acc[g][j];
   __syncthreads();
-  float v[TT][4];
-  if (!half) {
-    float gd[4], ud[4];
+  // half a wave per pair
+#pragma unroll 1
+  for (int q = 2 * wave + (lane >> 5); q < 16 * TT; q += 2 * M_WAVES) {
+    if (first + q >= met.n) break;
+    const int pair = pair_of<FEW>(met, first + q), c = 2 * (lane & 31);
+    const TokenScale d = token_scale(m.xd[pair / m.top_k]);
+    const int* sums = reinterpret_cast<const int*>(part);
+    float v[2];
+    uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int c = c0 + 4 * lk + e;
-      const int64_t r = (int64_t)expert * m.expert_rows + (c < m.n_mid ? c : m.n_mid - 1);
-      gd[e] = m.gated[r];
-      ud[e] = m.upd[r];
+    for (int e = 0; e < 2; ++e) {
+      // sum of channel 16 g' + 4 lk + i of column li: element i of lane 16 lk + li
+      const int of = (((c >> 4) * 2 * MOST + (q >> 4)) * WAVE + ((c >> 2) & 3) * 16 + (q & 15)) * 4 + (c & 3) + e;
+      constexpr int UP = MOST * WAVE * 4, HALF = 4 * 2 * MOST * WAVE * 4;
+      // in 64 bits, so that the codes that are made of it do not hang on the
+      // last place of an exp
+      const double g = (double)scaled(sums[of] + sums[of + HALF], d, gd[e], 0.0f);
+      const double u = (double)scaled(sums[of + UP] + sums[of + UP + HALF], d, ud[e], 0.0f);
+      v[e] = hc + e < m.n_mid ? (float)(activation(m.act, g) * u) : 0.0f;
+      const uint32_t mag = __builtin_bit_cast(uint32_t, v[e]) & 0x7fffffffu;
+      top = mag > top ? mag : top;
     }
 #pragma unroll
-    for (int j = 0; j < TT; ++j) {
-      const i32x4 gs = acc[0][j] + part[group][0][j][lane], us = acc[1][j] + part[group][1][j][lane];
-      const int i = 16 * j + li < n ? 16 * j + li : n - 1;
-      const TokenScale xd = token_scale(m.xd[list[i] / m.top_k]);
-      uint32_t top = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        // in 64 bits, so that the codes that are made of it do not hang on the
-        // last place of an exp
-        const double g = (double)scaled(gs[e], xd, gd[e], 0.0f), u = (double)scaled(us[e], xd, ud[e], 0.0f);
-        v[j][e] = c0 + 4 * lk + e < m.n_mid ? (float)(activation(m.act, g) * u) : 0.0f;
-        const uint32_t mag = __builtin_bit_cast(uint32_t, v[j][e]) & 0x7fffffffu;
-        top = mag > top ? mag : top;
-      }
-#pragma unroll
-      for (int s = 16; s < 64; s <<= 1) {
-        const uint32_t o = (uint32_t)__shfl_xor((int)top, s);
-        top = o > top ? o : top;
-      }
-      if (lk == 0) tops[group][16 * j + li] = top;
+    for (int s = 16; s > 0; s >>= 1) {
+      const uint32_t o = (uint32_t)__shfl_xor((int)top, s);
+      top = o > top ? o : top;
     }
-  }
-  __syncthreads();
-  if (!half) {
-#pragma unroll
-    for (int j = 0; j < TT; ++j) {
-      if (16 * j + li >= n) continue;
-      uint32_t top = 0;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const uint32_t o = tops[g][16 * j + li];
-        top = o > top ? o : top;
-      }
-      const CodeScale s = code_scale(top);
-      const int pair = list[16 * j + li];
-      uint32_t codes = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        codes |= s.finite ? ((uint32_t)(int)__builtin_rintf(v[j][e] * s.inv) & 0xffu) << (8 * e) : 0u;
-      *reinterpret_cast<uint32_t*>(m.h + ((int64_t)pair * m.blocks + block) * M_BLOCK + 16 * group + 4 * lk) = codes;
-      if (group == 0 && lk == 0) m.hd[(int64_t)pair * m.scale_pitch + block] = s.d;
-    }
+    const CodeScale s = code_scale(top);
+    const int lo = s.finite ? (int)__builtin_rintf(v[0] * s.inv) : 0, hi = s.finite ? (int)__builtin_rintf(v[1] * s.inv) : 0;
+    *reinterpret_cast<uint16_t*>(m.h + ((int64_t)pair * m.blocks + block) * M_BLOCK + c) =
+        (uint16_t)((lo & 0xff) | (hi & 0xff) << 8);
+    if ((lane & 31) == 0) m.hd[(int64_t)pair * m.scale_pitch + block] = s.d;
   }
   __syncthreads();
 }
 
 // One workgroup per expert that is met and block of hidden channels: it finds
 // its expert and the expert's pairs in the choices by itself (a captured call
-// replays with other choices).
-template <int MOST>
-__global__ __launch_bounds__(M_WAVES* WAVE) void k_moe_hidden(Moe m) {
+// replays with other choices). FEW: all pairs fit into a wave's lanes.
+template <int MOST, bool FEW>
+__global__ __launch_bounds__(M_WAVES* WAVE) __attribute__((amdgpu_waves_per_eu(2))) void k_moe_hidden(Moe m) {
   extern __shared__ uint16_t dynamic[];
   __shared__ uint32_t mask[MASK_WORDS];
   __shared__ int counts[M_WAVES];
-  __shared__ i32x4 part[4][2][4][WAVE];
-  __shared__ uint32_t tops[4][64];
+  __shared__ i32x4 part[2][4][2][MOST][WAVE];
   const int pairs = m.n_tok * m.top_k;
-  uint16_t *ids = dynamic, *list = dynamic + pairs;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int block = (int)(blockIdx.x % (uint32_t)m.blocks);
-  read_choices(m, 0, pairs, ids, mask);
-  const int expert = expert_of_rank(mask, (int)(blockIdx.x / (uint32_t)m.blocks));
-  if (expert < 0) return;
-  // its pairs in their order: every wave looks through a run of them
-  const int run = ((pairs + M_WAVES - 1) / M_WAVES + 63) & ~63;
-  const int from = wave * run, to = from + run < pairs ? from + run : pairs;
-  int mine = 0;
-  for (int i = from; i < to; i += 64) mine += __builtin_popcountll(__ballot(i + lane < to && ids[i + lane] == expert));
-  if (lane == 0) counts[wave] = mine;
-  __syncthreads();
-  int n = 0, put = 0;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int block = (int)(blockIdx.x % (uint32_t)m.blocks), rank = (int)(blockIdx.x / (uint32_t)m.blocks);
+  Met met;
+  if (FEW) {
+    met = met_of_few(choice_of(m, 0, pairs), rank);
+    if (met.expert < 0) return;
+  } else {
+    uint16_t *ids = dynamic, *list = dynamic + pairs;
+    read_choices(m, 0, pairs, ids, mask);
+    met.expert = __builtin_amdgcn_readfirstlane(expert_of_rank(mask, rank));
+    if (met.expert < 0) return;
+    // its pairs in their order: every wave looks through a run of them
+    const int run = ((pairs + M_WAVES - 1) / M_WAVES + 63) & ~63;
+    const int from = wave * run, to = from + run < pairs ? from + run : pairs;
+    int mine = 0;
+    for (int i = from; i < to; i += 64) mine += __builtin_popcountll(__ballot(i + lane < to && ids[i + lane] == met.expert));
+    if (lane == 0) counts[wave] = mine;
+    __syncthreads();
+    int n = 0, put = 0;
 #pragma unroll
-  for (int w = 0; w < M_WAVES; ++w) {
-    put += w < wave ? counts[w] : 0;
-    n += counts[w];
+    for (int w = 0; w < M_WAVES; ++w) {
+      put += w < wave ? counts[w] : 0;
+      n += counts[w];
+    }
+    for (int i = from; i < to; i += 64) {
+      const bool is = i + lane < to && ids[i + lane] == met.expert;
+      const uint64_t all = __ballot(is);
+      if (is) list[put + __builtin_popcountll(all & ((1ull << lane) - 1))] = (uint16_t)(i + lane);
+      put += __builtin_popcountll(all);
+    }
+    __syncthreads();
+    met.n = __builtin_amdgcn_readfirstlane(n);
+    met.list = list;
   }
-  for (int i = from; i < to; i += 64) {
-    const bool is = i + lane < to && ids[i + lane] == expert;
-    const uint64_t all = __ballot(is);
-    if (is) list[put + __builtin_popcountll(all & ((1ull << lane) - 1))] = (uint16_t)(i + lane);
-    put += __builtin_popcountll(all);
-  }
-  __syncthreads();
-  for (int at = 0; at < n;) {
-    const int left = n - at;
+  for (int at = 0; at < met.n;) {
+    const int left = met.n - at;
     if (MOST == 1 || left <= 16) {
-      hidden_block<1>(m, expert, block, list + at, left < 16 ? left : 16, part, tops);
+      hidden_block<1, MOST, FEW>(m, met, at, block, part);
       at += 16;
     } else if (MOST == 2 || left <= 32) {
-      hidden_block<2>(m, expert, block, list + at, left < 32 ? left : 32, part, tops);
+      hidden_block<2, MOST, FEW>(m, met, at, block, part);
       at += 32;
     } else {
-      hidden_block<4>(m, expert, block, list + at, left < 64 ? left : 64, part, tops);
+      if constexpr (MOST == 4) hidden_block<4, MOST, FEW>(m, met, at, block, part);
       at += 64;
     }
   }
@@ -415,58 +474,83 @@ constexpr int D_SLOTS = 512;     // partial sums of 16 channels that a workgroup
 
 // One expert's sums of 16 output channels over blocks of hidden channels, for
 // 16 TT pairs: exact per block, times the block's scale in fp32.
-template <int TT>
-__device__ __forceinline__ void down_block(const Moe& m, int expert, int c0, int from, int to, const uint16_t* list, int n,
-                                           int first_pair, float (*sums)[16]) {
+template <int TT, bool FEW>
+__device__ __forceinline__ void down_block(const Moe& m, const Met& met, int at, int c0, int from, int to, int first_pair,
+                                           float (*sums)[16]) {
   const int lane = threadIdx.x & 63;
   const int li = lane & 15, lk = lane >> 4;
-  const int64_t row = (int64_t)expert * m.n_in + (c0 + li < m.n_in ? c0 + li : m.n_in - 1);
-  const int8_t* w = m.down + row * m.mid_bytes + 16 * lk;
-  const int8_t* h[TT];
-  const float* hd[TT];
+  const int64_t rows = (int64_t)__builtin_amdgcn_readfirstlane(met.expert) * m.n_in;
+  const Buffer w = buffer_of(m.down + (rows + c0) * m.mid_bytes,
+                             (uint32_t)(m.n_in - c0 < 16 ? m.n_in - c0 : 16) * (uint32_t)m.mid_bytes);
+  const uint32_t pairs = (uint32_t)(m.n_tok * m.top_k);
+  const Buffer hs = buffer_of(m.h, pairs * (uint32_t)(m.blocks * M_BLOCK)), hds = buffer_of(m.hd, pairs * (uint32_t)(m.scale_pitch * 4));
+  uint32_t off[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = 8 * h + (li & 7);        // rows behind the last repeat it
+    off[h] = (uint32_t)(c0 + r < m.n_in ? r : m.n_in - 1 - c0) * (uint32_t)m.mid_bytes + 64 * (li >> 3) + 16 * lk;
+  }
+  int pair[TT];
+  uint32_t h[TT], hd[TT];
 #pragma unroll
   for (int j = 0; j < TT; ++j) {
-    const int64_t pair = first_pair + list[16 * j + li < n ? 16 * j + li : n - 1];
-    h[j] = m.h + pair * m.blocks * M_BLOCK + 16 * lk;
-    hd[j] = m.hd + pair * m.scale_pitch;
+    pair[j] = pair_of<FEW>(met, at + 16 * j + li);
+    const bool is = at + 16 * j + li < met.n;
+    h[j] = is ? (uint32_t)(first_pair + pair[j]) * (uint32_t)(m.blocks * M_BLOCK) + 16 * lk : NOWHERE;
+    hd[j] = is ? (uint32_t)(first_pair + pair[j]) * (uint32_t)(m.scale_pitch * 4) : NOWHERE;
   }
   f32x4 acc[TT] = {};
-  for (int k = from; k < to; k += 4) {
+  // four blocks, 256 bytes of a row, at a time; behind the last block the row
+  // of codes has zeros up to its next 128, the hidden row nothing
+  const int last = m.mid_bytes - 128;
+  struct Stage {
     i32x4 a[4], b[4][TT];
     f32x4 d[TT];
+  };
+  pipeline<2, Stage>(from, to, 4,
+      [&](Stage& s, int k) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int c = k + u < m.blocks ? k + u : m.blocks - 1;
-      a[u] = *reinterpret_cast<const i32x4*>(w + c * 64);
+        for (int u = 0; u < 2; ++u) {
+          const int c = k * 64 + 128 * u < last ? k * 64 + 128 * u : last;
+          s.a[2 * u] = load16_once(w, off[0], c);
+          s.a[2 * u + 1] = load16_once(w, off[1], c);
+        }
 #pragma unroll
-      for (int j = 0; j < TT; ++j) b[u][j] = *reinterpret_cast<const i32x4*>(h[j] + c * 64);
-    }
+        for (int u = 0; u < 4; ++u) {
+          const int c = k + u < m.blocks ? k + u : m.blocks - 1;
 #pragma unroll
-    for (int j = 0; j < TT; ++j) d[j] = *reinterpret_cast<const f32x4*>(hd[j] + k);
+          for (int j = 0; j < TT; ++j) s.b[u][j] = load16(hs, h[j], c * 64);
+        }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (k + u >= m.blocks) continue;
+        for (int j = 0; j < TT; ++j) s.d[j] = __builtin_bit_cast(f32x4, load16(hds, hd[j], k * 4));
+      },
+      [&](Stage& s, int k) {
+        turn(s.a[0], s.a[1]);
+        turn(s.a[2], s.a[3]);
 #pragma unroll
-      for (int j = 0; j < TT; ++j) {
-        const i32x4 s = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u], b[u][j], i32x4{0, 0, 0, 0}, 0, 0, 0);
+        for (int u = 0; u < 4; ++u) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][e] += d[j][u] * (float)s[e];
-      }
-    }
-  }
+          for (int j = 0; j < TT; ++j) {
+            const i32x4 p = __builtin_amdgcn_mfma_i32_16x16x64_i8(s.a[u], s.b[u][j], i32x4{0, 0, 0, 0}, 0, 0, 0);
+            const float d = k + u < m.blocks ? s.d[j][u] : 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][e] += d * (float)p[e];
+          }
+        }
+      });
   float wd[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int c = c0 + 4 * lk + e;
-    wd[e] = m.downd[(int64_t)expert * m.n_in + (c < m.n_in ? c : m.n_in - 1)];
+    wd[e] = m.downd[rows + (c < m.n_in ? c : m.n_in - 1)];
   }
 #pragma unroll
   for (int j = 0; j < TT; ++j)
-    if (16 * j + li < n) {
+    if (at + 16 * j + li < met.n) {
       f32x4 o;
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = acc[j][e] * wd[e];
-      *reinterpret_cast<f32x4*>(&sums[list[16 * j + li]][4 * lk]) = o;
+      *reinterpret_cast<f32x4*>(&sums[pair[j]][4 * lk]) = o;
     }
 }
 
@@ -479,57 +563,76 @@ __device__ __forceinline__ float value_at(const void* x, int64_t i) {
 // experts that these tokens meet in turn (with fewer than eight of them, parts
 // of an expert's sum), every pair's sums go to LDS, and a token's are added up
 // in the order of its slots.
-template <int DST, int MOST>
-__global__ __launch_bounds__(M_WAVES* WAVE) void k_moe_down(Moe m, int tokens_each) {
+template <int DST, int MOST, bool FEW>
+__global__ __launch_bounds__(M_WAVES* WAVE) __attribute__((amdgpu_waves_per_eu(MOST == 1 ? 4 : 2))) void k_moe_down(Moe m, int tokens_each) {
+  constexpr int PAIRS = FEW ? 64 : D_SLOTS;
   __shared__ uint32_t mask[MASK_WORDS];
-  __shared__ uint16_t ids[D_SLOTS];
-  __shared__ uint16_t lists[M_WAVES][D_SLOTS];
+  __shared__ uint16_t ids[PAIRS];
+  __shared__ float weights[PAIRS];
+  __shared__ uint16_t lists[FEW ? 1 : M_WAVES][PAIRS];
   __shared__ float sums[D_SLOTS][16];
   const int tiles = (m.n_in + 15) / 16;
   const int c0 = (int)(blockIdx.x % (uint32_t)tiles) * 16, t0 = (int)(blockIdx.x / (uint32_t)tiles) * tokens_each;
   const int tokens = m.n_tok - t0 < tokens_each ? m.n_tok - t0 : tokens_each;
   const int first = t0 * m.top_k, pairs = tokens * m.top_k;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  read_choices(m, first, pairs, ids, mask);
-  int met = 0;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if (tid < pairs) weights[tid] = m.weights[first + tid];
+  int choice = -1, met_all = 0;
+  if (FEW) {
+    choice = choice_of(m, first, pairs);
+    if (tid < pairs) ids[tid] = (uint16_t)(choice < 0 ? NO_EXPERT : choice);
+    for (uint64_t left = __ballot(choice >= 0); left; ++met_all)
+      left &= ~__ballot(choice == __builtin_amdgcn_readlane(choice, __builtin_ctzll(left)));
+  } else {
+    read_choices(m, first, pairs, ids, mask);
 #pragma unroll 8
-  for (int w = 0; w < MASK_WORDS; ++w) met += __builtin_popcount(mask[w]);
+    for (int w = 0; w < MASK_WORDS; ++w) met_all += __builtin_popcount(mask[w]);
+    met_all = __builtin_amdgcn_readfirstlane(met_all);
+  }
   // parts of a sum in groups of four blocks
   const int groups = m.scale_pitch / 4;
   int parts = 1;
-  if (met > 0 && met < M_WAVES) {
-    parts = M_WAVES / met;
+  if (met_all > 0 && met_all < M_WAVES) {
+    parts = M_WAVES / met_all;
     if (parts > D_SLOTS / pairs) parts = D_SLOTS / pairs;
     if (parts > groups) parts = groups;
   }
-  uint16_t* list = lists[wave];
-  for (int item = wave; item < met * parts; item += M_WAVES) {
+  for (int item = wave; item < met_all * parts; item += M_WAVES) {
     const int part = item % parts;
-    const int expert = expert_of_rank(mask, item / parts);
-    int n = 0;
-    for (int i = 0; i < pairs; i += 64) {
-      const bool is = i + lane < pairs && ids[i + lane] == expert;
-      const uint64_t all = __ballot(is);
-      if (is) list[n + __builtin_popcountll(all & ((1ull << lane) - 1))] = (uint16_t)(i + lane);
-      n += __builtin_popcountll(all);
+    Met met;
+    if (FEW) {
+      met = met_of_few(choice, item / parts);
+    } else {
+      uint16_t* list = lists[wave];
+      met.expert = __builtin_amdgcn_readfirstlane(expert_of_rank(mask, item / parts));
+      met.n = 0;
+      met.list = list;
+      for (int i = 0; i < pairs; i += 64) {
+        const bool is = i + lane < pairs && ids[i + lane] == met.expert;
+        const uint64_t all = __ballot(is);
+        if (is) list[met.n + __builtin_popcountll(all & ((1ull << lane) - 1))] = (uint16_t)(i + lane);
+        met.n += __builtin_popcountll(all);
+      }
+      wave_sync();
     }
-    wave_sync();
     const int from = groups * part / parts * 4, to = groups * (part + 1) / parts * 4;
     float(*out)[16] = sums + part * pairs;
-    for (int at = 0; at < n;) {
-      const int left = n - at;
-      if (MOST == 1 || left <= 16) {
-        down_block<1>(m, expert, c0, from, to, list + at, left < 16 ? left : 16, first, out);
+    for (int at = 0; at < met.n;) {
+      if (MOST == 1 || met.n - at <= 16) {
+        down_block<1, FEW>(m, met, at, c0, from, to, first, out);
         at += 16;
       } else {
-        down_block<2>(m, expert, c0, from, to, list + at, left < 32 ? left : 32, first, out);
+        if constexpr (MOST == 2) down_block<2, FEW>(m, met, at, c0, from, to, first, out);
         at += 32;
       }
     }
-    wave_sync();
+    if (!FEW) wave_sync();   // the list has been read
   }
+  float residual = 0.0f;
+  const bool mine = tid < tokens * 16 && c0 + (tid & 15) < m.n_in;
+  if (m.residual && mine) residual = value_at<DST>(m.residual, (int64_t)(t0 + (tid >> 4)) * m.residual_stride + c0 + (tid & 15));
   __syncthreads();
-  for (int i = threadIdx.x; i < tokens * 16; i += M_WAVES * WAVE) {
+  for (int i = tid; i < tokens * 16; i += M_WAVES * WAVE) {
     const int t = i >> 4, c = c0 + (i & 15);
     if (c >= m.n_in) continue;
     float v = 0.0f;
@@ -538,9 +641,9 @@ __global__ __launch_bounds__(M_WAVES* WAVE) void k_moe_down(Moe m, int tokens_ea
       if (ids[pair] == NO_EXPERT) continue;
       float s = sums[pair][i & 15];
       for (int q = 1; q < parts; ++q) s += sums[q * pairs + pair][i & 15];
-      v += m.weights[first + pair] * s;
+      v += weights[pair] * s;
     }
-    if (m.residual) v += value_at<DST>(m.residual, (int64_t)(t0 + t) * m.residual_stride + c);
+    if (m.residual) v += i == tid ? residual : value_at<DST>(m.residual, (int64_t)(t0 + t) * m.residual_stride + c);
     const int64_t at = (int64_t)(t0 + t) * m.y_stride + c;
     if (DST == QR_BF16) reinterpret_cast<uint16_t*>(m.y)[at] = bf16_bits(v);
     else reinterpret_cast<float*>(m.y)[at] = v;
@@ -608,17 +711,27 @@ int launch_moe(const Moe& m, hipStream_t s) {
   const int64_t pairs = (int64_t)m.n_tok * m.top_k;
   const int64_t met = pairs < m.n_experts ? pairs : m.n_experts;
   const dim3 grid((uint32_t)(met * m.blocks)), block(M_WAVES * WAVE);
-  const size_t lds = (size_t)pairs * 2 * sizeof(uint16_t);
   const int64_t each = (pairs + m.n_experts - 1) / m.n_experts;   // pairs of an expert on average
-  if (each <= 6) hipLaunchKernelGGL((k_moe_hidden<1>), grid, block, lds, s, m);
-  else if (each <= 16) hipLaunchKernelGGL((k_moe_hidden<2>), grid, block, lds, s, m);
-  else hipLaunchKernelGGL((k_moe_hidden<4>), grid, block, lds, s, m);
+  if (pairs <= 64) {
+    if (each <= 6) hipLaunchKernelGGL((k_moe_hidden<1, true>), grid, block, 0, s, m);
+    else hipLaunchKernelGGL((k_moe_hidden<4, true>), grid, block, 0, s, m);
+  } else {
+    const size_t lds = (size_t)pairs * 2 * sizeof(uint16_t);
+    if (each <= 6) hipLaunchKernelGGL((k_moe_hidden<1, false>), grid, block, lds, s, m);
+    else if (each <= 16) hipLaunchKernelGGL((k_moe_hidden<2, false>), grid, block, lds, s, m);
+    else hipLaunchKernelGGL((k_moe_hidden<4, false>), grid, block, lds, s, m);
+  }
   const int rc = qr_check_launch("k_moe_hidden");
   if (rc != QR_OK) return rc;
   const int tokens_each = D_SLOTS / m.top_k < 64 ? D_SLOTS / m.top_k : 64;
   const dim3 tiles((uint32_t)((m.n_in + 15) / 16) * (uint32_t)((m.n_tok + tokens_each - 1) / tokens_each));
-  if (each <= 6) hipLaunchKernelGGL((k_moe_down<DST, 1>), tiles, block, 0, s, m, tokens_each);
-  else hipLaunchKernelGGL((k_moe_down<DST, 2>), tiles, block, 0, s, m, tokens_each);
+  if (pairs <= 64) {
+    if (each <= 6) hipLaunchKernelGGL((k_moe_down<DST, 1, true>), tiles, block, 0, s, m, tokens_each);
+    else hipLaunchKernelGGL((k_moe_down<DST, 2, true>), tiles, block, 0, s, m, tokens_each);
+  } else {
+    if (each <= 6) hipLaunchKernelGGL((k_moe_down<DST, 1, false>), tiles, block, 0, s, m, tokens_each);
+    else hipLaunchKernelGGL((k_moe_down<DST, 2, false>), tiles, block, 0, s, m, tokens_each);
+  }
   return qr_check_launch("k_moe_down");
 }
 
