@@ -202,52 +202,65 @@ __device__ __forceinline__ void store_four(const Product& p, const Epilogue& ep,
 // 14 us, 3.3 TB/s; one token, 4096 x 4096: 5.4 us). From some 24 tokens on
 // every workgroup's reading of the tokens costs more, and tiles in LDS win.
 constexpr int F_WAVES = 8;
-constexpr int F_BATCH = 4;   // chunks of a wave whose loads are in flight together
+// Chunks of a wave whose loads are in flight together: with a gate, which has
+// twice the rows, two of them in 64 registers leave room for four workgroups on
+// a CU (one token, 11008 x 4096 gated: 19.1 us, four 21.9; without a gate, 4096
+// x 4096: two 6.3 us, four 5.5).
+template <int EPI>
+constexpr int few_batch() { return EPI == GATED ? 2 : 4; }
 
 template <int DST, int TT, int EPI>
 __global__ __launch_bounds__(F_WAVES* WAVE) void k_matmul_i8_few(Product p, Epilogue ep) {
   constexpr int G = EPI == GATED ? 2 : 1;   // weight rows per channel: gate and up
+  constexpr int F_BATCH = few_batch<EPI>();
   __shared__ i32x4 part[F_WAVES][G][TT][WAVE];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 15, lk = lane >> 4;
   const int out_tiles = (p.n_out + 15) / 16;
   const int o0 = (int)(blockIdx.x % out_tiles) * 16, t0 = (int)(blockIdx.x / out_tiles) * 16 * TT;
   // rows behind the last repeat it: their results are not stored
-  const int wr = o0 + li < p.n_out ? o0 + li : p.n_out - 1;
-  const int8_t* w[G];
+  const int w_last = p.n_out - o0 < 16 ? p.n_out - 1 - o0 : 15, x_last = p.n_tok - t0 < 16 * TT ? p.n_tok - 1 - t0 : 16 * TT - 1;
+  const uint32_t rb = (uint32_t)p.row_bytes;
+  Buffer w[G];
 #pragma unroll
-  for (int g = 0; g < G; ++g) w[g] = (g ? ep.up : p.w) + (int64_t)wr * p.row_bytes + 16 * lk;
-  const int8_t* x[TT];
+  for (int g = 0; g < G; ++g) w[g] = buffer_of((g ? ep.up : p.w) + (int64_t)o0 * p.row_bytes, (uint32_t)(w_last + 1) * rb);
+  const Buffer xs = buffer_of(p.x + (int64_t)t0 * p.row_bytes, (uint32_t)(x_last + 1) * rb);
+  uint32_t at[2], x[TT];
 #pragma unroll
-  for (int j = 0; j < TT; ++j) {
-    const int xr = t0 + 16 * j + li < p.n_tok ? t0 + 16 * j + li : p.n_tok - 1;
-    x[j] = p.x + (int64_t)xr * p.row_bytes + 16 * lk;
+  for (int h = 0; h < 2; ++h) {
+    const int r = 8 * h + (li & 7);
+    at[h] = (uint32_t)(r < w_last ? r : w_last) * rb + 64 * (li >> 3) + 16 * lk;
   }
+#pragma unroll
+  for (int j = 0; j < TT; ++j) x[j] = 16 * j + li <= x_last ? (uint32_t)(16 * j + li) * rb + 16 * lk : NOWHERE;
   const int chunks = p.row_bytes / 128;
   i32x4 acc[G][TT] = {};
   for (int c0 = wave; c0 < chunks; c0 += F_WAVES * F_BATCH) {
-    i32x4 a[F_BATCH][2][G], b[F_BATCH][2][TT];
+    i32x4 a[F_BATCH][G][2], b[F_BATCH][2][TT];
 #pragma unroll
     for (int u = 0; u < F_BATCH; ++u) {
-      const int c = c0 + u * F_WAVES < chunks ? c0 + u * F_WAVES : c0;
+      const int c = (c0 + u * F_WAVES < chunks ? c0 + u * F_WAVES : c0) * 128;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        // (two workgroups of 32 tokens may read the same weights)
 #pragma unroll
-        for (int g = 0; g < G; ++g) a[u][h][g] = *reinterpret_cast<const i32x4*>(w[g] + c * 128 + 64 * h);
+        for (int g = 0; g < G; ++g) a[u][g][h] = TT == 2 ? load16(w[g], at[h], c) : load16_once(w[g], at[h], c);
 #pragma unroll
-        for (int j = 0; j < TT; ++j) b[u][h][j] = *reinterpret_cast<const i32x4*>(x[j] + c * 128 + 64 * h);
+        for (int j = 0; j < TT; ++j) b[u][h][j] = load16(xs, x[j], c + 64 * h);
       }
     }
 #pragma unroll
     for (int u = 0; u < F_BATCH; ++u) {
       if (c0 + u * F_WAVES < chunks) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int g = 0; g < G; ++g) {
+          turn(a[u][g][0], a[u][g][1]);
 #pragma unroll
-          for (int j = 0; j < TT; ++j)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int g = 0; g < G; ++g)
-              acc[g][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u][h][g], b[u][h][j], acc[g][j], 0, 0, 0);
+            for (int j = 0; j < TT; ++j)
+              acc[g][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u][g][h], b[u][h][j], acc[g][j], 0, 0, 0);
+        }
       }
     }
   }

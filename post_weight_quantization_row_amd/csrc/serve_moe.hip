@@ -34,7 +34,25 @@ struct Route {
 };
 
 constexpr int R_CHUNK = 32;      // values of the sum that a wave takes at a time
-constexpr int R_WAVES = 4;
+constexpr int R_WAVES = 8;
+constexpr int R_SPLITS = 8;      // at most
+
+// Eight neighbouring values as they lie in memory.
+template <int SRC>
+struct Eight {
+  u16x8_any v;
+  __device__ __forceinline__ double get(int i) const { return (double)bf16_value(v[i]); }
+};
+template <>
+struct Eight<QR_F32> {
+  f32x4_any v[2];
+  __device__ __forceinline__ double get(int i) const { return (double)v[i >> 2][i & 3]; }
+};
+
+template <int SRC>
+__device__ __forceinline__ Eight<SRC> eight_at(const uint8_t* row, int at) {
+  return *reinterpret_cast<const Eight<SRC>*>(row + (int64_t)at * (SRC == QR_BF16 ? 2 : 4));
+}
 
 // Logits: 16 TE experts x 16 TT tokens per workgroup, the sum split over its
 // waves (and, with few tiles, over workgroups) in chunks of 32 values. Products
@@ -44,7 +62,7 @@ constexpr int R_WAVES = 4;
 template <int SRC, int WSRC, int TE, int TT>
 __global__ __launch_bounds__(R_WAVES* WAVE) void k_route_logits(Route p, int expert_tiles, int token_tiles) {
   __shared__ f64x4 part[R_WAVES][TE][TT][WAVE];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 15, lk = lane >> 4;
   int block = (int)blockIdx.x;
   const int be = block % expert_tiles;
@@ -62,13 +80,34 @@ __global__ __launch_bounds__(R_WAVES* WAVE) void k_route_logits(Route p, int exp
     wr[i] = reinterpret_cast<const uint8_t*>(p.w) + (int64_t)(e < p.n_experts ? e : p.n_experts - 1) * p.n_in * (WSRC == QR_BF16 ? 2 : 4);
   }
   f64x4 acc[TE][TT] = {};
-  const int step = R_WAVES * p.splits * R_CHUNK;
-  for (int k = (split * R_WAVES + wave) * R_CHUNK; k < p.n_in; k += step) {
+  struct Stage {
+    Eight<WSRC> a[TE];
+    Eight<SRC> b[TT];
+  };
+  // whole chunks first, then what is left of the row, for the wave whose turn it is
+  const int chunks = p.n_in / R_CHUNK, step = R_WAVES * p.splits, from = split * R_WAVES + wave;
+  pipeline<TE * TT == 1 ? 4 : 2, Stage>(from, chunks, step,
+      [&](Stage& s, int k) {
+#pragma unroll
+        for (int i = 0; i < TE; ++i) s.a[i] = eight_at<WSRC>(wr[i], k * R_CHUNK + 8 * lk);
+#pragma unroll
+        for (int j = 0; j < TT; ++j) s.b[j] = eight_at<SRC>(xr[j], k * R_CHUNK + 8 * lk);
+      },
+      [&](Stage& s, int) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+#pragma unroll
+          for (int i = 0; i < TE; ++i)
+#pragma unroll
+            for (int j = 0; j < TT; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f64_16x16x4f64(s.a[i].get(u), s.b[j].get(u), acc[i][j], 0, 0, 0);
+      });
+  if (p.n_in % R_CHUNK != 0 && chunks % step == from) {
     float a[TE][8], b[TT][8];
 #pragma unroll
-    for (int i = 0; i < TE; ++i) load8<WSRC>(wr[i], k + 8 * lk, p.n_in, a[i]);
+    for (int i = 0; i < TE; ++i) load8<WSRC>(wr[i], chunks * R_CHUNK + 8 * lk, p.n_in, a[i]);
 #pragma unroll
-    for (int j = 0; j < TT; ++j) load8<SRC>(xr[j], k + 8 * lk, p.n_in, b[j]);
+    for (int j = 0; j < TT; ++j) load8<SRC>(xr[j], chunks * R_CHUNK + 8 * lk, p.n_in, b[j]);
 #pragma unroll
     for (int u = 0; u < 8; ++u)
 #pragma unroll
@@ -106,6 +145,48 @@ __device__ __forceinline__ uint64_t order_key(double v) {
   return u >> 63 ? ~u : u | 1ull << 63;
 }
 
+__device__ __forceinline__ double of_key(uint64_t k) {
+  return __builtin_bit_cast(double, k >> 63 ? k & ~(1ull << 63) : ~k);   // (a NaN's key gives a NaN)
+}
+
+// `v` of the lane that the DPP control names, zero where there is none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t moved(uint64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xf, false);
+  return (uint64_t)hi << 32 | lo;
+}
+
+__device__ __forceinline__ uint64_t last_lane(uint64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, 63);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), 63);
+  return (uint64_t)hi << 32 | lo;
+}
+
+// The largest key and the sum of a wave, without LDS: rows of 16 lanes by
+// shifts of 1, 2, 4 and 8, then the rows' last lanes passed on.
+__device__ __forceinline__ uint64_t wave_largest(uint64_t v) {
+  const auto take = [&](uint64_t o) { v = o > v ? o : v; };
+  take(moved<0x111, 0xf>(v));
+  take(moved<0x112, 0xf>(v));
+  take(moved<0x114, 0xf>(v));
+  take(moved<0x118, 0xf>(v));
+  take(moved<0x142, 0xa>(v));
+  take(moved<0x143, 0xc>(v));
+  return last_lane(v);
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+  const auto add = [&](uint64_t o) { v += __builtin_bit_cast(double, o); };
+  add(moved<0x111, 0xf>(__builtin_bit_cast(uint64_t, v)));
+  add(moved<0x112, 0xf>(__builtin_bit_cast(uint64_t, v)));
+  add(moved<0x114, 0xf>(__builtin_bit_cast(uint64_t, v)));
+  add(moved<0x118, 0xf>(__builtin_bit_cast(uint64_t, v)));
+  add(moved<0x142, 0xa>(__builtin_bit_cast(uint64_t, v)));
+  add(moved<0x143, 0xc>(__builtin_bit_cast(uint64_t, v)));
+  return __builtin_bit_cast(double, last_lane(__builtin_bit_cast(uint64_t, v)));
+}
+
 // One wave per token, expert lane + 64 j in its slot j.
 template <int J>
 __global__ __launch_bounds__(256) void k_route_choose(Route p) {
@@ -113,81 +194,71 @@ __global__ __launch_bounds__(256) void k_route_choose(Route p) {
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= p.n_tok) return;
   double v[J];
+  float bias[J];
   uint64_t key[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const int e = lane + 64 * j;
-    v[j] = 0.0;
-    if (e < p.n_experts)
-      for (int s = 0; s < p.splits; ++s) v[j] += p.logits[((int64_t)s * p.n_tok + t) * p.n_experts + e];
+    const int e = lane + 64 * j, at = e < p.n_experts ? e : p.n_experts - 1;
+    bias[j] = p.bias ? p.bias[at] : 0.0f;
+    double part[R_SPLITS];
+#pragma unroll
+    for (int s = 0; s < R_SPLITS; ++s) part[s] = s < p.splits ? p.logits[((int64_t)s * p.n_tok + t) * p.n_experts + at] : 0.0;
+    v[j] = part[0];
+#pragma unroll
+    for (int s = 1; s < R_SPLITS; ++s) v[j] += part[s];
   }
   if (p.score == QR_SCORE_SIGMOID) {
 #pragma unroll
     for (int j = 0; j < J; ++j) v[j] = 1.0 / (1.0 + exp(-v[j]));
   } else {
-    double top = -__builtin_inf();
+    uint64_t top = 0;
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-      if (lane + 64 * j < p.n_experts) top = v[j] > top ? v[j] : top;
-#pragma unroll
-    for (int s = 32; s > 0; s >>= 1) {
-      const double o = __shfl_xor(top, s);
-      top = o > top ? o : top;
+    for (int j = 0; j < J; ++j) {
+      const uint64_t k = order_key(v[j]);
+      if (lane + 64 * j < p.n_experts && k > top) top = k;
     }
+    const double most = of_key(wave_largest(top));
     double sum = 0.0;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      v[j] = exp(v[j] - top);
+      v[j] = exp(v[j] - most);
       if (lane + 64 * j < p.n_experts) sum += v[j];
     }
-#pragma unroll
-    for (int s = 32; s > 0; s >>= 1) sum += __shfl_xor(sum, s);
+    sum = wave_sum(sum);
 #pragma unroll
     for (int j = 0; j < J; ++j) v[j] /= sum;
   }
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int e = lane + 64 * j;
-    const float b = p.bias && e < p.n_experts ? p.bias[e] : 0.0f;
-    key[j] = e < p.n_experts && b != -__builtin_inff() ? order_key(v[j] + (double)b) : 0;
-  }
+  for (int j = 0; j < J; ++j)
+    key[j] = lane + 64 * j < p.n_experts && bias[j] != -__builtin_inff() ? order_key(v[j] + (double)bias[j]) : 0;
   // lane r keeps what the r-th round chose
   int chosen = -1;
   double score = 0.0;
   for (int r = 0; r < p.top_k; ++r) {
     uint64_t best = 0;
-    int at = 0;
-    double mine = 0.0;
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-      if (key[j] > best) {
-        best = key[j];
-        at = lane + 64 * j;
-        mine = v[j];
-      }
-#pragma unroll
-    for (int s = 32; s > 0; s >>= 1) {
-      const uint64_t o = (uint64_t)__shfl_xor((unsigned long long)best, s);
-      const int oa = __shfl_xor(at, s);
-      if (o > best || (o == best && oa < at)) {
-        best = o;
-        at = oa;
-      }
-    }
+    for (int j = 0; j < J; ++j) best = key[j] > best ? key[j] : best;
+    best = wave_largest(best);
     if (best == 0) break;
-    const double won = __shfl(mine, at & 63);
+    // among equals the lowest: the first slot that has one, its first lane
+    int at = -1;
+    double won = 0.0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const uint64_t have = __ballot(key[j] == best);
+      if (at >= 0 || have == 0) continue;
+      const int from = __builtin_ctzll(have);
+      at = 64 * j + from;
+      won = __shfl(v[j], from);
+      if (lane == from) key[j] = 0;
+    }
     if (lane == r) {
       chosen = at;
       score = won;
     }
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-      if (lane + 64 * j == at) key[j] = 0;
   }
   if (p.renorm) {
-    double sum = score;
-#pragma unroll
-    for (int s = 32; s > 0; s >>= 1) sum += __shfl_xor(sum, s);
+    const double sum = wave_sum(score);
     score = sum == 0.0 ? 0.0 : score / sum;
   }
   if (lane < p.top_k) {
@@ -659,7 +730,7 @@ struct RoutePlan {
 };
 
 // Tiles of 32 x 32 where they fill the chip, else of 16 x 16 with the sum split
-// until there are some 512 workgroups.
+// until there are some 256 workgroups.
 RoutePlan route_plan(int64_t n_experts, int64_t n_tok, int64_t n_in) {
   RoutePlan r;
   r.wide = ((n_experts + 31) / 32) * ((n_tok + 31) / 32) >= 256;
@@ -667,8 +738,8 @@ RoutePlan route_plan(int64_t n_experts, int64_t n_tok, int64_t n_in) {
   r.expert_tiles = (int)((n_experts + tile - 1) / tile);
   r.token_tiles = (int)((n_tok + tile - 1) / tile);
   const int64_t most = (n_in + R_CHUNK * R_WAVES - 1) / (R_CHUNK * R_WAVES);
-  int64_t s = 512 / ((int64_t)r.expert_tiles * r.token_tiles);
-  s = s > 16 ? 16 : s;
+  int64_t s = 256 / ((int64_t)r.expert_tiles * r.token_tiles);
+  s = s > R_SPLITS ? R_SPLITS : s;
   s = s > most ? most : s;
   r.splits = (int)(s < 1 ? 1 : s);
   return r;
