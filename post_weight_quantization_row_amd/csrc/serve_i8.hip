@@ -150,35 +150,71 @@ __device__ __forceinline__ float load_one(const void* x, int64_t at) {
   return SRC == QR_BF16 ? bf16_value(reinterpret_cast<const uint16_t*>(x)[at]) : reinterpret_cast<const float*>(x)[at];
 }
 
-// One output before its rounding to the output's type, without the residual.
+// Scales and biases of four neighbouring channels; the last one's behind it.
 template <int EPI>
-__device__ __forceinline__ float output(const Product& p, const Epilogue& ep, int o, int sum, int up, const TokenScale& xd) {
-  float v = scaled(sum, xd, p.wd[o], p.bias ? p.bias[o] : 0.0f);
-  if (EPI != PLAIN) v = activation(ep.act, v);
-  if (EPI == GATED) v *= scaled(up, xd, ep.upd[o], ep.up_bias ? ep.up_bias[o] : 0.0f);
-  return v;
-}
+struct Channels {
+  float wd[4], bias[4], upd[4], up_bias[4];
+
+  __device__ __forceinline__ Channels(const Product& p, const Epilogue& ep, int o) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int c = o + e < p.n_out ? o + e : p.n_out - 1;
+      wd[e] = p.wd[c];
+      bias[e] = p.bias ? p.bias[c] : 0.0f;
+      upd[e] = EPI == GATED ? ep.upd[c] : 0.0f;
+      up_bias[e] = EPI == GATED && ep.up_bias ? ep.up_bias[c] : 0.0f;
+    }
+  }
+};
 
 // Stores four neighbouring channels of one token; up: the gate's second sums.
 template <int DST, int EPI>
-__device__ __forceinline__ void store_four(const Product& p, const Epilogue& ep, int tok, int o, const i32x4& sum,
-                                           const i32x4& up, const TokenScale& xd) {
+__device__ __forceinline__ void store_four(const Product& p, const Epilogue& ep, const Channels<EPI>& c, int tok, int o,
+                                           const i32x4& sum, const i32x4& up, const TokenScale& xd) {
   const int64_t at = (int64_t)tok * p.y_stride + o, from = (int64_t)tok * ep.residual_stride + o;
+  const bool whole = o + 4 <= p.n_out;
+  float v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[e] = scaled(sum[e], xd, c.wd[e], c.bias[e]);
+    if (EPI != PLAIN) v[e] = activation(ep.act, v[e]);
+    if (EPI == GATED) v[e] *= scaled(up[e], xd, c.upd[e], c.up_bias[e]);
+  }
+  if (EPI != PLAIN && ep.residual) {
+    if (whole && DST == QR_BF16) {
+      const u16x4_any r = *reinterpret_cast<const u16x4_any*>(reinterpret_cast<const uint16_t*>(ep.residual) + from);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += bf16_value(r[e]);
+    } else if (whole) {
+      const f32x4_any r = *reinterpret_cast<const f32x4_any*>(reinterpret_cast<const float*>(ep.residual) + from);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += r[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (o + e < p.n_out) v[e] += load_one<DST>(ep.residual, from + e);
+    }
+  }
+  if (whole && DST == QR_BF16) {
+    *reinterpret_cast<u16x4_any*>(reinterpret_cast<uint16_t*>(p.y) + at) =
+        u16x4_any{bf16_bits(v[0]), bf16_bits(v[1]), bf16_bits(v[2]), bf16_bits(v[3])};
+  } else if (whole) {
+    *reinterpret_cast<f32x4_any*>(reinterpret_cast<float*>(p.y) + at) = f32x4_any{v[0], v[1], v[2], v[3]};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (o + e < p.n_out) store_one<DST>(p.y, at + e, v[e]);
+  }
+}
+
+// The same without an epilogue, where the scales are loaded as they are needed.
+template <int DST>
+__device__ __forceinline__ void store_plain(const Product& p, int tok, int o, const i32x4& sum, const TokenScale& xd) {
+  const int64_t at = (int64_t)tok * p.y_stride + o;
   if (o + 4 <= p.n_out) {
     float v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = output<EPI>(p, ep, o + e, sum[e], up[e], xd);
-    if (EPI != PLAIN && ep.residual) {
-      if (DST == QR_BF16) {
-        const u16x4_any r = *reinterpret_cast<const u16x4_any*>(reinterpret_cast<const uint16_t*>(ep.residual) + from);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += bf16_value(r[e]);
-      } else {
-        const f32x4_any r = *reinterpret_cast<const f32x4_any*>(reinterpret_cast<const float*>(ep.residual) + from);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += r[e];
-      }
-    }
+    for (int e = 0; e < 4; ++e) v[e] = scaled(sum[e], xd, p.wd[o + e], p.bias ? p.bias[o + e] : 0.0f);
     if (DST == QR_BF16)
       *reinterpret_cast<u16x4_any*>(reinterpret_cast<uint16_t*>(p.y) + at) =
           u16x4_any{bf16_bits(v[0]), bf16_bits(v[1]), bf16_bits(v[2]), bf16_bits(v[3])};
@@ -186,12 +222,8 @@ __device__ __forceinline__ void store_four(const Product& p, const Epilogue& ep,
       *reinterpret_cast<f32x4_any*>(reinterpret_cast<float*>(p.y) + at) = f32x4_any{v[0], v[1], v[2], v[3]};
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (o + e >= p.n_out) continue;
-      float v = output<EPI>(p, ep, o + e, sum[e], up[e], xd);
-      if (EPI != PLAIN && ep.residual) v += load_one<DST>(ep.residual, from + e);
-      store_one<DST>(p.y, at + e, v);
-    }
+    for (int e = 0; e < 4; ++e)
+      if (o + e < p.n_out) store_one<DST>(p.y, at + e, scaled(sum[e], xd, p.wd[o + e], p.bias ? p.bias[o + e] : 0.0f));
   }
 }
 
@@ -278,7 +310,9 @@ __global__ __launch_bounds__(F_WAVES* WAVE) void k_matmul_i8_few(Product p, Epil
       for (int v = 1; v < F_WAVES; ++v) sum[g] += part[v][g][wave][lane];
     }
     const int tok = t0 + 16 * wave + li;
-    if (tok < p.n_tok) store_four<DST, EPI>(p, ep, tok, o0 + 4 * lk, sum[0], sum[G - 1], token_scale(p.xd[tok]));
+    if (tok >= p.n_tok) return;
+    if constexpr (EPI == PLAIN) store_plain<DST>(p, tok, o0 + 4 * lk, sum[0], token_scale(p.xd[tok]));
+    else store_four<DST, EPI>(p, ep, Channels<EPI>(p, ep, o0 + 4 * lk), tok, o0 + 4 * lk, sum[0], sum[G - 1], token_scale(p.xd[tok]));
   }
 }
 
@@ -435,19 +469,23 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(NI * N
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
           const i32x4 sum = {acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]};
-          store_four<DST, EPI>(p, ep, tok, o0 + wo + 32 * i + 2 * e + 4 * lh, sum, sum, xd);
+          store_plain<DST>(p, tok, o0 + wo + 32 * i + 2 * e + 4 * lh, sum, xd);
         }
     }
   } else {
     // 32 tokens at a time through the wave's own part of LDS: the epilogue is
-    // then one short loop over neighbouring channels (unrolled over the
-    // accumulators it was too long for the compiler to keep them in registers)
-    constexpr int W = 32 * NI, PITCH = W + 4, FOURS = W / (EPI == GATED ? 8 : 4);
+    // then one short loop (unrolled over the accumulators it was too long for the
+    // compiler to keep them in registers), and a lane keeps its four channels
+    constexpr int W = 32 * NI, PITCH = W + 4, FOURS = W / (EPI == GATED ? 8 : 4), TOKENS = 64 / FOURS;
     static_assert(4 * 32 * PITCH * 4 <= (int)sizeof(all_lds), "the waves' sums fit");
     int* sums = reinterpret_cast<int*>(all_lds) + wave * (32 * PITCH);
+    const int four = lane % FOURS, piece = four * 4 / PIECE, o = o0 + (wo / 32 + piece) * PIECE + four * 4 % PIECE;
+    const Channels<EPI> channels(p, ep, o < p.n_out ? o : p.n_out - 1);
+    const int* from = sums + (lane / FOURS) * PITCH + 32 * piece + four * 4 % PIECE;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      if (t0 + wt + 32 * j >= p.n_tok) break;
+      const int first = t0 + wt + 32 * j;
+      if (first >= p.n_tok) break;
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -455,14 +493,12 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(NI * N
           *reinterpret_cast<i32x4*>(sums + li * PITCH + 32 * i + 2 * e + 4 * lh) =
               i32x4{acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]};
       wave_sync();
-#pragma unroll 1
-      for (int at = lane; at < 32 * FOURS; at += 64) {
-        const int t = at / FOURS, four = at % FOURS, tok = t0 + wt + 32 * j + t;
-        const int piece = four * 4 / PIECE, o = o0 + (wo / 32 + piece) * PIECE + four * 4 % PIECE;
-        if (tok >= p.n_tok || o >= p.n_out) continue;
-        const int* from = sums + t * PITCH + 32 * piece + four * 4 % PIECE;
-        store_four<DST, EPI>(p, ep, tok, o, *reinterpret_cast<const i32x4*>(from),
-                             *reinterpret_cast<const i32x4*>(from + (EPI == GATED ? 16 : 0)), token_scale(p.xd[tok]));
+#pragma unroll 2
+      for (int t = 0; t < 32; t += TOKENS) {
+        const int tok = first + t + lane / FOURS;
+        if (tok < p.n_tok && o < p.n_out)
+          store_four<DST, EPI>(p, ep, channels, tok, o, *reinterpret_cast<const i32x4*>(from + t * PITCH),
+                               *reinterpret_cast<const i32x4*>(from + t * PITCH + (EPI == GATED ? 16 : 0)), token_scale(p.xd[tok]));
       }
       wave_sync();
     }

@@ -126,15 +126,18 @@ __device__ __forceinline__ void load8(const void* row, int at, int n, float (&v)
   }
 }
 
-// Eight values rounded to codes, in eight bytes.
+// Eight values rounded to codes, in eight bytes. A sum with 1.5 * 2^23 is
+// rounded to a whole number, to even like rint, and has it in its low bits.
 __device__ __forceinline__ u32x2 pack_codes(const float (&v)[8], float inv) {
   u32x2 o;
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    uint32_t u = 0;
+    uint32_t u[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u |= ((uint32_t)(int)__builtin_rintf(v[4 * w + i] * inv) & 0xffu) << (8 * i);
-    o[w] = u;
+    for (int i = 0; i < 4; ++i) u[i] = __builtin_bit_cast(uint32_t, v[4 * w + i] * inv + 0x1.8p23f);
+    // bytes 0 of two words each side by side, then the two halves
+    const uint32_t lo = __builtin_amdgcn_perm(u[1], u[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(u[3], u[2], 0x04000c0cu);
+    o[w] = lo | hi;
   }
   return o;
 }
