@@ -1,6 +1,8 @@
 """Compiles libqrow.so (the HIP kernels and the C-ABI) for gfx950 in-tree."""
 import os
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,7 +22,7 @@ PROBE_SOURCES = [os.path.join(HERE, "csrc", "valu_rates.hip")]
 PROBE_LIB = os.path.join(HERE, "libqrow_probe.so")
 
 HIPCC_FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     # every float operation as written: no contraction, no fast-math,
     # correctly rounded fp32 division and square root
     "-ffp-contract=off", "-fno-fast-math",
@@ -30,10 +32,7 @@ HIPCC_FLAGS = [
 ]
 
 
-def _hipcc(sources, lib, verbose):
-    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-    tmp = lib + ".tmp"
-    cmd = [hipcc, *HIPCC_FLAGS, "-I", INCLUDE, "-o", tmp, *sources]
+def _run(cmd, verbose):
     r = subprocess.run(cmd, capture_output=True, text=True)
     # the host pass does not know the packed-fp32 feature and says so
     noise = "is not a recognized feature for this target"
@@ -42,6 +41,18 @@ def _hipcc(sources, lib, verbose):
         raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
     if verbose and msgs:
         print("\n".join(msgs))
+
+
+def _hipcc(sources, lib, verbose):
+    """Every source by itself, side by side, then one link."""
+    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+    tmp = lib + ".tmp"
+    with tempfile.TemporaryDirectory() as d, ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+        objects = [os.path.join(d, os.path.basename(s) + ".o") for s in sources]
+        for done in [pool.submit(_run, [hipcc, *HIPCC_FLAGS, "-c", "-I", INCLUDE, "-o", o, s], verbose)
+                     for s, o in zip(sources, objects)]:
+            done.result()
+        _run([hipcc, *HIPCC_FLAGS, "-shared", "-o", tmp, *objects], verbose)
     os.replace(tmp, lib)
     return lib
 
