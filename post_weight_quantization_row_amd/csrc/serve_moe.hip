@@ -377,13 +377,15 @@ __device__ __forceinline__ int pair_of(const Met& r, int at) {
   return found;
 }
 
+constexpr int HIDDEN_TILES = 4;        // of 16 pairs, whose products share the weights they are made with
+
 // Gate and up products of one block of 64 hidden channels for 16 TT pairs of
 // one expert, and their 8-bit hidden values. Waves 0-3 have 16 channels each and
 // the first half of the sum, waves 4-7 the second; a wave holds one batch of
 // loads while the next is on its way.
-template <int TT, int MOST, bool FEW>
+template <int TT, bool FEW>
 __device__ __forceinline__ void hidden_block(const Moe& m, const Met& met, int first, int block,
-                                             i32x4 (*part)[4][2][MOST][WAVE]) {
+                                             i32x4 (*part)[4][2][HIDDEN_TILES][WAVE]) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 15, lk = lane >> 4, group = wave & 3, half = wave >> 2;
   const int c0 = M_BLOCK * block + 16 * group;
@@ -458,8 +460,8 @@ __device__ __forceinline__ void hidden_block(const Moe& m, const Met& met, int f
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       // sum of channel 16 g' + 4 lk + i of column li: element i of lane 16 lk + li
-      const int of = (((c >> 4) * 2 * MOST + (q >> 4)) * WAVE + ((c >> 2) & 3) * 16 + (q & 15)) * 4 + (c & 3) + e;
-      constexpr int UP = MOST * WAVE * 4, HALF = 4 * 2 * MOST * WAVE * 4;
+      const int of = (((c >> 4) * 2 * HIDDEN_TILES + (q >> 4)) * WAVE + ((c >> 2) & 3) * 16 + (q & 15)) * 4 + (c & 3) + e;
+      constexpr int UP = HIDDEN_TILES * WAVE * 4, HALF = 4 * 2 * HIDDEN_TILES * WAVE * 4;
       // in 64 bits, so that the codes that are made of it do not hang on the
       // last place of an exp
       const double g = (double)scaled(sums[of] + sums[of + HALF], d, gd[e], 0.0f);
@@ -485,12 +487,12 @@ __device__ __forceinline__ void hidden_block(const Moe& m, const Met& met, int f
 // One workgroup per expert that is met and block of hidden channels: it finds
 // its expert and the expert's pairs in the choices by itself (a captured call
 // replays with other choices). FEW: all pairs fit into a wave's lanes.
-template <int MOST, bool FEW>
-__global__ __launch_bounds__(M_WAVES* WAVE) __attribute__((amdgpu_waves_per_eu(2))) void k_moe_hidden(Moe m) {
+template <bool FEW>
+__global__ __launch_bounds__(M_WAVES* WAVE) void k_moe_hidden(Moe m) {
   extern __shared__ uint16_t dynamic[];
   __shared__ uint32_t mask[MASK_WORDS];
   __shared__ int counts[M_WAVES];
-  __shared__ i32x4 part[2][4][2][MOST][WAVE];
+  __shared__ i32x4 part[2][4][2][HIDDEN_TILES][WAVE];
   const int pairs = m.n_tok * m.top_k;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int block = (int)(blockIdx.x % (uint32_t)m.blocks), rank = (int)(blockIdx.x / (uint32_t)m.blocks);
@@ -528,14 +530,14 @@ __global__ __launch_bounds__(M_WAVES* WAVE) __attribute__((amdgpu_waves_per_eu(2
   }
   for (int at = 0; at < met.n;) {
     const int left = met.n - at;
-    if (MOST == 1 || left <= 16) {
-      hidden_block<1, MOST, FEW>(m, met, at, block, part);
+    if (left <= 16) {
+      hidden_block<1, FEW>(m, met, at, block, part);
       at += 16;
-    } else if (MOST == 2 || left <= 32) {
-      hidden_block<2, MOST, FEW>(m, met, at, block, part);
+    } else if (left <= 32) {
+      hidden_block<2, FEW>(m, met, at, block, part);
       at += 32;
     } else {
-      if constexpr (MOST == 4) hidden_block<4, MOST, FEW>(m, met, at, block, part);
+      hidden_block<4, FEW>(m, met, at, block, part);
       at += 64;
     }
   }
@@ -783,25 +785,24 @@ int launch_moe(const Moe& m, hipStream_t s) {
   const int64_t met = pairs < m.n_experts ? pairs : m.n_experts;
   const dim3 grid((uint32_t)(met * m.blocks)), block(M_WAVES * WAVE);
   const int64_t each = (pairs + m.n_experts - 1) / m.n_experts;   // pairs of an expert on average
-  if (pairs <= 64) {
-    if (each <= 6) hipLaunchKernelGGL((k_moe_hidden<1, true>), grid, block, 0, s, m);
-    else hipLaunchKernelGGL((k_moe_hidden<4, true>), grid, block, 0, s, m);
-  } else {
-    const size_t lds = (size_t)pairs * 2 * sizeof(uint16_t);
-    if (each <= 6) hipLaunchKernelGGL((k_moe_hidden<1, false>), grid, block, lds, s, m);
-    else if (each <= 16) hipLaunchKernelGGL((k_moe_hidden<2, false>), grid, block, lds, s, m);
-    else hipLaunchKernelGGL((k_moe_hidden<4, false>), grid, block, lds, s, m);
-  }
+  const bool few = pairs <= 64;
+  if (few) hipLaunchKernelGGL((k_moe_hidden<true>), grid, block, 0, s, m);
+  else hipLaunchKernelGGL((k_moe_hidden<false>), grid, block, (size_t)pairs * 2 * sizeof(uint16_t), s, m);
   const int rc = qr_check_launch("k_moe_hidden");
   if (rc != QR_OK) return rc;
-  const int tokens_each = D_SLOTS / m.top_k < 64 ? D_SLOTS / m.top_k : 64;
+  const int tokens_each = D_SLOTS / m.top_k;
   const dim3 tiles((uint32_t)((m.n_in + 15) / 16) * (uint32_t)((m.n_tok + tokens_each - 1) / tokens_each));
-  if (pairs <= 64) {
-    if (each <= 6) hipLaunchKernelGGL((k_moe_down<DST, 1, true>), tiles, block, 0, s, m, tokens_each);
-    else hipLaunchKernelGGL((k_moe_down<DST, 2, true>), tiles, block, 0, s, m, tokens_each);
+  // 32 pairs at a time where experts have that many and their sums are long:
+  // half as many workgroups fit on a CU then. Measured, us a layer, 16 first:
+  // 8 experts of 11008, 8 pairs each 217 / 220, 16 290 / 279, 20 339 / 300, 32
+  // 437 / 420; 64 experts of 1408, 12 each 203 / 202, 24 309 / 322, 48 446 / 492
+  const bool wide = each > 12 && m.n_mid >= 4096;
+  if (few) {
+    if (wide) hipLaunchKernelGGL((k_moe_down<DST, 2, true>), tiles, block, 0, s, m, tokens_each);
+    else hipLaunchKernelGGL((k_moe_down<DST, 1, true>), tiles, block, 0, s, m, tokens_each);
   } else {
-    if (each <= 6) hipLaunchKernelGGL((k_moe_down<DST, 1, false>), tiles, block, 0, s, m, tokens_each);
-    else hipLaunchKernelGGL((k_moe_down<DST, 2, false>), tiles, block, 0, s, m, tokens_each);
+    if (wide) hipLaunchKernelGGL((k_moe_down<DST, 2, false>), tiles, block, 0, s, m, tokens_each);
+    else hipLaunchKernelGGL((k_moe_down<DST, 1, false>), tiles, block, 0, s, m, tokens_each);
   }
   return qr_check_launch("k_moe_down");
 }
