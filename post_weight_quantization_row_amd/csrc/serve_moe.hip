@@ -5,6 +5,8 @@
 
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "qr_internal.h"
 #include "qrow.h"
 #include "serve/qrow_moe.h"
@@ -632,6 +634,63 @@ __device__ __forceinline__ float value_at(const void* x, int64_t i) {
   return DST == QR_BF16 ? bf16_value(reinterpret_cast<const uint16_t*>(x)[i]) : reinterpret_cast<const float*>(x)[i];
 }
 
+// Up to 512 pairs sorted by expert, in LDS: a thread has a pair, counters of all
+// experts give it a place among its expert's (which one does not matter to any
+// result) and their running sums the expert's place among those that are met.
+struct Sorted {
+  uint32_t count[QR_MOE_MAX_EXPERTS];          // pairs, later where an expert's begin
+  uint32_t waves[M_WAVES];
+  uint16_t experts[D_SLOTS], begin[D_SLOTS + 1], pairs[D_SLOTS];
+};
+
+__device__ __forceinline__ int sort_pairs(const Moe& m, int first, int n, Sorted& s, uint16_t* ids) {
+  constexpr int EACH = QR_MOE_MAX_EXPERTS / (M_WAVES * WAVE);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int id = tid < n ? m.ids[first + tid] : -1;
+  const bool is = (uint32_t)id < (uint32_t)m.n_experts;
+  if (tid < n) ids[tid] = (uint16_t)(is ? id : NO_EXPERT);
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) s.count[EACH * tid + i] = 0;
+  __syncthreads();
+  uint32_t place = 0;
+  if (is) place = atomicAdd(&s.count[id], 1u);
+  __syncthreads();
+  // running sums of pairs (low half) and of experts that have any (high half)
+  uint32_t mine[EACH], sum = 0;
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    mine[i] = s.count[EACH * tid + i];
+    sum += mine[i] ? mine[i] + 0x10000u : 0u;
+  }
+  uint32_t up = sum;
+#pragma unroll
+  for (int d = 1; d < WAVE; d <<= 1) {
+    const uint32_t o = (uint32_t)__shfl_up((int)up, d);
+    if (lane >= d) up += o;
+  }
+  if (lane == 63) s.waves[wave] = up;
+  __syncthreads();
+  uint32_t before = up - sum, all = 0;
+#pragma unroll
+  for (int w = 0; w < M_WAVES; ++w) {
+    if (w < wave) before += s.waves[w];
+    all += s.waves[w];
+  }
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    if (!mine[i]) continue;
+    s.experts[before >> 16] = (uint16_t)(EACH * tid + i);
+    s.begin[before >> 16] = (uint16_t)before;
+    s.count[EACH * tid + i] = before & 0xffffu;
+    before += mine[i] + 0x10000u;
+  }
+  if (tid == 0) s.begin[all >> 16] = (uint16_t)all;
+  __syncthreads();
+  if (is) s.pairs[s.count[id] + place] = (uint16_t)tid;
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane((int)(all >> 16));
+}
+
 // 16 output channels of a run of tokens per workgroup. Its waves take the
 // experts that these tokens meet in turn (with fewer than eight of them, parts
 // of an expert's sum), every pair's sums go to LDS, and a token's are added up
@@ -639,10 +698,10 @@ __device__ __forceinline__ float value_at(const void* x, int64_t i) {
 template <int DST, int MOST, bool FEW>
 __global__ __launch_bounds__(M_WAVES* WAVE) __attribute__((amdgpu_waves_per_eu(MOST == 1 ? 4 : 2))) void k_moe_down(Moe m, int tokens_each) {
   constexpr int PAIRS = FEW ? 64 : D_SLOTS;
-  __shared__ uint32_t mask[MASK_WORDS];
+  struct None {};
+  __shared__ std::conditional_t<FEW, None, Sorted> sorted;
   __shared__ uint16_t ids[PAIRS];
   __shared__ float weights[PAIRS];
-  __shared__ uint16_t lists[FEW ? 1 : M_WAVES][PAIRS];
   __shared__ float sums[D_SLOTS][16];
   const int tiles = (m.n_in + 15) / 16;
   const int c0 = (int)(blockIdx.x % (uint32_t)tiles) * 16, t0 = (int)(blockIdx.x / (uint32_t)tiles) * tokens_each;
@@ -651,16 +710,13 @@ __global__ __launch_bounds__(M_WAVES* WAVE) __attribute__((amdgpu_waves_per_eu(M
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   if (tid < pairs) weights[tid] = m.weights[first + tid];
   int choice = -1, met_all = 0;
-  if (FEW) {
+  if constexpr (FEW) {
     choice = choice_of(m, first, pairs);
     if (tid < pairs) ids[tid] = (uint16_t)(choice < 0 ? NO_EXPERT : choice);
     for (uint64_t left = __ballot(choice >= 0); left; ++met_all)
       left &= ~__ballot(choice == __builtin_amdgcn_readlane(choice, __builtin_ctzll(left)));
   } else {
-    read_choices(m, first, pairs, ids, mask);
-#pragma unroll 8
-    for (int w = 0; w < MASK_WORDS; ++w) met_all += __builtin_popcount(mask[w]);
-    met_all = __builtin_amdgcn_readfirstlane(met_all);
+    met_all = sort_pairs(m, first, pairs, sorted, ids);
   }
   // parts of a sum in groups of four blocks
   const int groups = m.scale_pitch / 4;
@@ -673,20 +729,13 @@ __global__ __launch_bounds__(M_WAVES* WAVE) __attribute__((amdgpu_waves_per_eu(M
   for (int item = wave; item < met_all * parts; item += M_WAVES) {
     const int part = item % parts;
     Met met;
-    if (FEW) {
+    if constexpr (FEW) {
       met = met_of_few(choice, item / parts);
     } else {
-      uint16_t* list = lists[wave];
-      met.expert = __builtin_amdgcn_readfirstlane(expert_of_rank(mask, item / parts));
-      met.n = 0;
-      met.list = list;
-      for (int i = 0; i < pairs; i += 64) {
-        const bool is = i + lane < pairs && ids[i + lane] == met.expert;
-        const uint64_t all = __ballot(is);
-        if (is) list[met.n + __builtin_popcountll(all & ((1ull << lane) - 1))] = (uint16_t)(i + lane);
-        met.n += __builtin_popcountll(all);
-      }
-      wave_sync();
+      const int r = item / parts, begin = __builtin_amdgcn_readfirstlane(sorted.begin[r]);
+      met.expert = __builtin_amdgcn_readfirstlane(sorted.experts[r]);
+      met.n = __builtin_amdgcn_readfirstlane(sorted.begin[r + 1]) - begin;
+      met.list = sorted.pairs + begin;
     }
     const int from = groups * part / parts * 4, to = groups * (part + 1) / parts * 4;
     float(*out)[16] = sums + part * pairs;
@@ -699,7 +748,6 @@ __global__ __launch_bounds__(M_WAVES* WAVE) __attribute__((amdgpu_waves_per_eu(M
         at += 32;
       }
     }
-    if (!FEW) wave_sync();   // the list has been read
   }
   float residual = 0.0f;
   const bool mine = tid < tokens * 16 && c0 + (tid & 15) < m.n_in;
