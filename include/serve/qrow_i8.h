@@ -108,7 +108,8 @@ typedef struct {
  * epilogue   NULL: qr_matmul_i8.
  * residual   [n_tok, n_out] of type dst, rows residual_stride >= n_out elements
  *            apart. It may be y itself (the same pointer and stride: added in
- *            place); otherwise the two must not overlap (refused).
+ *            place); otherwise the two must not overlap (refused). y must not
+ *            overlap the other operands either (not looked at).
  * Every step is in fp32: the two products each as in qr_matmul_i8; the
  * activation, within 8 * 2^-24 of |p(w)| (and 2^-110 where exp overflows) for
  * the fp32 p(w) it is given; the gate's product and the residual's addition

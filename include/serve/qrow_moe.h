@@ -108,9 +108,10 @@ size_t qr_moe_i8_workspace_bytes(const qr_moe *m, int64_t n_tok,
  * and the residual are fp32, an expert's terms in an order that n_tok, top_k
  * and n_mid fix together with the number of distinct experts met, a token's
  * experts in the order of their slots.
- * The weights of an expert pass the chip once for up to 64 of its tokens: the
- * operator is made for few of them. More are right, up to the limit, and read
- * the weights again for each 64.
+ * The operator is made for few tokens, whose time is that of the weights' way
+ * through the chip: once for up to 64 tokens of an expert through gate and up,
+ * and for up to 16 (32 where there are many and n_mid is 4096 or more) through
+ * down. More are right, up to the limit, and read the weights again.
  * Limits: 1 <= top_k <= QR_MOE_MAX_TOP_K, n_tok * top_k <= QR_MOE_MAX_PAIRS,
  * and those of qr_moe. n_tok == 0 is a no-op.
  */

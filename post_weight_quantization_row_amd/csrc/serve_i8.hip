@@ -229,8 +229,9 @@ __device__ __forceinline__ void store_plain(const Product& p, int tok, int o, co
 
 // Few tokens: 16 channels x 16 * TT tokens per workgroup, the sum split over
 // its waves in chunks of 128 values, every operand loaded straight into the
-// registers that the matrix instruction reads (row li, 16 bytes at 16 lk). The
-// weights pass the chip once: bound by their bytes (16 tokens, 11008 x 4096:
+// registers that the matrix instruction reads (row li, 16 bytes at 16 lk; whole
+// lines of the weights, turned in registers). The weights pass the chip once:
+// bound by their bytes (16 tokens, 11008 x 4096:
 // 14 us, 3.3 TB/s; one token, 4096 x 4096: 5.4 us). From some 24 tokens on
 // every workgroup's reading of the tokens costs more, and tiles in LDS win.
 constexpr int F_WAVES = 8;

@@ -61,6 +61,13 @@ __device__ __forceinline__ Eight<SRC> eight_at(const uint8_t* row, int at) {
 // of fp32 values are exact in 64 bits, and so are the 64-bit matrix
 // instructions' operands: row li, element lk of each four. A lane loads eight
 // neighbouring values and feeds them to eight instructions, both sides alike.
+//
+// With many tokens bound by the 64-bit matrix instructions: 2048 tokens, 256
+// experts, 7168 values 127 us, 59 TFLOP/s (a large 64-bit library product: 71).
+// Few tokens are the time of two dependent trips to memory (one token: 5.9 us).
+// The bf16 matrix cores would be an order faster, but their fp32 sums do not
+// settle a choice between near scores, and exact sums for the chosen experts and
+// their neighbours cost what was won (45 us, and 71 for nine exact sums a token).
 template <int SRC, int WSRC, int TE, int TT>
 __global__ __launch_bounds__(R_WAVES* WAVE) void k_route_logits(Route p, int expert_tiles, int token_tiles) {
   __shared__ f64x4 part[R_WAVES][TE][TT][WAVE];
@@ -189,7 +196,9 @@ __device__ __forceinline__ double wave_sum(double v) {
   return __builtin_bit_cast(double, last_lane(__builtin_bit_cast(uint64_t, v)));
 }
 
-// One wave per token, expert lane + 64 j in its slot j.
+// One wave per token, expert lane + 64 j in its slot j. Rounds of the largest key
+// by DPP (through LDS permutes one token took 23 us); 6.2 us for one token, 7.0
+// for 2048.
 template <int J>
 __global__ __launch_bounds__(256) void k_route_choose(Route p) {
   const int lane = threadIdx.x & 63;
@@ -383,8 +392,8 @@ constexpr int HIDDEN_TILES = 4;        // of 16 pairs, whose products share the 
 
 // Gate and up products of one block of 64 hidden channels for 16 TT pairs of
 // one expert, and their 8-bit hidden values. Waves 0-3 have 16 channels each and
-// the first half of the sum, waves 4-7 the second; a wave holds one batch of
-// loads while the next is on its way.
+// the first half of the sum, waves 4-7 the second: a wave reads neighbouring
+// lines of 32 rows, four stages of 4 KB ahead.
 template <int TT, bool FEW>
 __device__ __forceinline__ void hidden_block(const Moe& m, const Met& met, int first, int block,
                                              i32x4 (*part)[4][2][HIDDEN_TILES][WAVE]) {
@@ -489,6 +498,12 @@ __device__ __forceinline__ void hidden_block(const Moe& m, const Met& met, int f
 // One workgroup per expert that is met and block of hidden channels: it finds
 // its expert and the expert's pairs in the choices by itself (a captured call
 // replays with other choices). FEW: all pairs fit into a wave's lanes.
+//
+// Bound by the weights' bytes. Eight of 256 experts, 7168 x 2048, for one token:
+// 39 us, 6.0 TB/s (merely reading as many bytes from 256 workgroups: 37 us); 113
+// of them for 64 tokens: 572 us, 5.8 TB/s. 23 tokens of 8 experts of 4096 x 11008:
+// 142 us, 5.1 TB/s, 1376 workgroups being 5.4 rounds of the chip. With 64-bit
+// addresses, a batch at a time and through the caches: 54, 748 and 202 us.
 template <bool FEW>
 __global__ __launch_bounds__(M_WAVES* WAVE) void k_moe_hidden(Moe m) {
   extern __shared__ uint16_t dynamic[];
@@ -695,6 +710,12 @@ __device__ __forceinline__ int sort_pairs(const Moe& m, int first, int n, Sorted
 // experts that these tokens meet in turn (with fewer than eight of them, parts
 // of an expert's sum), every pair's sums go to LDS, and a token's are added up
 // in the order of its slots.
+//
+// Bound by the weights' bytes, and by the start of every expert's: eight experts
+// of 2048 x 7168 for one token 24.5 us, 4.8 TB/s (merely read: 21 us), 113 for 64
+// tokens 320 us, 5.2 TB/s, 8 of 11008 x 4096 for 23 tokens 77 us (merely read: 69
+// to 75). Two workgroups to a CU, within 128 registers; loads that run on into
+// the wave's next expert spilled 40 of them (555 us).
 template <int DST, int MOST, bool FEW>
 __global__ __launch_bounds__(M_WAVES* WAVE) __attribute__((amdgpu_waves_per_eu(MOST == 1 ? 4 : 2))) void k_moe_down(Moe m, int tokens_each) {
   constexpr int PAIRS = FEW ? 64 : D_SLOTS;
