@@ -53,7 +53,9 @@ size_t qr_moe_route_workspace_bytes(int64_t n_experts, int64_t n_tok,
  *           an id of -1.
  * Logits are sums in 64 bits of exact products, and scores, choice and weights
  * follow in 64 bits: the choice does not depend on the launch shape unless two
- * scores agree to some 2^-50. Weights are rounded to fp32 at the end.
+ * scores agree to some 2^-50. Weights are rounded to fp32 at the end. (For many
+ * bf16 tokens, an expert that fp32 sums with their error bound already leave out
+ * of a token's choice gets no 64-bit sum; choice and weights are the same.)
  * Limits: 1 <= n_experts <= QR_MOE_MAX_EXPERTS, 1 <= top_k <= min(n_experts,
  * QR_MOE_MAX_TOP_K), 1 <= n_in <= 131072, n_tok < 2^22. n_tok == 0 is a no-op.
  */

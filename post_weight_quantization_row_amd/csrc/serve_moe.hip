@@ -18,6 +18,8 @@ using namespace serve;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef double f64x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------------------
@@ -28,6 +30,7 @@ struct Route {
   const void* w;
   const float* bias;
   double* logits;        // [splits][n_tok][n_experts]
+  float* squares;        // of rough logits, sums over the rows: [splits][n_tok] of x, [splits][n_experts] of w
   int32_t* ids;
   float* weights;
   int64_t x_stride;
@@ -65,9 +68,6 @@ __device__ __forceinline__ Eight<SRC> eight_at(const uint8_t* row, int at) {
 // With many tokens bound by the 64-bit matrix instructions: 2048 tokens, 256
 // experts, 7168 values 127 us, 59 TFLOP/s (a large 64-bit library product: 71).
 // Few tokens are the time of two dependent trips to memory (one token: 5.9 us).
-// The bf16 matrix cores would be an order faster, but their fp32 sums do not
-// settle a choice between near scores, and exact sums for the chosen experts and
-// their neighbours cost what was won (45 us, and 71 for nine exact sums a token).
 template <int SRC, int WSRC, int TE, int TT>
 __global__ __launch_bounds__(R_WAVES* WAVE) void k_route_logits(Route p, int expert_tiles, int token_tiles) {
   __shared__ f64x4 part[R_WAVES][TE][TT][WAVE];
@@ -196,61 +196,73 @@ __device__ __forceinline__ double wave_sum(double v) {
   return __builtin_bit_cast(double, last_lane(__builtin_bit_cast(uint64_t, v)));
 }
 
-// One wave per token, expert lane + 64 j in its slot j. Rounds of the largest key
-// by DPP (through LDS permutes one token took 23 us); 6.2 us for one token, 7.0
-// for 2048.
+// A wave's view of one token: expert lane + 64 j in its slot j.
 template <int J>
-__global__ __launch_bounds__(256) void k_route_choose(Route p) {
+__device__ __forceinline__ void load_logits(const Route& p, int64_t t, double (&l)[J], float (&bias)[J]) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= p.n_tok) return;
-  double v[J];
-  float bias[J];
-  uint64_t key[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int e = lane + 64 * j, at = e < p.n_experts ? e : p.n_experts - 1;
     bias[j] = p.bias ? p.bias[at] : 0.0f;
     double part[R_SPLITS];
 #pragma unroll
-    for (int s = 0; s < R_SPLITS; ++s) part[s] = s < p.splits ? p.logits[((int64_t)s * p.n_tok + t) * p.n_experts + at] : 0.0;
-    v[j] = part[0];
+    for (int s = 0; s < R_SPLITS; ++s) part[s] = s < p.splits ? __builtin_nontemporal_load(p.logits + ((int64_t)s * p.n_tok + t) * p.n_experts + at) : 0.0;
+    l[j] = part[0];
 #pragma unroll
-    for (int s = 1; s < R_SPLITS; ++s) v[j] += part[s];
+    for (int s = 1; s < R_SPLITS; ++s) l[j] += part[s];
   }
+}
+
+// Scores in the place of logits.
+template <int J>
+__device__ __forceinline__ void make_scores(const Route& p, double (&v)[J]) {
+  const int lane = threadIdx.x & 63;
   if (p.score == QR_SCORE_SIGMOID) {
 #pragma unroll
     for (int j = 0; j < J; ++j) v[j] = 1.0 / (1.0 + exp(-v[j]));
-  } else {
-    uint64_t top = 0;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const uint64_t k = order_key(v[j]);
-      if (lane + 64 * j < p.n_experts && k > top) top = k;
-    }
-    const double most = of_key(wave_largest(top));
-    double sum = 0.0;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      v[j] = exp(v[j] - most);
-      if (lane + 64 * j < p.n_experts) sum += v[j];
-    }
-    sum = wave_sum(sum);
-#pragma unroll
-    for (int j = 0; j < J; ++j) v[j] /= sum;
+    return;
   }
+  uint64_t top = 0;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const uint64_t k = order_key(v[j]);
+    if (lane + 64 * j < p.n_experts && k > top) top = k;
+  }
+  const double most = of_key(wave_largest(top));
+  double sum = 0.0;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    v[j] = exp(v[j] - most);
+    if (lane + 64 * j < p.n_experts) sum += v[j];
+  }
+  sum = wave_sum(sum);
+#pragma unroll
+  for (int j = 0; j < J; ++j) v[j] /= sum;
+}
+
+// The top_k largest of v + bias, largest first: round r's into lane r, with its v
+// and the key it was found by; `next`, of the round behind it (0: there is none).
+struct Found {
+  int expert;
+  double value;
+  uint64_t key, next;
+};
+
+template <int J>
+__device__ __forceinline__ Found find_largest(const Route& p, const double (&v)[J], const float (&bias)[J]) {
+  const int lane = threadIdx.x & 63;
+  uint64_t key[J];
 #pragma unroll
   for (int j = 0; j < J; ++j)
     key[j] = lane + 64 * j < p.n_experts && bias[j] != -__builtin_inff() ? order_key(v[j] + (double)bias[j]) : 0;
-  // lane r keeps what the r-th round chose
-  int chosen = -1;
-  double score = 0.0;
-  for (int r = 0; r < p.top_k; ++r) {
+  Found f = {-1, 0.0, 0, 0};
+  for (int r = 0;; ++r) {
     uint64_t best = 0;
 #pragma unroll
     for (int j = 0; j < J; ++j) best = key[j] > best ? key[j] : best;
     best = wave_largest(best);
-    if (best == 0) break;
+    if (lane == r - 1) f.next = best;
+    if (best == 0 || r == p.top_k) break;
     // among equals the lowest: the first slot that has one, its first lane
     int at = -1;
     double won = 0.0;
@@ -264,18 +276,343 @@ __global__ __launch_bounds__(256) void k_route_choose(Route p) {
       if (lane == from) key[j] = 0;
     }
     if (lane == r) {
-      chosen = at;
-      score = won;
+      f.expert = at;
+      f.value = won;
+      f.key = best;
     }
   }
+  return f;
+}
+
+__device__ __forceinline__ void store_choice(const Route& p, int64_t t, const Found& f) {
+  const int lane = threadIdx.x & 63;
+  double w = f.value;
   if (p.renorm) {
-    const double sum = wave_sum(score);
-    score = sum == 0.0 ? 0.0 : score / sum;
+    const double sum = wave_sum(w);
+    w = sum == 0.0 ? 0.0 : w / sum;
   }
   if (lane < p.top_k) {
-    p.ids[t * p.top_k + lane] = chosen;
-    p.weights[t * p.top_k + lane] = chosen < 0 ? 0.0f : (float)(score * (double)p.factor);
+    p.ids[t * p.top_k + lane] = f.expert;
+    p.weights[t * p.top_k + lane] = f.expert < 0 ? 0.0f : (float)(w * (double)p.factor);
   }
+}
+
+// One wave per token. Rounds of the largest key by DPP (through LDS permutes one
+// token took 23 us); 6.2 us for one token, 7.0 for 2048.
+template <int J>
+__global__ __launch_bounds__(256) void k_route_choose(Route p) {
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= p.n_tok) return;
+  double v[J];
+  float bias[J];
+  load_logits<J>(p, t, v, bias);
+  make_scores<J>(p, v);
+  store_choice(p, t, find_largest<J>(p, v, bias));
+}
+
+// Rough logits of many tokens, both sides bf16: the bf16 matrix cores' fp32 sums
+// of ROUGH_SUM products, added up in 64 bits. k_route_settle takes exact ones
+// where they matter. 2048 tokens, 256 experts, 7168 values: 27 us, of which the
+// products are 6; the steps' parts follow each other in the one workgroup of a CU
+// (two of them, or loads five steps ahead: no faster).
+//
+// 64 experts x 128 tokens per workgroup, 64 values of the sum per step through
+// LDS, loads ROUGH_AHEAD steps ahead. In LDS the 16-byte piece c of row r lies at
+// r * 128 + (c ^ (r / 2 % 8)) * 16: sixteen lanes that take one piece of
+// neighbouring rows meet all banks.
+constexpr int ROUGH_SUM = 128, ROUGH_E = 64, ROUGH_T = 128, ROUGH_K = 64, ROUGH_AHEAD = 3;
+
+__global__ __launch_bounds__(512) void k_route_rough(Route p, int expert_tiles, int token_tiles) {
+  __shared__ u32x4 tile[2][(ROUGH_E + ROUGH_T) * 8];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int li = lane & 15, lk = lane >> 4;
+  // workgroups are dealt to the 8 dies in turn: each die gets neighbouring tiles,
+  // so that the experts' tiles of one token tile find it in one L2
+  const int all = (int)gridDim.x, die = (int)(blockIdx.x % 8);
+  int block = die * (all / 8) + (die < all % 8 ? die : all % 8) + (int)(blockIdx.x / 8);
+  const int be = block % expert_tiles;
+  block /= expert_tiles;
+  const int bt = block % token_tiles, split = block / token_tiles;
+  // staging: piece tid % 8 of rows tid / 8 (experts) and 64 and 128 behind it (tokens)
+  const int row = tid >> 3, col = tid & 7;
+  const uint16_t* src[3];
+  {
+    const int e = be * ROUGH_E + row, t = bt * ROUGH_T + row;
+    src[0] = reinterpret_cast<const uint16_t*>(p.w) + (int64_t)(e < p.n_experts ? e : p.n_experts - 1) * p.n_in + 8 * col;
+    src[1] = reinterpret_cast<const uint16_t*>(p.x) + (int64_t)(t < p.n_tok ? t : p.n_tok - 1) * p.x_stride + 8 * col;
+    src[2] = reinterpret_cast<const uint16_t*>(p.x) + (int64_t)(t + 64 < p.n_tok ? t + 64 : p.n_tok - 1) * p.x_stride + 8 * col;
+  }
+  const int put = row * 8 + (col ^ ((row >> 1) & 7));
+  u32x4 raw[ROUGH_AHEAD][3];
+  auto load = [&](u32x4 (&r)[3], int step) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) r[i] = __builtin_bit_cast(u32x4, *reinterpret_cast<const u16x8_any*>(src[i] + step * ROUGH_K));
+  };
+  float sq[3] = {};
+  auto stage = [&](const u32x4 (&r)[3], u32x4* to) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      to[put + i * 64 * 8] = r[i];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bf16x2 two = __builtin_bit_cast(bf16x2, (uint32_t)r[i][k]);
+        sq[i] = __builtin_amdgcn_fdot2_f32_bf16(two, two, sq[i], false);
+      }
+    }
+  };
+  // a wave's part of the tile: 32 experts x 32 tokens
+  const int we = (wave & 1) * 32, wt = ROUGH_E + (wave >> 1) * 32;
+  f64x4 acc[2][2] = {};
+  f32x4 sum[2][2] = {};
+  auto multiply = [&](const u32x4* from) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      bf16x8 a[2], b[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int ra = we + 16 * i + li, rb = wt + 16 * i + li;
+        a[i] = __builtin_bit_cast(bf16x8, from[ra * 8 + ((4 * k + lk) ^ ((ra >> 1) & 7))]);
+        b[i] = __builtin_bit_cast(bf16x8, from[rb * 8 + ((4 * k + lk) ^ ((rb >> 1) & 7))]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) sum[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], sum[i][j], 0, 0, 0);
+    }
+  };
+  auto flush = [&]() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][j][v] += (double)sum[i][j][v];
+        sum[i][j] = f32x4{0, 0, 0, 0};
+      }
+  };
+  // whole steps; what is left of the rows is the last split's, behind them
+  const int steps = p.n_in / ROUGH_K;
+  const int from = (int)((int64_t)steps * split / p.splits), to = (int)((int64_t)steps * (split + 1) / p.splits);
+#pragma unroll
+  for (int s = 0; s < ROUGH_AHEAD; ++s)
+    if (from + s < to) load(raw[s], from + s);
+  if (from < to) stage(raw[0], tile[0]);
+  if (from + ROUGH_AHEAD < to) load(raw[0], from + ROUGH_AHEAD);
+  __syncthreads();
+  int s = from;
+  // (no conditions here: where loads may or may not be on their way, all are waited for)
+  for (; s + 2 * ROUGH_AHEAD < to; s += ROUGH_AHEAD) {
+#pragma unroll
+    for (int u = 0; u < ROUGH_AHEAD; ++u) {
+      const int now = (s + u - from) & 1;
+      stage(raw[(u + 1) % ROUGH_AHEAD], tile[now ^ 1]);
+      load(raw[(u + 1) % ROUGH_AHEAD], s + u + 1 + ROUGH_AHEAD);
+      multiply(tile[now]);
+      if (now) flush();
+      __syncthreads();
+    }
+  }
+  for (; s < to; s += ROUGH_AHEAD) {
+#pragma unroll
+    for (int u = 0; u < ROUGH_AHEAD; ++u) {
+      const int now = (s + u - from) & 1;
+      if (s + u >= to) break;
+      if (s + u + 1 < to) {
+        stage(raw[(u + 1) % ROUGH_AHEAD], tile[now ^ 1]);
+        if (s + u + 1 + ROUGH_AHEAD < to) load(raw[(u + 1) % ROUGH_AHEAD], s + u + 1 + ROUGH_AHEAD);
+      }
+      multiply(tile[now]);
+      if (now) flush();
+      __syncthreads();
+    }
+  }
+  flush();
+  if (split == p.splits - 1 && p.n_in % ROUGH_K != 0) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      u16x8_any v;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = steps * ROUGH_K + 8 * col + k < p.n_in ? src[i][steps * ROUGH_K + k] : (uint16_t)0;
+      raw[0][i] = __builtin_bit_cast(u32x4, v);
+    }
+    stage(raw[0], tile[0]);
+    __syncthreads();
+    multiply(tile[0]);
+    flush();
+  }
+  // a lane holds experts 4 lk + v of a tile for token li
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int t = bt * ROUGH_T + wt - ROUGH_E + 16 * j + li;
+    if (t >= p.n_tok) continue;
+    double* out = p.logits + ((int64_t)split * p.n_tok + t) * p.n_experts;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int e = be * ROUGH_E + we + 16 * i + 4 * lk + v;
+        if (e < p.n_experts) out[e] = acc[i][j][v];
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) sq[i] += __shfl_xor(sq[i], d);
+    const int e = be * ROUGH_E + row, t = bt * ROUGH_T + row + 64 * (i - 1);
+    if (col != 0) continue;
+    if (i == 0 && bt == 0 && e < p.n_experts) p.squares[(int64_t)p.splits * p.n_tok + (int64_t)split * p.n_experts + e] = sq[i];
+    if (i > 0 && be == 0 && t < p.n_tok) p.squares[(int64_t)split * p.n_tok + t] = sq[i];
+  }
+}
+
+// How far a token's rough logits may be off: fp32 sums of ROUGH_SUM exact
+// products, each addition off by a last place of the products' magnitudes added
+// up (twice what rounding does), and those at most the rows' lengths multiplied.
+// Zero for a row of zeros, whose logits are exact. (By one wave.)
+__device__ __forceinline__ double rough_error(const Route& p, int64_t t) {
+  const int lane = threadIdx.x & 63;
+  float x = 0.0f, w = 0.0f;
+  for (int s = 0; s < p.splits; ++s) x += p.squares[(int64_t)s * p.n_tok + t];
+  for (int e = lane; e < p.n_experts; e += WAVE) {
+    float v = 0.0f;
+    for (int s = 0; s < p.splits; ++s) v += p.squares[(int64_t)p.splits * p.n_tok + (int64_t)s * p.n_experts + e];
+    w = v > w || v != v ? v : w;
+  }
+  const double most = of_key(wave_largest(order_key((double)w)));
+  if (x < 0x1p-80f) {            // squares and products may have vanished
+    uint32_t any = 0;
+    const uint16_t* row = reinterpret_cast<const uint16_t*>(p.x) + t * p.x_stride;
+    for (int at = lane; at < p.n_in; at += WAVE) any |= row[at] & 0x7fffu;
+    return __ballot(any != 0) ? __builtin_inf() : 0.0;
+  }
+  if (most < 0x1p-80) return __builtin_inf();
+  return ROUGH_SUM * 0x1p-23 * 1.02 * __builtin_sqrt((double)x) * __builtin_sqrt(most);
+}
+
+// The exact logits of N experts of a list, by one wave.
+template <int N>
+__device__ __forceinline__ void exact_logits(const Route& p, int64_t t, const uint16_t* list, double* out) {
+  const int lane = threadIdx.x & 63;
+  const uint16_t* x = reinterpret_cast<const uint16_t*>(p.x) + t * p.x_stride;
+  const uint16_t* w[N];
+#pragma unroll
+  for (int q = 0; q < N; ++q)
+    w[q] = reinterpret_cast<const uint16_t*>(p.w) + (int64_t)__builtin_amdgcn_readfirstlane(list[q]) * p.n_in;
+  double sum[N] = {};
+  const int whole = p.n_in / (8 * WAVE) * (8 * WAVE);
+#pragma unroll 2
+  for (int at = 8 * lane; at < whole; at += 8 * WAVE) {
+    const u16x8_any a = __builtin_nontemporal_load(reinterpret_cast<const u16x8_any*>(x + at));
+    u16x8_any b[N];
+#pragma unroll
+    for (int q = 0; q < N; ++q) b[q] = *reinterpret_cast<const u16x8_any*>(w[q] + at);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const double v = (double)bf16_value(a[i]);
+#pragma unroll
+      for (int q = 0; q < N; ++q) sum[q] = __builtin_fma(v, (double)bf16_value(b[q][i]), sum[q]);
+    }
+  }
+  if (whole < p.n_in) {
+    float a[8], b[8];
+    load8<QR_BF16>(x, whole + 8 * lane, p.n_in, a);
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      load8<QR_BF16>(w[q], whole + 8 * lane, p.n_in, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[q] = __builtin_fma((double)a[i], (double)b[i], sum[q]);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const double l = wave_sum(sum[q]);
+    if (lane == 0) out[q] = l;
+  }
+}
+
+// The choice from rough logits, off by up to d: one workgroup per token. What is
+// found as the largest, u = logit or (with a bias, of sigmoids, whose slope is at
+// most 1/4) score + bias, is off by up to d or d / 4. The chosen ones get exact
+// logits, for their weights, and so does all that lies so near to one that it may
+// come before it; the choice is then made again, of the scores, which is the one
+// that exact logits throughout would give. Near is also what the 64 bits of a score
+// (+ bias) may not tell apart: that part of the margin is seen only where sigmoids
+// near one, scores of no size or a huge bias round the differences away.
+//
+// 2048 tokens, 8 of 256 experts: 43 us, 30 of them for some nine exact logits a
+// token (four vector instructions a product, conversions to 64 bits most of them).
+// 64 registers, for eight workgroups to a CU, which hide each other's waits (100:
+// 55 us).
+template <int J>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(J <= 4 ? 8 : J == 8 ? 4 : 2))) void k_route_settle(Route p) {
+  __shared__ double exact[64 * J];
+  __shared__ uint16_t list[64 * J];
+  __shared__ int listed;
+  __shared__ double rough;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = blockIdx.x;
+  double l[J];
+  float bias[J];
+  int at[J];                     // where the list has this lane's experts, or -1
+  double u[J];
+  Found f;
+  if (wave == 0) {
+    load_logits<J>(p, t, l, bias);
+#pragma unroll
+    for (int j = 0; j < J; ++j) u[j] = p.bias ? 1.0 / (1.0 + exp(-l[j])) : l[j];
+    f = find_largest<J>(p, u, bias);
+  } else if (wave == 1) {
+    const double d = rough_error(p, t);
+    if (lane == 0) rough = d;
+  }
+  __syncthreads();
+  if (wave == 0) {
+    const double d = rough;
+    uint32_t want = 0;           // of this lane's experts: bit j
+    const double u0 = of_key(f.key), u1 = of_key(f.next);
+    double margin;
+    if (p.bias) margin = 0.52 * d + 0x1p-50 * (1.0 + __builtin_fabs(u0) + __builtin_fabs(u1));
+    else if (p.score == QR_SCORE_SIGMOID) margin = 2.0 * d + 0x1p-49 * (1.0 + exp(u0));
+    else margin = u1 - of_key(__shfl(f.key, 0)) < -690.0 ? __builtin_inf() : 2.0 * d + 0x1p-48;
+    for (uint64_t unsure = __ballot(f.expert >= 0 && f.next != 0 && !(u0 - u1 > margin)); unsure; unsure &= unsure - 1) {
+      const int r = __builtin_ctzll(unsure);
+      const double upper = __shfl(u0 + margin, r), lower = __shfl(u1 - margin, r);
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const double v = u[j] + (double)bias[j];
+        if (lane + 64 * j < p.n_experts && !(v > upper) && !(v < lower)) want |= 1u << j;
+      }
+    }
+    for (int r = 0; r < p.top_k; ++r) {
+      const int e = __builtin_amdgcn_readlane(f.expert, r);
+      if (e >= 0 && lane == (e & 63)) want |= 1u << (e >> 6);
+    }
+    if (d == 0.0) want = 0;
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const bool is = want >> j & 1;
+      const uint64_t all = __ballot(is);
+      at[j] = is ? n + __builtin_popcountll(all & ((1ull << lane) - 1)) : -1;
+      if (is) list[at[j]] = (uint16_t)(lane + 64 * j);
+      n += __builtin_popcountll(all);
+    }
+    if (lane == 0) listed = n;
+  }
+  __syncthreads();
+  const int n = __builtin_amdgcn_readfirstlane(listed);
+  // dealt evenly: a wave's experts share the token's row
+  for (int i = n * wave / 4; i < n * (wave + 1) / 4; i += 2) {
+    if (n * (wave + 1) / 4 - i == 1) exact_logits<1>(p, t, list + i, exact + i);
+    else exact_logits<2>(p, t, list + i, exact + i);
+  }
+  __syncthreads();
+  if (wave != 0) return;
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+    if (at[j] >= 0) l[j] = exact[at[j]];
+  make_scores<J>(p, l);
+  store_choice(p, t, find_largest<J>(p, l, bias));
 }
 
 // ---------------------------------------------------------------------------
@@ -796,19 +1133,25 @@ __global__ __launch_bounds__(M_WAVES* WAVE) __attribute__((amdgpu_waves_per_eu(M
 // launches
 
 struct RoutePlan {
-  bool wide;
+  bool rough, wide;
   int expert_tiles, token_tiles, splits;
 };
 
-// Tiles of 32 x 32 where they fill the chip, else of 16 x 16 with the sum split
-// until there are some 256 workgroups.
-RoutePlan route_plan(int64_t n_experts, int64_t n_tok, int64_t n_in) {
+// Rough logits where there is much to multiply; tiles of 32 x 32 where they fill
+// the chip, or of 16 x 16; and the sum split until there are some 256 workgroups.
+// Measured, us (8 of 256 experts, 7168 values): 512 tokens in 64 bits 49.5, rough
+// 49.5; 1024 74 and 56, 2048 132 and 69, 4096 254 and 114; 8 of 512, 4096 values:
+// 512 tokens 50 and 53, 1024 85 and 52.
+RoutePlan route_plan(bool rough, int64_t n_experts, int64_t n_tok, int64_t n_in) {
   RoutePlan r;
-  r.wide = ((n_experts + 31) / 32) * ((n_tok + 31) / 32) >= 256;
-  const int64_t tile = r.wide ? 32 : 16;
-  r.expert_tiles = (int)((n_experts + tile - 1) / tile);
-  r.token_tiles = (int)((n_tok + tile - 1) / tile);
-  const int64_t most = (n_in + R_CHUNK * R_WAVES - 1) / (R_CHUNK * R_WAVES);
+  r.rough = rough && n_experts * n_tok > ((int64_t)1 << 30) / n_in;
+  r.wide = !r.rough && ((n_experts + 31) / 32) * ((n_tok + 31) / 32) >= 256;
+  const int64_t experts = r.rough ? ROUGH_E : r.wide ? 32 : 16, tokens = r.rough ? ROUGH_T : r.wide ? 32 : 16;
+  r.expert_tiles = (int)((n_experts + experts - 1) / experts);
+  r.token_tiles = (int)((n_tok + tokens - 1) / tokens);
+  // (a part of the sum has eight waves' chunks, or four steps)
+  const int64_t part = r.rough ? 4 * ROUGH_K : R_CHUNK * R_WAVES;
+  const int64_t most = (n_in + part - 1) / part;
   int64_t s = 256 / ((int64_t)r.expert_tiles * r.token_tiles);
   s = s > R_SPLITS ? R_SPLITS : s;
   s = s > most ? most : s;
@@ -816,18 +1159,32 @@ RoutePlan route_plan(int64_t n_experts, int64_t n_tok, int64_t n_in) {
   return r;
 }
 
+size_t route_bytes(const RoutePlan& r, int64_t n_experts, int64_t n_tok) {
+  const size_t logits = (size_t)r.splits * (size_t)n_tok * (size_t)n_experts * sizeof(double);
+  return logits + (r.rough ? (size_t)r.splits * (size_t)(n_tok + n_experts) * sizeof(float) : 0);
+}
+
+template <int J>
+int launch_choose(const Route& p, bool rough, hipStream_t s) {
+  if (rough) {
+    hipLaunchKernelGGL((k_route_settle<J>), dim3((uint32_t)p.n_tok), dim3(256), 0, s, p);
+    return qr_check_launch("k_route_settle");
+  }
+  hipLaunchKernelGGL((k_route_choose<J>), dim3((uint32_t)((p.n_tok + 3) / 4)), dim3(256), 0, s, p);
+  return qr_check_launch("k_route_choose");
+}
+
 template <int SRC, int WSRC>
 int launch_route(const Route& p, const RoutePlan& r, hipStream_t s) {
   const dim3 grid((uint32_t)(r.expert_tiles * (int64_t)r.token_tiles * r.splits)), block(R_WAVES * WAVE);
-  if (r.wide) hipLaunchKernelGGL((k_route_logits<SRC, WSRC, 2, 2>), grid, block, 0, s, p, r.expert_tiles, r.token_tiles);
+  if (r.rough) hipLaunchKernelGGL(k_route_rough, grid, dim3(512), 0, s, p, r.expert_tiles, r.token_tiles);
+  else if (r.wide) hipLaunchKernelGGL((k_route_logits<SRC, WSRC, 2, 2>), grid, block, 0, s, p, r.expert_tiles, r.token_tiles);
   else hipLaunchKernelGGL((k_route_logits<SRC, WSRC, 1, 1>), grid, block, 0, s, p, r.expert_tiles, r.token_tiles);
-  int rc = qr_check_launch("k_route_logits");
+  const int rc = qr_check_launch(r.rough ? "k_route_rough" : "k_route_logits");
   if (rc != QR_OK) return rc;
-  const dim3 tokens((uint32_t)((p.n_tok + 3) / 4));
-  if (p.n_experts <= 64) hipLaunchKernelGGL((k_route_choose<1>), tokens, dim3(256), 0, s, p);
-  else if (p.n_experts <= 256) hipLaunchKernelGGL((k_route_choose<4>), tokens, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((k_route_choose<16>), tokens, dim3(256), 0, s, p);
-  return qr_check_launch("k_route_choose");
+  if (p.n_experts <= 64) return launch_choose<1>(p, r.rough, s);
+  if (p.n_experts <= 256) return launch_choose<4>(p, r.rough, s);
+  return p.n_experts <= 512 ? launch_choose<8>(p, r.rough, s) : launch_choose<16>(p, r.rough, s);
 }
 
 bool route_shapes(int64_t n_experts, int64_t n_tok, int64_t n_in) {
@@ -882,7 +1239,10 @@ extern "C" {
 
 size_t qr_moe_route_workspace_bytes(int64_t n_experts, int64_t n_tok, int64_t n_in) {
   if (!route_shapes(n_experts, n_tok, n_in) || n_tok == 0) return 0;
-  return (size_t)route_plan(n_experts, n_tok, n_in).splits * (size_t)n_tok * (size_t)n_experts * sizeof(double);
+  // enough for either way to the logits: which one is taken goes by types and scores
+  const size_t a = route_bytes(route_plan(false, n_experts, n_tok, n_in), n_experts, n_tok);
+  const size_t b = route_bytes(route_plan(true, n_experts, n_tok, n_in), n_experts, n_tok);
+  return a > b ? a : b;
 }
 
 int qr_moe_route(int src, const void* x, int64_t x_stride, int wtype, const void* w, const float* bias,
@@ -909,8 +1269,17 @@ int qr_moe_route(int src, const void* x, int64_t x_stride, int wtype, const void
   const size_t need = qr_moe_route_workspace_bytes(n_experts, n_tok, n_in);
   if (!workspace || !qr_aligned(workspace, 256)) return qr_fail(QR_EINVAL_PTR, "workspace must be non-NULL and 256-byte aligned");
   if (workspace_bytes < need) return qr_fail(QR_EINVAL_SHAPE, "workspace has %zu bytes, %zu are needed", workspace_bytes, need);
-  const RoutePlan r = route_plan(n_experts, n_tok, n_in);
-  const Route p = {x, w, bias, reinterpret_cast<double*>(workspace), ids, weights, x_stride, (int)n_experts, (int)n_tok,
+  // Both sides bf16, no softmax whose scores meet a bias or are the weights as they
+  // are (those hang on all of the logits), and experts enough, since an exact logit
+  // costs as much as seven on the matrix cores. 4096 tokens, us, in 64 bits and
+  // rough: 1 of 128 experts 81 and 48, 8 of 128 85 and 75, 8 of 192 119 and 81; but
+  // 32 of 256 166 and 187, 6 of 64 (2048 values) 29 and 44
+  const bool rough = src == QR_BF16 && wtype == QR_BF16 && (score == QR_SCORE_SIGMOID || (renorm && !bias)) &&
+                     n_experts > 64 + 7 * top_k;
+  const RoutePlan r = route_plan(rough, n_experts, n_tok, n_in);
+  double* logits = reinterpret_cast<double*>(workspace);
+  float* squares = reinterpret_cast<float*>(logits + (size_t)r.splits * (size_t)n_tok * (size_t)n_experts);
+  const Route p = {x, w, bias, logits, squares, ids, weights, x_stride, (int)n_experts, (int)n_tok,
                    (int)n_in, (int)top_k, r.splits, score, renorm, factor};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (src == QR_BF16) return wtype == QR_BF16 ? launch_route<QR_BF16, QR_BF16>(p, r, s) : launch_route<QR_BF16, QR_F32>(p, r, s);
