@@ -51,6 +51,8 @@ size_t qr_moe_route_workspace_bytes(int64_t n_experts, int64_t n_tok,
  *           before everything. -1 behind the experts that can be chosen.
  *  weights  fp32 [n_tok, top_k], written: their scores (without bias); 0 beside
  *           an id of -1.
+ *  workspace 256-byte aligned, qr_moe_route_workspace_bytes bytes, of one call at
+ *           a time. It, ids and weights overlap nothing else (not looked at).
  * Logits are sums in 64 bits of exact products, and scores, choice and weights
  * follow in 64 bits: the choice does not depend on the launch shape unless two
  * scores agree to some 2^-50. Weights are rounded to fp32 at the end. (For many
@@ -102,6 +104,8 @@ size_t qr_moe_i8_workspace_bytes(const qr_moe *m, int64_t n_tok,
  *  dst, y   QR_F32 or QR_BF16; [n_tok, n_in], token t at element t * y_stride
  *           (>= n_in), written completely. y overlaps no other input (refused
  *           for x, xd, ids and weights; the experts' weights are not looked at).
+ *  workspace 256-byte aligned, qr_moe_i8_workspace_bytes bytes, of one call at a
+ *           time; overlaps nothing (refused for x, xd, ids, weights, residual and y).
  * Steps: gate and up products as in qr_matmul_i8, in fp32; act(gate) * up in 64
  * bits, rounded to fp32; these hidden rows are held in 8 bits with one fp32
  * scale per 64 channels (max / 127, codes rint(h * (127 / max)), the rule of

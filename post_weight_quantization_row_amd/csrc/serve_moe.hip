@@ -1328,6 +1328,12 @@ int qr_moe_i8(const qr_moe* m, const int8_t* x, const float* xd, const int32_t* 
       rows_meet_range(y, y_stride * esize, row, n_tok, weights, pairs * 4) ||
       rows_meet_range(y, y_stride * esize, row, n_tok, workspace, (int64_t)need))
     return qr_fail(QR_EINVAL_PTR, "y must not overlap x, xd, ids, weights or the workspace");
+  if (rows_meet_range(workspace, (int64_t)need, (int64_t)need, 1, x, n_tok * in_bytes) ||
+      rows_meet_range(workspace, (int64_t)need, (int64_t)need, 1, xd, n_tok * 4) ||
+      rows_meet_range(workspace, (int64_t)need, (int64_t)need, 1, ids, pairs * 4) ||
+      rows_meet_range(workspace, (int64_t)need, (int64_t)need, 1, weights, pairs * 4) ||
+      (residual && rows_meet_range(residual, residual_stride * esize, row, n_tok, workspace, (int64_t)need)))
+    return qr_fail(QR_EINVAL_PTR, "the workspace must not overlap x, xd, ids, weights or residual");
   const int64_t blocks = (m->n_mid + M_BLOCK - 1) / M_BLOCK;
   int8_t* h = reinterpret_cast<int8_t*>(workspace);
   const Moe a = {m->gate, m->up, m->down, m->gated, m->upd, m->downd, x, xd, ids, weights, h,

@@ -222,6 +222,18 @@ def test_experts_overlaps(lib):
     assert call(ys=256, xd=y + 256, ids=y + 512, weights=y + 1024 + 256) == DEVICE
 
 
+@no_gpu
+def test_experts_workspace_overlaps(lib):
+    """Choices that change under the call would part the waves of a workgroup."""
+    m, ws = moe(), 0x7000000
+    need = lib.qr_moe_i8_workspace_bytes(C.byref(m), 4, 2)
+    call = lambda **kw: moe_call(lib, ws=ws, **kw)
+    assert call() == DEVICE and call(ids=ws + need, weights=ws - 32, x=ws - 512 - 32, r=ws + need + 32) == DEVICE
+    for kw in (dict(ids=ws + need - 4), dict(ids=ws - 28), dict(weights=ws), dict(x=ws - 496), dict(xd=ws + 4), dict(r=ws + need - 4),
+               dict(r=ws - 1020)):
+        assert call(**kw) == -3 and "workspace must not overlap" in qr_last_error(), kw
+
+
 # --------------------------------------------------------------------------
 # the binding
 
