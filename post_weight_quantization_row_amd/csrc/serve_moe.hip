@@ -166,23 +166,31 @@ __device__ __forceinline__ uint64_t moved(uint64_t v) {
   return (uint64_t)hi << 32 | lo;
 }
 
-__device__ __forceinline__ uint64_t last_lane(uint64_t v) {
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, 63);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), 63);
+__device__ __forceinline__ uint64_t of_lane(uint64_t v, int lane) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
   return (uint64_t)hi << 32 | lo;
 }
 
 // The largest key and the sum of a wave, without LDS: rows of 16 lanes by
 // shifts of 1, 2, 4 and 8, then the rows' last lanes passed on.
-__device__ __forceinline__ uint64_t wave_largest(uint64_t v) {
-  const auto take = [&](uint64_t o) { v = o > v ? o : v; };
+__device__ __forceinline__ uint32_t wave_largest(uint32_t v) {
+  const auto take = [&](uint64_t o) { v = (uint32_t)o > v ? (uint32_t)o : v; };
   take(moved<0x111, 0xf>(v));
   take(moved<0x112, 0xf>(v));
   take(moved<0x114, 0xf>(v));
   take(moved<0x118, 0xf>(v));
   take(moved<0x142, 0xa>(v));
   take(moved<0x143, 0xc>(v));
-  return last_lane(v);
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// (the high halves, and the low ones where more than one lane has the highest)
+__device__ __forceinline__ uint64_t wave_largest(uint64_t v) {
+  const uint32_t hi = wave_largest((uint32_t)(v >> 32));
+  const uint64_t have = __ballot((uint32_t)(v >> 32) == hi);
+  if ((have & (have - 1)) == 0) return of_lane(v, __builtin_ctzll(have));
+  return (uint64_t)hi << 32 | wave_largest((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
 }
 
 __device__ __forceinline__ double wave_sum(double v) {
@@ -193,7 +201,7 @@ __device__ __forceinline__ double wave_sum(double v) {
   add(moved<0x118, 0xf>(__builtin_bit_cast(uint64_t, v)));
   add(moved<0x142, 0xa>(__builtin_bit_cast(uint64_t, v)));
   add(moved<0x143, 0xc>(__builtin_bit_cast(uint64_t, v)));
-  return __builtin_bit_cast(double, last_lane(__builtin_bit_cast(uint64_t, v)));
+  return __builtin_bit_cast(double, of_lane(__builtin_bit_cast(uint64_t, v), 63));
 }
 
 // A wave's view of one token: expert lane + 64 j in its slot j.
@@ -272,7 +280,7 @@ __device__ __forceinline__ Found find_largest(const Route& p, const double (&v)[
       if (at >= 0 || have == 0) continue;
       const int from = __builtin_ctzll(have);
       at = 64 * j + from;
-      won = __shfl(v[j], from);
+      won = __builtin_bit_cast(double, of_lane(__builtin_bit_cast(uint64_t, v[j]), from));
       if (lane == from) key[j] = 0;
     }
     if (lane == r) {
@@ -298,7 +306,7 @@ __device__ __forceinline__ void store_choice(const Route& p, int64_t t, const Fo
 }
 
 // One wave per token. Rounds of the largest key by DPP (through LDS permutes one
-// token took 23 us); 6.2 us for one token, 7.0 for 2048.
+// token took 23 us); 6.0 us for one token, 7.0 for 2048.
 template <int J>
 __global__ __launch_bounds__(256) void k_route_choose(Route p) {
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -539,10 +547,11 @@ __device__ __forceinline__ void exact_logits(const Route& p, int64_t t, const ui
 // (+ bias) may not tell apart: that part of the margin is seen only where sigmoids
 // near one, scores of no size or a huge bias round the differences away.
 //
-// 2048 tokens, 8 of 256 experts: 43 us, 30 of them for some nine exact logits a
-// token (four vector instructions a product, conversions to 64 bits most of them).
-// 64 registers, for eight workgroups to a CU, which hide each other's waits (100:
-// 55 us).
+// 2048 tokens, 8 of 256 experts: 42 us, some 30 of them for nine exact logits a
+// token. Vector instructions are issued in 56% of the time, four for each product
+// of a sum (conversions to 64 bits most of them) and half as many again for the
+// choice; a sum's halves or quarters dealt to the waves: no faster. 64 registers,
+// for eight workgroups to a CU, which hide each other's waits (100: 55 us).
 template <int J>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(J <= 4 ? 8 : J == 8 ? 4 : 2))) void k_route_settle(Route p) {
   __shared__ double exact[64 * J];
@@ -556,6 +565,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(J <= 4 ? 8 
   int at[J];                     // where the list has this lane's experts, or -1
   double u[J];
   Found f;
+  uint64_t unsure = 0;
   if (wave == 0) {
     load_logits<J>(p, t, l, bias);
 #pragma unroll
@@ -568,36 +578,43 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(J <= 4 ? 8 
   __syncthreads();
   if (wave == 0) {
     const double d = rough;
-    uint32_t want = 0;           // of this lane's experts: bit j
     const double u0 = of_key(f.key), u1 = of_key(f.next);
     double margin;
     if (p.bias) margin = 0.52 * d + 0x1p-50 * (1.0 + __builtin_fabs(u0) + __builtin_fabs(u1));
     else if (p.score == QR_SCORE_SIGMOID) margin = 2.0 * d + 0x1p-49 * (1.0 + exp(u0));
     else margin = u1 - of_key(__shfl(f.key, 0)) < -690.0 ? __builtin_inf() : 2.0 * d + 0x1p-48;
-    for (uint64_t unsure = __ballot(f.expert >= 0 && f.next != 0 && !(u0 - u1 > margin)); unsure; unsure &= unsure - 1) {
-      const int r = __builtin_ctzll(unsure);
-      const double upper = __shfl(u0 + margin, r), lower = __shfl(u1 - margin, r);
+    const uint64_t found = __ballot(f.expert >= 0);
+    unsure = __ballot(f.expert >= 0 && f.next != 0 && !(u0 - u1 > margin));
+    if (unsure == 0) {           // the choice stands as it is
+      if (f.expert >= 0) list[lane] = (uint16_t)f.expert;
+      if (lane == 0) listed = d == 0.0 ? 0 : __builtin_popcountll(found);
+    } else {
+      uint32_t want = 0;         // of this lane's experts: bit j
+      for (uint64_t left = unsure; left; left &= left - 1) {
+        const int r = __builtin_ctzll(left);
+        const double upper = __shfl(u0 + margin, r), lower = __shfl(u1 - margin, r);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const double v = u[j] + (double)bias[j];
+          if (lane + 64 * j < p.n_experts && !(v > upper) && !(v < lower)) want |= 1u << j;
+        }
+      }
+      for (int r = 0; r < p.top_k; ++r) {
+        const int e = __builtin_amdgcn_readlane(f.expert, r);
+        if (e >= 0 && lane == (e & 63)) want |= 1u << (e >> 6);
+      }
+      if (d == 0.0) want = 0;
+      int n = 0;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const double v = u[j] + (double)bias[j];
-        if (lane + 64 * j < p.n_experts && !(v > upper) && !(v < lower)) want |= 1u << j;
+        const bool is = want >> j & 1;
+        const uint64_t all = __ballot(is);
+        at[j] = is ? n + __builtin_popcountll(all & ((1ull << lane) - 1)) : -1;
+        if (is) list[at[j]] = (uint16_t)(lane + 64 * j);
+        n += __builtin_popcountll(all);
       }
+      if (lane == 0) listed = n;
     }
-    for (int r = 0; r < p.top_k; ++r) {
-      const int e = __builtin_amdgcn_readlane(f.expert, r);
-      if (e >= 0 && lane == (e & 63)) want |= 1u << (e >> 6);
-    }
-    if (d == 0.0) want = 0;
-    int n = 0;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const bool is = want >> j & 1;
-      const uint64_t all = __ballot(is);
-      at[j] = is ? n + __builtin_popcountll(all & ((1ull << lane) - 1)) : -1;
-      if (is) list[at[j]] = (uint16_t)(lane + 64 * j);
-      n += __builtin_popcountll(all);
-    }
-    if (lane == 0) listed = n;
   }
   __syncthreads();
   const int n = __builtin_amdgcn_readfirstlane(listed);
@@ -608,6 +625,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(J <= 4 ? 8 
   }
   __syncthreads();
   if (wave != 0) return;
+  if (unsure == 0) {
+    // the first one is the largest; a softmax is divided by the chosen ones' sum
+    const double v = n ? exact[f.expert >= 0 ? lane : 0] : 0.0, most = __shfl(v, 0);
+    f.value = f.expert < 0 ? 0.0 : p.score == QR_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-v)) : exp(v - most);
+    store_choice(p, t, f);
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < J; ++j)
     if (at[j] >= 0) l[j] = exact[at[j]];
