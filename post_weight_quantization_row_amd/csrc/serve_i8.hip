@@ -167,43 +167,58 @@ struct Channels {
   }
 };
 
-// Stores four neighbouring channels of one token; up: the gate's second sums.
-template <int DST, int EPI>
-__device__ __forceinline__ void store_four(const Product& p, const Epilogue& ep, const Channels<EPI>& c, int tok, int o,
-                                           const i32x4& sum, const i32x4& up, const TokenScale& xd) {
-  const int64_t at = (int64_t)tok * p.y_stride + o, from = (int64_t)tok * ep.residual_stride + o;
+// Four neighbouring channels of some tokens: sums (up: the gate's second ones),
+// token and its scale. A token of -1 is none.
+struct Four {
+  i32x4 sum, up;
+  TokenScale d;
+  int tok;
+};
+
+template <int DST, int EPI, int N>
+__device__ __forceinline__ void store_fours(const Product& p, const Epilogue& ep, const Channels<EPI>& c, int o, const Four (&f)[N]) {
   const bool whole = o + 4 <= p.n_out;
-  float v[4];
+  float v[4 * N];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    v[e] = scaled(sum[e], xd, c.wd[e], c.bias[e]);
-    if (EPI != PLAIN) v[e] = activation(ep.act, v[e]);
-    if (EPI == GATED) v[e] *= scaled(up[e], xd, c.upd[e], c.up_bias[e]);
-  }
-  if (EPI != PLAIN && ep.residual) {
+  for (int t = 0; t < N; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[4 * t + e] = scaled(f[t].sum[e], f[t].d, c.wd[e], c.bias[e]);
+  if (EPI != PLAIN) activate(ep.act, v);
+#pragma unroll
+  for (int t = 0; t < N; ++t) {
+    if (f[t].tok < 0) continue;
+    const int64_t at = (int64_t)f[t].tok * p.y_stride + o, from = (int64_t)f[t].tok * ep.residual_stride + o;
+    float u[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      u[e] = v[4 * t + e];
+      if (EPI == GATED) u[e] *= scaled(f[t].up[e], f[t].d, c.upd[e], c.up_bias[e]);
+    }
+    if (EPI != PLAIN && ep.residual) {
+      if (whole && DST == QR_BF16) {
+        const u16x4_any r = *reinterpret_cast<const u16x4_any*>(reinterpret_cast<const uint16_t*>(ep.residual) + from);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[e] += bf16_value(r[e]);
+      } else if (whole) {
+        const f32x4_any r = *reinterpret_cast<const f32x4_any*>(reinterpret_cast<const float*>(ep.residual) + from);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[e] += r[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (o + e < p.n_out) u[e] += load_one<DST>(ep.residual, from + e);
+      }
+    }
     if (whole && DST == QR_BF16) {
-      const u16x4_any r = *reinterpret_cast<const u16x4_any*>(reinterpret_cast<const uint16_t*>(ep.residual) + from);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += bf16_value(r[e]);
+      *reinterpret_cast<u16x4_any*>(reinterpret_cast<uint16_t*>(p.y) + at) =
+          u16x4_any{bf16_bits(u[0]), bf16_bits(u[1]), bf16_bits(u[2]), bf16_bits(u[3])};
     } else if (whole) {
-      const f32x4_any r = *reinterpret_cast<const f32x4_any*>(reinterpret_cast<const float*>(ep.residual) + from);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += r[e];
+      *reinterpret_cast<f32x4_any*>(reinterpret_cast<float*>(p.y) + at) = f32x4_any{u[0], u[1], u[2], u[3]};
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (o + e < p.n_out) v[e] += load_one<DST>(ep.residual, from + e);
+        if (o + e < p.n_out) store_one<DST>(p.y, at + e, u[e]);
     }
-  }
-  if (whole && DST == QR_BF16) {
-    *reinterpret_cast<u16x4_any*>(reinterpret_cast<uint16_t*>(p.y) + at) =
-        u16x4_any{bf16_bits(v[0]), bf16_bits(v[1]), bf16_bits(v[2]), bf16_bits(v[3])};
-  } else if (whole) {
-    *reinterpret_cast<f32x4_any*>(reinterpret_cast<float*>(p.y) + at) = f32x4_any{v[0], v[1], v[2], v[3]};
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (o + e < p.n_out) store_one<DST>(p.y, at + e, v[e]);
   }
 }
 
@@ -313,7 +328,7 @@ __global__ __launch_bounds__(F_WAVES* WAVE) void k_matmul_i8_few(Product p, Epil
     const int tok = t0 + 16 * wave + li;
     if (tok >= p.n_tok) return;
     if constexpr (EPI == PLAIN) store_plain<DST>(p, tok, o0 + 4 * lk, sum[0], token_scale(p.xd[tok]));
-    else store_four<DST, EPI>(p, ep, Channels<EPI>(p, ep, o0 + 4 * lk), tok, o0 + 4 * lk, sum[0], sum[G - 1], token_scale(p.xd[tok]));
+    else store_fours<DST, EPI, 1>(p, ep, Channels<EPI>(p, ep, o0 + 4 * lk), o0 + 4 * lk, {{sum[0], sum[G - 1], token_scale(p.xd[tok]), tok}});
   }
 }
 
@@ -332,10 +347,13 @@ __global__ __launch_bounds__(F_WAVES* WAVE) void k_matmul_i8_few(Product p, Epil
 // sixteen lanes that take one piece of neighbouring rows meet all banks.
 //
 // 32x32x32 products: with 16x16x64 ones the compiler moved 350 accumulators a
-// step between registers. 8192^3: 1940 to 2130 TOP/s by card (a library product
-// 2270 to 2510); 8192 x 11008 x 4096: 446 to 477 us. With the loads and stores
-// not dealt between the products 8192^3 took 17% longer, with the loads right
-// behind the stores 10%. The small tiles, several to a CU, keep loads early
+// step between registers. 8192^3: 2020 to 2200 TOP/s by card and codes (a library
+// product on the same card 2000 to 2310); 8192 x 11008 x 4096: 380 to 410 us; with
+// a gate 750 to 820, in which the matrix cores are busy for 48% of the clocks (they
+// alone, fed from registers, reach 3050 to 3300 TOP/s). A quarter of the gate's
+// time is the epilogue, during which its CU multiplies nothing. With the loads and
+// stores not dealt between the products 8192^3 took 17% longer, with the loads
+// right behind the stores 10%. The small tiles, several to a CU, keep loads early
 // (11% slower otherwise).
 //
 // KS parts of a workgroup take every KS-th step, each with its own LDS, and
@@ -393,12 +411,24 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(NI * N
   // steps part, part + KS, ... are this part's; one behind the last is not used
   const int all = p.row_bytes / 128, steps = (all + KS - 1) / KS;
   auto at_step = [&](int s) { return (int64_t)(s * KS + part < all ? s * KS + part : all - 1) * 128; };
+  {
+    i32x4 first[NQ];
 #pragma unroll
-  for (int q = 0; q < NQ; ++q) load(q, at_step(0));
+    for (int q = 0; q < NQ; ++q) {
+      load(q, at_step(0));
+      first[q] = raw[q];
+    }
 #pragma unroll
-  for (int q = 0; q < NQ; ++q) store(q, lds[0]);
+    for (int q = 0; q < NQ; ++q) load(q, at_step(1));
 #pragma unroll
-  for (int q = 0; q < NQ; ++q) load(q, at_step(1));
+    for (int q = 0; q < NQ; ++q) *reinterpret_cast<i32x4*>(lds[0] + put + q * 32 * 128) = first[q];
+  }
+  float xd[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int tok = t0 + wt + 32 * j + li;
+    xd[j] = p.xd[tok < p.n_tok ? tok : p.n_tok - 1];
+  }
   __syncthreads();
   read(lds[0], 0, a[0], b[0]);
   for (int s = 0; s < steps; ++s) {
@@ -454,55 +484,46 @@ __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(NI * N
         for (int n = 0; n < NI * NJ; ++n) acc[n / NJ][n % NJ] += sums[(wave * NI * NJ + n) * 64 + lane];
       }
     }
-    if (EPI != PLAIN) __syncthreads();   // the sums have been read
+    __syncthreads();   // the sums have been read
     if (part != 0) return;
-  } else if constexpr (EPI != PLAIN) {
-    __syncthreads();                     // the last tile has been read
-  }
-  if constexpr (EPI == PLAIN) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int tok = t0 + wt + 32 * j + li;
-      if (tok >= p.n_tok) continue;
-      const TokenScale xd = token_scale(p.xd[tok]);
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          const i32x4 sum = {acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]};
-          store_plain<DST>(p, tok, o0 + wo + 32 * i + 2 * e + 4 * lh, sum, xd);
-        }
-    }
   } else {
-    // 32 tokens at a time through the wave's own part of LDS: the epilogue is
-    // then one short loop (unrolled over the accumulators it was too long for the
-    // compiler to keep them in registers), and a lane keeps its four channels
-    constexpr int W = 32 * NI, PITCH = W + 4, FOURS = W / (EPI == GATED ? 8 : 4), TOKENS = 64 / FOURS;
-    static_assert(4 * 32 * PITCH * 4 <= (int)sizeof(all_lds), "the waves' sums fit");
-    int* sums = reinterpret_cast<int*>(all_lds) + wave * (32 * PITCH);
-    const int four = lane % FOURS, piece = four * 4 / PIECE, o = o0 + (wo / 32 + piece) * PIECE + four * 4 % PIECE;
-    const Channels<EPI> channels(p, ep, o < p.n_out ? o : p.n_out - 1);
-    const int* from = sums + (lane / FOURS) * PITCH + 32 * piece + four * 4 % PIECE;
+    __syncthreads();   // the last tile has been read
+  }
+  // 32 tokens at a time through the wave's own part of LDS: the epilogue is then
+  // one short loop (unrolled over the accumulators it was too long for the
+  // compiler to keep them in registers), a lane keeps its four channels, and a
+  // token's are stored side by side. Behind a token's sums lies its scale.
+  constexpr int W = 32 * NI, PITCH = W + 4, FOURS = W / (EPI == GATED ? 8 : 4), TOKENS = 64 / FOURS, AT_ONCE = 2;
+  static_assert(4 * 32 * PITCH * 4 <= (int)sizeof(all_lds), "the waves' sums fit");
+  int* sums = reinterpret_cast<int*>(all_lds) + wave * (32 * PITCH);
+  const int four = lane % FOURS, piece = four * 4 / PIECE, o = o0 + (wo / 32 + piece) * PIECE + four * 4 % PIECE;
+  const Channels<EPI> channels(p, ep, o < p.n_out ? o : p.n_out - 1);
+  const int* from = sums + (lane / FOURS) * PITCH + 32 * piece + four * 4 % PIECE;
+  const int* scales = sums + (lane / FOURS) * PITCH + W;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int first = t0 + wt + 32 * j;
-      if (first >= p.n_tok) break;
+  for (int j = 0; j < NJ; ++j) {
+    const int first = t0 + wt + 32 * j;
+    if (first >= p.n_tok) break;
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; e += 4)
-          *reinterpret_cast<i32x4*>(sums + li * PITCH + 32 * i + 2 * e + 4 * lh) =
-              i32x4{acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]};
-      wave_sync();
-#pragma unroll 2
-      for (int t = 0; t < 32; t += TOKENS) {
-        const int tok = first + t + lane / FOURS;
-        if (tok < p.n_tok && o < p.n_out)
-          store_four<DST, EPI>(p, ep, channels, tok, o, *reinterpret_cast<const i32x4*>(from + t * PITCH),
-                               *reinterpret_cast<const i32x4*>(from + t * PITCH + (EPI == GATED ? 16 : 0)), token_scale(p.xd[tok]));
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<i32x4*>(sums + li * PITCH + 32 * i + 2 * e + 4 * lh) =
+            i32x4{acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]};
+    if (lh == 0) *reinterpret_cast<TokenScale*>(sums + li * PITCH + W) = token_scale(xd[j]);
+    wave_sync();
+#pragma unroll 1
+    for (int t = 0; t < 32; t += AT_ONCE * TOKENS) {
+      Four f[AT_ONCE];
+#pragma unroll
+      for (int u = 0; u < AT_ONCE; ++u) {
+        const int r = t + u * TOKENS, tok = first + r + lane / FOURS;
+        f[u] = {*reinterpret_cast<const i32x4*>(from + r * PITCH), *reinterpret_cast<const i32x4*>(from + r * PITCH + (EPI == GATED ? 16 : 0)),
+                *reinterpret_cast<const TokenScale*>(scales + r * PITCH), tok < p.n_tok && o < p.n_out ? tok : -1};
       }
-      wave_sync();
+      store_fours<DST, EPI, AT_ONCE>(p, ep, channels, o, f);
     }
+    wave_sync();
   }
 }
 
@@ -536,16 +557,19 @@ int64_t tiles_of(const Product& p, int out, int tok) {
 // byte then serves more products), and below that the sum split inside a
 // workgroup, so that a CU has 8 or 16 waves at work. Measured, us (channels x
 // values 4096 x 4096 unless said), the choice first:
-//   16 tokens            k_few 1: 11      64x64 in four parts: 14
-//   24 x 11008 channels  64x64 in four: 15     k_few 2: 23
-//   48 tokens            k_few 4: 12           64x64 in four: 14
-//   64 x 11008           64x64 in four: 17     k_few 4: 34
-//   128 x 11008          64x128 in two: 21     64x64 in four: 29
-//   512                  64x128 in two: 20     64x64 in four: 27
-//   1024                 128x128 in two: 29    64x128 in two: 37
-//   1500                 128x128: 44           128x128 in two: 53
-//   4096                 256x256: 82           128x128: 96
-//   700 x 11008 (129 tiles of 256x256)         128x128: 70    256x256: 74
+//   16 tokens            k_few 1: 6.5     64x64 in four parts: 11
+//   24 x 11008 channels  64x64 in four: 13     k_few 2: 18
+//   48 tokens            k_few 4: 11           64x64 in four: 11
+//   64 x 11008           64x64 in four: 13     k_few 4: 31
+//   128 x 11008          64x128 in two: 17     64x64 in four: 23
+//   512                  64x128 in two: 18     64x64 in four: 24
+//   1024                 128x128 in two: 28    64x128 in two: 34
+//   1500                 128x128: 43           128x128 in two: 48
+//   2000 (128 tiles of 256x256)                128x128: 50    256x256: 57
+//   700 x 11008 (129)    256x256: 53           128x128: 62
+//   4096 (256)           256x256: 76           128x128: 93
+//   4800 (304)           128x128: 106          256x256: 119
+//   5800 (368)           256x256: 122          128x128: 129
 template <int DST, int EPI>
 int launch_product(const Product& p, const Epilogue& ep, hipStream_t s) {
   constexpr int64_t CUS = 256;
@@ -558,9 +582,10 @@ int launch_product(const Product& p, const Epilogue& ep, hipStream_t s) {
   if (t64 <= CUS) return launch_tile<DST, 1, 1, 4, EPI>(p, ep, s);
   if (tiles_of<EPI>(p, 64, 128) <= CUS) return launch_tile<DST, 1, 2, 2, EPI>(p, ep, s);
   if (tiles_of<EPI>(p, 128, 128) <= CUS) return launch_tile<DST, 2, 2, 2, EPI>(p, ep, s);
-  // 256x256 where the last round of workgroups does not leave too many idle
+  // 256x256 where the last round of workgroups does not leave too many idle: a
+  // single round may be half empty, since 128x128 needs a second one there
   const int64_t t256 = tiles_of<EPI>(p, 256, 256), rounds = (t256 + CUS - 1) / CUS;
-  if (t256 * 100 >= rounds * CUS * 65) return launch_tile<DST, 4, 4, 1, EPI>(p, ep, s);
+  if (t256 * 100 > rounds * CUS * (rounds == 1 ? 50 : 65)) return launch_tile<DST, 4, 4, 1, EPI>(p, ep, s);
   return launch_tile<DST, 2, 2, 1, EPI>(p, ep, s);
 }
 

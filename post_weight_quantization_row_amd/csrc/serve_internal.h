@@ -207,6 +207,23 @@ __device__ __forceinline__ T activation(int act, T x) {
   }
 }
 
+// The same of N values with one branch: their steps then run side by side
+// (8192 tokens, 11008 x 4096 gated: one by one 862 us, four 839, eight 797 to 837).
+template <int N>
+__device__ __forceinline__ void activate(int act, float (&v)[N]) {
+  const auto each = [&](int kind) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = activation(kind, v[i]);
+  };
+  switch (act) {
+    case QR_ACT_RELU: each(QR_ACT_RELU); break;
+    case QR_ACT_SILU: each(QR_ACT_SILU); break;
+    case QR_ACT_GELU: each(QR_ACT_GELU); break;
+    case QR_ACT_GELU_TANH: each(QR_ACT_GELU_TANH); break;
+    default: break;
+  }
+}
+
 // Whether any of n rows of `row` bytes, a_step bytes apart, shares memory with
 // one of the rows at b: parts of one buffer lie between each other without
 // meeting.
