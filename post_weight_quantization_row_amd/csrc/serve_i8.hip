@@ -350,8 +350,10 @@ __global__ __launch_bounds__(F_WAVES* WAVE) void k_matmul_i8_few(Product p, Epil
 // step between registers. 8192^3: 2020 to 2200 TOP/s by card and codes (a library
 // product on the same card 2000 to 2310); 8192 x 11008 x 4096: 380 to 410 us; with
 // a gate 750 to 820, in which the matrix cores are busy for 48% of the clocks (they
-// alone, fed from registers, reach 3050 to 3300 TOP/s). A quarter of the gate's
-// time is the epilogue, during which its CU multiplies nothing. With the loads and
+// alone, fed from registers, reach 3050 to 3300 TOP/s). The loop itself passes at
+// 2700 (sums of 512 and of 4096 values compared); 30% of the gate's time is the
+// epilogue, during which its CU multiplies nothing. Workgroups that go on to a next
+// tile, its first steps asked for before the epilogue: no faster. With the loads and
 // stores not dealt between the products 8192^3 took 17% longer, with the loads
 // right behind the stores 10%. The small tiles, several to a CU, keep loads early
 // (11% slower otherwise).
