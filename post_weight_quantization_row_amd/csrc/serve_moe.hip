@@ -636,7 +636,9 @@ __device__ __forceinline__ void exact_logits(const Route& p, int64_t t, const ui
 // come before it; the choice is then made again, of the scores, which is the one
 // that exact logits throughout would give. Near is also what the 64 bits of a score
 // (+ bias) may not tell apart: that part of the margin is seen only where sigmoids
-// near one, scores of no size or a huge bias round the differences away.
+// near one, scores of no size or a huge bias round the differences away. Of two
+// logits found more than 2 d apart that both give scores of zero (below -709 of
+// themselves, or of the largest), the lower one is found below -690.
 //
 // 2048 tokens, 8 of 256 experts: 41 us, some 30 of them for nine exact logits a
 // token. Vector instructions are issued in 56% of the time, four for each product
@@ -672,7 +674,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(J <= 4 ? 8 
     const double u0 = of_key(f.key), u1 = of_key(f.next);
     double margin;
     if (p.bias) margin = 0.52 * d + 0x1p-50 * (1.0 + __builtin_fabs(u0) + __builtin_fabs(u1));
-    else if (p.score == QR_SCORE_SIGMOID) margin = 2.0 * d + 0x1p-49 * (1.0 + exp(u0));
+    else if (p.score == QR_SCORE_SIGMOID) margin = u1 < -690.0 ? __builtin_inf() : 2.0 * d + 0x1p-49 * (1.0 + exp(u0));
     else margin = u1 - of_key(__shfl(f.key, 0)) < -690.0 ? __builtin_inf() : 2.0 * d + 0x1p-48;
     const uint64_t found = __ballot(f.expert >= 0);
     unsure = __ballot(f.expert >= 0 && f.next != 0 && !(u0 - u1 > margin));
