@@ -567,7 +567,9 @@ __global__ __launch_bounds__(512) void k_route_rough(Route p, int expert_tiles, 
 // How far a token's rough logits may be off: fp32 sums of ROUGH_SUM exact
 // products, each addition off by a last place of the products' magnitudes added
 // up (twice what rounding does), and those at most the rows' lengths multiplied.
-// Zero for a row of zeros, whose logits are exact. (By one wave.)
+// Zero for a row of zeros, whose logits are exact, unless a weight may be no
+// number: the choice that stands by itself then takes zeros for its logits. (By
+// one wave.)
 __device__ __forceinline__ double rough_error(const Route& p, int64_t t) {
   const int lane = threadIdx.x & 63;
   float x = 0.0f, w = 0.0f;
@@ -582,7 +584,7 @@ __device__ __forceinline__ double rough_error(const Route& p, int64_t t) {
     uint32_t any = 0;
     const uint16_t* row = reinterpret_cast<const uint16_t*>(p.x) + t * p.x_stride;
     for (int at = lane; at < p.n_in; at += WAVE) any |= row[at] & 0x7fffu;
-    return __ballot(any != 0) ? __builtin_inf() : 0.0;
+    return __ballot(any != 0) || !(most < __builtin_inf()) ? __builtin_inf() : 0.0;
   }
   if (most < 0x1p-80) return __builtin_inf();
   return ROUGH_SUM * 0x1p-23 * 1.02 * __builtin_sqrt((double)x) * __builtin_sqrt(most);

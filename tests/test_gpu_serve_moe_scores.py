@@ -26,3 +26,20 @@ def test_sigmoids_that_vanish(sv, first):  # noqa: F811
             check_route(got, x, w, 8, "sigmoid", None, renorm, 1.0)
             if first == -100.0:
                 assert (got[0].cpu().numpy()[:, 3 * some:] == np.arange(8 - 3 * some)).all()
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("top_k", [1, 8])
+def test_zeros_against_a_row_of_no_numbers(sv, top_k, value):  # noqa: F811
+    """One expert is left to choose from, and zero times its infinite weight is no
+    number: a token of zeros has that weight too."""
+    say(f"zeros and {value}, top {top_k}")
+    t, e, k = 3000, 240, 1600
+    x, w, b = rows(t, e, k, 12)
+    x[::2] = 0
+    w[17:19, 5] = value
+    b[:] = -np.inf
+    b[17] = 0.25
+    got = sv.qr_moe_route(x.cuda(), w.cuda(), top_k, score="sigmoid", bias=dev(b))
+    check_route(got, x, w, top_k, "sigmoid", b, True, 1.0)
+    assert (got[0][:, 0] == 17).all() and (got[0][:, 1:] == -1).all() and torch.isnan(got[1][::2, 0]).all()
