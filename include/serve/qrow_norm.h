@@ -40,7 +40,8 @@ extern "C" {
  * sum may be x or residual, and y may be x, residual or neither (the same
  * pointer and stride: in place); apart from that no output may overlap an input
  * or another output (refused).
- * Limits: 1 <= n <= QR_I8_MAX_IN; n_rows < 2^24. n_rows == 0 is a no-op.
+ * Limits: 1 <= n <= QR_I8_MAX_IN; n_rows < 2^24, and < 2^22 where n > 8192.
+ * n_rows == 0 is a no-op.
  */
 int qr_norm_rows_i8(int src, const void *x, int64_t x_stride,
                     const void *residual, int64_t residual_stride, int wtype,

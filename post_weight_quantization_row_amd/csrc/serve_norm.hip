@@ -201,9 +201,10 @@ __global__ __launch_bounds__(WAVES > 4 ? WAVES * WAVE : 256) __attribute__((amdg
 
 template <int SRC, int WAVES, int KEEP>
 int launch(const Norm& p, hipStream_t s) {
-  const uint32_t rows = WAVES > 4 ? 1 : 4 / WAVES;
-  hipLaunchKernelGGL((k_norm_rows_i8<SRC, WAVES, KEEP>), dim3(((uint32_t)p.n_rows + rows - 1) / rows),
-                     dim3(WAVES > 4 ? WAVES * WAVE : 256), 0, s, p);
+  const uint32_t rows = WAVES > 4 ? 1 : 4 / WAVES, threads = WAVES > 4 ? WAVES * WAVE : 256;
+  const uint32_t groups = ((uint32_t)p.n_rows + rows - 1) / rows;
+  if (groups > UINT32_MAX / threads) return qr_fail(QR_EOVERFLOW, "n_rows=%d is more than one launch holds", p.n_rows);
+  hipLaunchKernelGGL((k_norm_rows_i8<SRC, WAVES, KEEP>), dim3(groups), dim3(threads), 0, s, p);
   return qr_check_launch("k_norm_rows_i8");
 }
 
