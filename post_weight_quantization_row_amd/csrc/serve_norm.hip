@@ -225,7 +225,7 @@ int launch_norm(const Norm& p, hipStream_t s) {
 struct Rows {
   const char* name;
   const void* p;
-  int64_t stride;   // bytes
+  int64_t stride;   // elements; bytes once it is known to be no more than that holds
 };
 
 }  // namespace
@@ -244,16 +244,17 @@ extern "C" int qr_norm_rows_i8(int src, const void* x, int64_t x_stride, const v
   if (!residual != !sum && n_rows > 0) return qr_fail(QR_EINVAL_PTR, "residual and sum must both be given or both be NULL");
   const int64_t esize = src == QR_BF16 ? 2 : 4;
   // inputs, then the outputs that may be one of them
-  const Rows rows[4] = {{"x", x, x_stride * esize}, {"residual", residual, residual_stride * esize},
-                        {"sum", sum, sum_stride * esize}, {"y", y, y_stride * esize}};
-  const int64_t strides[4] = {x_stride, residual_stride, sum_stride, y_stride};
+  Rows rows[4] = {{"x", x, x_stride}, {"residual", residual, residual_stride}, {"sum", sum, sum_stride}, {"y", y, y_stride}};
   for (int i = 0; i < 4; ++i) {
     if (i > 0 && !rows[i].p) continue;
-    if (strides[i] < n) return qr_fail(QR_EINVAL_SHAPE, "%s_stride=%lld is below n", rows[i].name, (long long)strides[i]);
+    if (rows[i].stride < n) return qr_fail(QR_EINVAL_SHAPE, "%s_stride=%lld is below n", rows[i].name, (long long)rows[i].stride);
   }
   if (n_rows == 0) return QR_OK;
-  for (int i = 0; i < 4; ++i)
-    if (rows[i].p && strides[i] > INT64_MAX / 4 / n_rows) return qr_fail(QR_EOVERFLOW, "%s_stride is too large", rows[i].name);
+  for (Rows& r : rows) {
+    if (!r.p) continue;
+    if (r.stride > INT64_MAX / 4 / n_rows) return qr_fail(QR_EOVERFLOW, "%s_stride is too large", r.name);
+    r.stride *= esize;
+  }
   if (n_rows > UINT32_MAX / 256) return qr_fail(QR_EOVERFLOW, "n_rows=%lld is more than one launch holds", (long long)n_rows);
   if (!x || !codes || !scales) return qr_fail(QR_EINVAL_PTR, "x, codes and scales must be non-NULL");
   for (int i = 0; i < 4; ++i)
