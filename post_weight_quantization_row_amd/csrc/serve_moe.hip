@@ -1285,9 +1285,11 @@ size_t route_bytes(const RoutePlan& r, int64_t n_experts, int64_t n_tok) {
 
 template <int J>
 int launch_choose(const Route& p, bool rough, hipStream_t s) {
-  if (rough) {
-    hipLaunchKernelGGL((k_route_settle<J>), dim3((uint32_t)p.n_tok), dim3(256), 0, s, p);
-    return qr_check_launch("k_route_settle");
+  if constexpr (J > 1) {         // (rough logits are those of more than 64 experts)
+    if (rough) {
+      hipLaunchKernelGGL((k_route_settle<J>), dim3((uint32_t)p.n_tok), dim3(256), 0, s, p);
+      return qr_check_launch("k_route_settle");
+    }
   }
   hipLaunchKernelGGL((k_route_choose<J>), dim3((uint32_t)((p.n_tok + 3) / 4)), dim3(256), 0, s, p);
   return qr_check_launch("k_route_choose");
@@ -1305,14 +1307,15 @@ int launch_route(const Route& p, const RoutePlan& r, hipStream_t s) {
     return qr_check_launch("k_route_small");
   }
   const dim3 grid((uint32_t)(r.expert_tiles * (int64_t)r.token_tiles * r.splits)), block(R_WAVES * WAVE);
-  if (r.rough) hipLaunchKernelGGL(k_route_rough, grid, dim3(512), 0, s, p, r.expert_tiles, r.token_tiles);
+  const bool rough = SRC == QR_BF16 && WSRC == QR_BF16 && r.rough;
+  if (rough) hipLaunchKernelGGL(k_route_rough, grid, dim3(512), 0, s, p, r.expert_tiles, r.token_tiles);
   else if (r.wide) hipLaunchKernelGGL((k_route_logits<SRC, WSRC, 2, 2>), grid, block, 0, s, p, r.expert_tiles, r.token_tiles);
   else hipLaunchKernelGGL((k_route_logits<SRC, WSRC, 1, 1>), grid, block, 0, s, p, r.expert_tiles, r.token_tiles);
-  const int rc = qr_check_launch(r.rough ? "k_route_rough" : "k_route_logits");
+  const int rc = qr_check_launch(rough ? "k_route_rough" : "k_route_logits");
   if (rc != QR_OK) return rc;
-  if (p.n_experts <= 64) return launch_choose<1>(p, r.rough, s);
-  if (p.n_experts <= 256) return launch_choose<4>(p, r.rough, s);
-  return p.n_experts <= 512 ? launch_choose<8>(p, r.rough, s) : launch_choose<16>(p, r.rough, s);
+  if (p.n_experts <= 64) return launch_choose<1>(p, rough, s);
+  if (p.n_experts <= 256) return launch_choose<4>(p, rough, s);
+  return p.n_experts <= 512 ? launch_choose<8>(p, rough, s) : launch_choose<16>(p, rough, s);
 }
 
 bool route_shapes(int64_t n_experts, int64_t n_tok, int64_t n_in) {
