@@ -111,11 +111,14 @@ typedef struct {
  *            place); otherwise the two must not overlap (refused). y must not
  *            overlap the other operands either (not looked at).
  * Every step is in fp32: the two products each as in qr_matmul_i8; the
- * activation, within 8 * 2^-24 of |p(w)| (and 2^-110 where exp overflows) for
- * the fp32 p(w) it is given; the gate's product and the residual's addition
- * rounded once each; then the rounding to dst.
- * Limits: those of qr_matmul_i8, with up those for 2 * n_out; act one of the
- * above.
+ * activation, within 8 * 2^-24 of |p| (and 2^-110 where exp overflows) for the
+ * fp32 p = p(w) it is given, and where its result a is 2^-110 or more in
+ * magnitude within 8 * 2^-24 (SILU), (36 + 2 p^2) * 2^-24 (GELU) or
+ * (8 + 5 t) * 2^-24 (GELU_TANH, t = 2 sqrt(2 / pi) |p + 0.044715 p^3|) of |a|;
+ * the gate's product and the residual's addition rounded once each; then the
+ * rounding to dst.
+ * Limits: those of qr_matmul_i8, with up and more than 16 tokens those for
+ * 2 * n_out; act one of the above.
  */
 int qr_matmul_i8_ex(const int8_t *w, const float *wd, const int8_t *x,
                     const float *xd, const float *bias,
