@@ -115,9 +115,12 @@ size_t qr_moe_i8_workspace_bytes(const qr_moe *m, int64_t n_tok,
  * and n_mid fix together with the number of distinct experts met, a token's
  * experts in the order of their slots.
  * The operator is made for few tokens, whose time is that of the weights' way
- * through the chip: once for up to 64 tokens of an expert through gate and up,
- * and for up to 16 (32 where there are many and n_mid is 4096 or more) through
- * down. More are right, up to the limit, and read the weights again.
+ * through the chip. Gate and up pass once for up to 64 tokens of an expert. Down
+ * passes once for up to 512 pairs of the call (whole tokens: 512 / top_k of them)
+ * and up to 16 of an expert (32 where there are many and n_mid is 4096 or more).
+ * More are right, up to the limit, and read the weights again: 128 tokens of 8
+ * experts each read down twice, 1024 of them up to 16 times, however few of an
+ * expert's pairs are among them.
  * Limits: 1 <= top_k <= QR_MOE_MAX_TOP_K, n_tok * top_k <= QR_MOE_MAX_PAIRS,
  * and those of qr_moe. n_tok == 0 is a no-op.
  */

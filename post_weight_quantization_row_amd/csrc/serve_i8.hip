@@ -246,8 +246,8 @@ __device__ __forceinline__ void store_plain(const Product& p, int tok, int o, co
 // its waves in chunks of 128 values, every operand loaded straight into the
 // registers that the matrix instruction reads (row li, 16 bytes at 16 lk; whole
 // lines of the weights, turned in registers). The weights pass the chip once:
-// bound by their bytes (16 tokens, 11008 x 4096:
-// 14 us, 3.3 TB/s; one token, 4096 x 4096: 5.4 us). From some 24 tokens on
+// bound by their bytes (16 tokens, 11008 x 4096: 14.2 to 15.0 us by card, 3.0 to 3.2
+// TB/s; one token, 4096 x 4096: 5.4 us). From some 24 tokens on
 // every workgroup's reading of the tokens costs more, and tiles in LDS win.
 constexpr int F_WAVES = 8;
 // Chunks of a wave whose loads are in flight together: with a gate, which has

@@ -646,7 +646,9 @@ __device__ __forceinline__ void exact_logits(const Route& p, int64_t t, const ui
 // token. Vector instructions are issued in 56% of the time, four for each product
 // of a sum (conversions to 64 bits most of them) and half as many again for the
 // choice; a sum's halves or quarters dealt to the waves: no faster. 64 registers,
-// for eight workgroups to a CU, which hide each other's waits (100: 55 us).
+// for eight workgroups to a CU, which hide each other's waits (100: 55 us); 9 more,
+// of the choice's state, lie in scratch memory during the sums (13 where there are
+// 512 experts, 23 with 1024).
 template <int J>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(J <= 4 ? 8 : J == 8 ? 4 : 2))) void k_route_settle(Route p) {
   __shared__ double exact[64 * J];
@@ -1171,7 +1173,10 @@ __device__ __forceinline__ int sort_pairs(const Moe& m, int first, int n, Sorted
 // of 2048 x 7168 for one token 24.5 us, 4.8 TB/s (merely read: 21 us), 113 for 64
 // tokens 320 us, 5.2 TB/s, 8 of 11008 x 4096 for 23 tokens 77 us (merely read: 69
 // to 75). Two workgroups to a CU, within 128 registers; loads that run on into
-// the wave's next expert spilled 40 of them (555 us).
+// the wave's next expert spilled 40 of them (555 us). Every run of tokens reads the
+// rows of the experts that it meets for itself: 64, 128, 256 and 1024 tokens, 8 of
+// 256 experts (226 to 256 met) 586, 1158, 1973 and 7874 us, 3.3, 6.7, 13 and 52 GB
+// from memory.
 template <int DST, int MOST, bool FEW>
 __global__ __launch_bounds__(M_WAVES* WAVE) __attribute__((amdgpu_waves_per_eu(MOST == 1 ? 4 : 2))) void k_moe_down(Moe m, int tokens_each) {
   constexpr int PAIRS = FEW ? 64 : D_SLOTS;

@@ -105,11 +105,14 @@ __device__ __forceinline__ uint32_t largest(uint32_t top, const float (&v)[8]) {
 // registers from its sum to its codes; what is longer is read again, twice. With
 // eight waves and more, which are for few rows, the weights are asked for
 // together with the row; else after its sum (16 registers less: a fifth wave per
-// SIMD).
+// SIMD, though 12 values of a bf16 row lie in scratch memory then, 14 with KEEP 4;
+// fp32 rows fit).
 //
 // Bound by one pass over memory: 8192 x 4096 bf16 with a residual 52 us, 4.5 TB/s
 // (a copy passes at 4.6); one row 3.5 us, the time of its dependent steps. The
-// 64-bit arithmetic costs nothing there (fp32 throughout: no faster).
+// 64-bit arithmetic costs nothing there (fp32 throughout: no faster). 8192 x 7168
+// 135 us, 3.0 TB/s: four waves a SIMD, and more bytes than the Infinity Cache holds
+// (8192 x 4096 out of it, the same rows again and again: 40 us).
 template <int SRC, int WAVES, int KEEP>
 __global__ __launch_bounds__(WAVES > 4 ? WAVES * WAVE : 256) __attribute__((amdgpu_waves_per_eu(KEEP == 2 && WAVES == 4 ? 5 : 4))) void k_norm_rows_i8(Norm p) {
   constexpr int LANES = WAVES * WAVE, ROWS = WAVES > 4 ? 1 : 4 / WAVES;
