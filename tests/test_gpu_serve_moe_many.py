@@ -13,6 +13,15 @@ BF16 = torch.bfloat16
 KINDS = [("softmax", False), ("sigmoid", True), ("sigmoid", False)]
 
 
+def equal_rows(x, w):
+    """x and w of the same logits for check_route, with one sum for rows of w that
+    are equal: a library's product may round columns at the end of a block
+    otherwise, and no two of them are equal in the oracle then."""
+    some, index = np.unique(w.double().numpy(), axis=0, return_inverse=True)
+    logits = x.double().numpy() @ some.T
+    return torch.from_numpy(logits[:, index.ravel()]), torch.eye(w.shape[0], dtype=torch.float64)
+
+
 def off(bias, on, seed):
     """A bias that leaves `on` of the experts, the first and the last among them."""
     keep = np.concatenate([[0, len(bias) - 1], 1 + np.random.default_rng(seed).permutation(len(bias) - 2)[:on - 2]])
@@ -30,7 +39,8 @@ def test_ties(sv, t, e, top_k):  # noqa: F811
         b = np.repeat(b[:37], -(-e // 37))[:e]
         for score, bias in KINDS + [("softmax", True)]:
             bias = b if bias else None
-            check_route(sv.qr_moe_route(x.cuda(), w.cuda(), top_k, score=score, bias=dev(bias)), x, w, top_k, score, bias, True, 1.0)
+            check_route(sv.qr_moe_route(x.cuda(), w.cuda(), top_k, score=score, bias=dev(bias)), *equal_rows(x, w), top_k, score,
+                        bias, True, 1.0)
         zero = torch.zeros_like(x).cuda()
         ids = sv.qr_moe_route(zero, w.cuda(), top_k)[0]
         assert (ids.cpu() == torch.arange(top_k)).all()
@@ -66,7 +76,8 @@ def test_ties_of_many_tokens(sv, t, e, k, top_k):  # noqa: F811
     b = np.repeat(b[:37], -(-e // 37))[:e]
     for score, bias in KINDS:
         bias = b if bias else None
-        check_route(sv.qr_moe_route(x.cuda(), w.cuda(), top_k, score=score, bias=dev(bias)), x, w, top_k, score, bias, True, 1.0)
+        check_route(sv.qr_moe_route(x.cuda(), w.cuda(), top_k, score=score, bias=dev(bias)), *equal_rows(x, w), top_k, score, bias,
+                    True, 1.0)
 
 
 @pytest.mark.parametrize("t,e,k,top_k", MANY)
